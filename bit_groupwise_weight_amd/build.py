@@ -43,7 +43,9 @@ def _units():
     units = [("lowbit_api.cpp", "lowbit_api.o", []),
              ("quant_pack.hip", "quant_pack.o", ["-ffp-contract=off"]),
              ("device_scratch.hip", "device_scratch.o", []),
-             ("act_quant.hip", "act_quant.o", ["-ffp-contract=off"])]
+             ("act_quant.hip", "act_quant.o", ["-ffp-contract=off"]),
+             ("norm_q8.hip", "norm_q8.o", ["-ffp-contract=off"]),
+             ("linear_f8.hip", "linear_f8.o", ["-mllvm", "-amdgpu-mfma-vgpr-form=1"])]
     for b in range(1, 8):
         units.append(("qmm_a8.hip", f"qmm_a8_b{b}.o",
                       [f"-DLOWBIT_BITS={b}", "-mllvm", "-amdgpu-mfma-vgpr-form=1"]))

@@ -186,6 +186,58 @@ hipError_t launch_qmm_a8_b5(const A8Params&, int mtt, int nt, int sz, hipStream_
 hipError_t launch_qmm_a8_b6(const A8Params&, int mtt, int nt, int sz, hipStream_t);
 hipError_t launch_qmm_a8_b7(const A8Params&, int mtt, int nt, int sz, hipStream_t);
 
+// ------------------------------------------------------ the 8-bit path --
+// What a norm writes beside h and y (the values of lowbit_q8_format).
+enum Q8Format : int { Q8_NONE = 0, Q8_I8 = 1, Q8_F8 = 2 };
+struct NormQ8Params {
+  const void* x;          // M x K act, 16-byte aligned
+  const void* residual;   // M x K act, or nullptr (then sum is nullptr too)
+  const void* weight;     // K act, or nullptr (ones)
+  void* sum;              // M x K act: x + residual (may be x or residual itself)
+  void* y;                // M x K act: the normalized rows, or nullptr
+  void* q;                // M x K codes (int8 or e4m3), or nullptr (Q8_NONE)
+  float* qscale;          // M (int8) or M x ceil(K / 128) (e4m3)
+  float eps;
+  int64_t M;
+  int K;                  // K % 16 == 0
+};
+hipError_t launch_norm_q8(const NormQ8Params&, int act, int fmt, hipStream_t);
+
+struct ActQuantF8Params {
+  const void* x;          // M x K act, 16-byte aligned
+  uint8_t* xq;            // M x K e4m3 codes, 16-byte aligned
+  float* xscale;          // M x ceil(K / 128)
+  int64_t M;
+  int K;                  // K % 16 == 0
+};
+hipError_t launch_act_quant_f8(const ActQuantF8Params&, int act, hipStream_t);
+
+struct WeightQuantF8Params {
+  const void* w;          // E x N x K act, 16-byte aligned
+  uint8_t* wq;            // E x N x K e4m3 codes, 16-byte aligned
+  float* wscale;          // E x ceil(N / 128) x ceil(K / 128)
+  int64_t E;
+  int N, K;               // K % 16 == 0
+};
+hipError_t launch_weight_quant_f8(const WeightQuantF8Params&, int act, hipStream_t);
+
+// Block-scaled e4m3 product, dense or grouped by expert.
+struct LinearF8Params {
+  const uint8_t* xq;      // M x K e4m3 codes, 16-byte aligned
+  const float* xs;        // M x kb
+  const int32_t* rows;    // T source rows of xq, or nullptr (row t reads row t)
+  const int32_t* offsets; // E + 1 row bounds of the experts, or nullptr (dense)
+  const uint8_t* wq;      // E x N x K e4m3 codes, 16-byte aligned
+  const float* ws;        // E x nb x kb
+  const void* bias;       // E x N, out type, or nullptr
+  void* y;                // T x N, out type
+  int64_t M, T;           // rows of xq, rows of y (equal without `rows`)
+  int N, K, E;            // K % 16 == 0
+  int kb, nb;             // ceil(K / 128), ceil(N / 128)
+  int tiles_n;            // column tiles
+};
+hipError_t launch_linear_f8(const LinearF8Params&, int out, hipStream_t);
+
 // ------------------------------------------------- library-owned scratch --
 // Size of the device array behind lowbit_linear_noalloc (per device).  The
 // largest K-split schedule of the MFMA path writes one fp32 partial per

@@ -546,6 +546,64 @@ void a8_tiles(int64_t M, int64_t N, int* mtt_out, int* nt_out) {
   *nt_out = nt;
 }
 
+// Limits of the 8-bit path: row lengths whose block counts and lane offsets
+// fit 32 bits, and launches of fewer than 2^32 threads (checked per call).
+constexpr int64_t kQ8MaxK = int64_t(1) << 23;
+constexpr int64_t kNormMaxM = int64_t(1) << 23;
+constexpr int64_t kF8MaxExperts = int64_t(1) << 16;
+int64_t f8_blocks(int64_t n) { return (n + 127) / 128; }
+
+lowbit_status check_q8_row(int64_t K, int unit) {
+  if (K <= 0 || K > kQ8MaxK || K % unit != 0)
+    return fail(LOWBIT_ERR_INVALID_ARG, "K=%lld must be a positive multiple of %d (at most 2^23)",
+                (long long)K, unit);
+  return LOWBIT_OK;
+}
+
+// Arguments of a block-scaled e4m3 product (shared by the dense and the
+// grouped call; offsets == nullptr with E == 0 is the dense one).
+lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_t* rows,
+                            const int32_t* offsets, const uint8_t* wq, const float* wscale,
+                            const void* bias, void* y, lowbit_dtype dtype, int64_t M, int64_t T, int64_t E,
+                            int64_t N, int64_t K, void* stream) {
+  lowbit_status st = check_q8_row(K, 16);
+  if (st != LOWBIT_OK) return st;
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  if (N <= 0 || N > kMaxDim) return fail(LOWBIT_ERR_INVALID_ARG, "N=%lld must be in 1..2^30", (long long)N);
+  if (M < 0 || M > kMaxDim || T < 0 || T > kMaxDim)
+    return fail(LOWBIT_ERR_INVALID_ARG, "rows M=%lld, T=%lld must be in 0..2^30", (long long)M, (long long)T);
+  if (!wq || !wscale) return fail(LOWBIT_ERR_INVALID_ARG, "NULL weight pointer");
+  if (T == 0) return LOWBIT_OK;
+  if (M == 0) return fail(LOWBIT_ERR_INVALID_ARG, "M=0 rows of xq for T=%lld rows of y", (long long)T);
+  if (!xq || !xscale || !y) return fail(LOWBIT_ERR_INVALID_ARG, "NULL xq, xscale or y");
+  if (!aligned(xq, 16) || !aligned(wq, 16))
+    return fail(LOWBIT_ERR_MISALIGNED, "xq and wq must be 16-byte aligned");
+  const size_t e = dtype_bytes(dtype);
+  if (!aligned(xscale, 4) || !aligned(wscale, 4) || !aligned(y, e) || (bias && !aligned(bias, e)) ||
+      (rows && !aligned(rows, 4)) || (offsets && !aligned(offsets, 4)))
+    return fail(LOWBIT_ERR_MISALIGNED,
+                "scales, rows, offsets, bias and y must be aligned to their element size");
+  lowbit::LinearF8Params p{};
+  p.xq = xq;
+  p.xs = xscale;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.wq = wq;
+  p.ws = wscale;
+  p.bias = bias;
+  p.y = y;
+  p.M = M;
+  p.T = T;
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.E = static_cast<int>(E);
+  p.kb = static_cast<int>(f8_blocks(K));
+  p.nb = static_cast<int>(f8_blocks(N));
+  const hipError_t he = lowbit::launch_linear_f8(p, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (he != hipSuccess) return hip_fail(he, "linear_f8 launch");
+  return LOWBIT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -781,6 +839,101 @@ lowbit_status lowbit_linear_a8(const int8_t* xq, const float* ascale, const uint
   const hipError_t he = kA8[bits](p, mtt, nt, act_kind(dtype), static_cast<hipStream_t>(stream));
   if (he != hipSuccess) return hip_fail(he, "qmm_a8 launch");
   return LOWBIT_OK;
+}
+
+lowbit_status lowbit_add_rmsnorm_q8(const void* x, const void* residual, const void* weight, float eps,
+                                    lowbit_dtype dtype, int64_t M, int64_t K, lowbit_q8_format format,
+                                    void* q, float* qscale, void* sum, void* y, void* stream) {
+  g_last_error.clear();
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  if (format != LOWBIT_Q8_NONE && format != LOWBIT_Q8_I8 && format != LOWBIT_Q8_F8)
+    return fail(LOWBIT_ERR_UNSUPPORTED, "format=%d", (int)format);
+  const lowbit_status st = check_q8_row(K, format == LOWBIT_Q8_I8 ? 32 : 16);
+  if (st != LOWBIT_OK) return st;
+  if (M < 0 || M > kNormMaxM) return fail(LOWBIT_ERR_INVALID_ARG, "M=%lld not in 0..2^23", (long long)M);
+  if (!(eps >= 1e-20f && eps <= 1.0f)) return fail(LOWBIT_ERR_INVALID_ARG, "eps=%g not in 1e-20..1", eps);
+  if (M == 0) return LOWBIT_OK;
+  if (!x) return fail(LOWBIT_ERR_INVALID_ARG, "NULL x");
+  if ((residual != nullptr) != (sum != nullptr))
+    return fail(LOWBIT_ERR_INVALID_ARG, "residual and sum go together");
+  if ((format != LOWBIT_Q8_NONE) != (q != nullptr) || (format != LOWBIT_Q8_NONE) != (qscale != nullptr))
+    return fail(LOWBIT_ERR_INVALID_ARG, "q and qscale are given with an 8-bit format and not without");
+  if (format == LOWBIT_Q8_NONE && !y) return fail(LOWBIT_ERR_INVALID_ARG, "no output: NULL y without a format");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) ||
+      !aligned(y, 16) || !aligned(q, 16) || !aligned(qscale, 4))
+    return fail(LOWBIT_ERR_MISALIGNED, "arrays must be 16-byte aligned, qscale 4-byte aligned");
+  lowbit::NormQ8Params p{};
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.sum = sum;
+  p.y = y;
+  p.q = q;
+  p.qscale = qscale;
+  p.eps = eps;
+  p.M = M;
+  p.K = static_cast<int>(K);
+  const hipError_t e =
+      lowbit::launch_norm_q8(p, act_kind(dtype), static_cast<int>(format), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "norm_q8 launch");
+  return LOWBIT_OK;
+}
+
+lowbit_status lowbit_quantize_act_f8(const void* x, lowbit_dtype dtype, int64_t M, int64_t K, uint8_t* xq,
+                                     float* xscale, void* stream) {
+  g_last_error.clear();
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  const lowbit_status st = check_q8_row(K, 16);
+  if (st != LOWBIT_OK) return st;
+  if (M < 0 || M > kMaxDim || M * f8_blocks(K) >= (int64_t(1) << 28))
+    return fail(LOWBIT_ERR_INVALID_ARG, "M=%lld: M * ceil(K / 128) must be below 2^28", (long long)M);
+  if (M == 0) return LOWBIT_OK;
+  if (!x || !xq || !xscale) return fail(LOWBIT_ERR_INVALID_ARG, "NULL x, xq or xscale");
+  if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(xscale, 4))
+    return fail(LOWBIT_ERR_MISALIGNED, "x and xq must be 16-byte aligned, xscale 4-byte aligned");
+  const lowbit::ActQuantF8Params p{x, xq, xscale, M, static_cast<int>(K)};
+  const hipError_t e = lowbit::launch_act_quant_f8(p, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "act_quant_f8 launch");
+  return LOWBIT_OK;
+}
+
+lowbit_status lowbit_quantize_weight_f8(const void* w, lowbit_dtype dtype, int64_t E, int64_t N, int64_t K,
+                                        uint8_t* wq, float* wscale, void* stream) {
+  g_last_error.clear();
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  const lowbit_status st = check_q8_row(K, 16);
+  if (st != LOWBIT_OK) return st;
+  if (E <= 0 || E > kF8MaxExperts || N <= 0 || N > kMaxDim ||
+      E * f8_blocks(N) * f8_blocks(K) >= (int64_t(1) << 24))
+    return fail(LOWBIT_ERR_INVALID_ARG,
+                "E=%lld N=%lld: must be positive, E at most 2^16, fewer than 2^24 blocks of 128 x 128",
+                (long long)E, (long long)N);
+  if (!w || !wq || !wscale) return fail(LOWBIT_ERR_INVALID_ARG, "NULL w, wq or wscale");
+  if (!aligned(w, 16) || !aligned(wq, 16) || !aligned(wscale, 4))
+    return fail(LOWBIT_ERR_MISALIGNED, "w and wq must be 16-byte aligned, wscale 4-byte aligned");
+  const lowbit::WeightQuantF8Params p{w, wq, wscale, E, static_cast<int>(N), static_cast<int>(K)};
+  const hipError_t e = lowbit::launch_weight_quant_f8(p, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "weight_quant_f8 launch");
+  return LOWBIT_OK;
+}
+
+lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uint8_t* wq,
+                               const float* wscale, const void* bias, void* y, lowbit_dtype dtype,
+                               int64_t M, int64_t N, int64_t K, void* stream) {
+  g_last_error.clear();
+  return run_linear_f8(xq, xscale, nullptr, nullptr, wq, wscale, bias, y, dtype, M, M, 0, N, K, stream);
+}
+
+lowbit_status lowbit_linear_f8_grouped(const uint8_t* xq, const float* xscale, const int32_t* rows,
+                                       const int32_t* offsets, const uint8_t* wq, const float* wscale,
+                                       const void* bias, void* y, lowbit_dtype dtype, int64_t M, int64_t T,
+                                       int64_t E, int64_t N, int64_t K, void* stream) {
+  g_last_error.clear();
+  if (E <= 0 || E > kF8MaxExperts) return fail(LOWBIT_ERR_INVALID_ARG, "E=%lld not in 1..2^16", (long long)E);
+  if (!offsets) return fail(LOWBIT_ERR_INVALID_ARG, "NULL offsets");
+  if (!rows && M != T && T != 0)
+    return fail(LOWBIT_ERR_INVALID_ARG, "without rows, xq's M=%lld must be y's T=%lld", (long long)M, (long long)T);
+  return run_linear_f8(xq, xscale, rows, offsets, wq, wscale, bias, y, dtype, M, T, E, N, K, stream);
 }
 
 }  // extern "C"

@@ -25,6 +25,8 @@ STATUS_NAMES = {
 }
 LOWBIT_F32, LOWBIT_F16, LOWBIT_BF16 = 0, 1, 2
 PATH_AUTO, PATH_QMV, PATH_QMM = 0, 1, 2
+Q8_NONE, Q8_I8, Q8_F8 = 0, 1, 2      # lowbit_q8_format
+F8_BLOCK = 128                       # K elements (and weight rows) sharing an e4m3 scale
 _DTYPE_ENUM = {torch.float32: LOWBIT_F32, torch.float16: LOWBIT_F16, torch.bfloat16: LOWBIT_BF16}
 _ENUM_DTYPE = {v: k for k, v in _DTYPE_ENUM.items()}
 
@@ -32,7 +34,8 @@ EXPORTED_SYMBOLS = (
     "lowbit_abi_version", "lowbit_packed_bytes", "lowbit_num_groups", "lowbit_quantize_pack",
     "lowbit_linear_workspace_bytes", "lowbit_linear", "lowbit_linear_path", "lowbit_linear_multi",
     "lowbit_status_string", "lowbit_last_error", "lowbit_linear_noalloc", "lowbit_set_tuning",
-    "lowbit_quantize_act_i8", "lowbit_linear_a8",
+    "lowbit_quantize_act_i8", "lowbit_linear_a8", "lowbit_add_rmsnorm_q8", "lowbit_quantize_act_f8",
+    "lowbit_quantize_weight_f8", "lowbit_linear_f8", "lowbit_linear_f8_grouped",
 )
 ABI_VERSION = 3
 # schedule overrides (include/lowbit_tuning.h)
@@ -108,6 +111,18 @@ def load() -> ctypes.CDLL:
     lib.lowbit_linear_a8.restype = ctypes.c_int
     lib.lowbit_linear_a8.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_int, ctypes.c_int,
                                      ctypes.c_int, c_i64, c_i64, c_i64, vp]
+    ci, cf = ctypes.c_int, ctypes.c_float
+    lib.lowbit_add_rmsnorm_q8.restype = ci
+    lib.lowbit_add_rmsnorm_q8.argtypes = [vp, vp, vp, cf, ci, c_i64, c_i64, ci, vp, vp, vp, vp, vp]
+    lib.lowbit_quantize_act_f8.restype = ci
+    lib.lowbit_quantize_act_f8.argtypes = [vp, ci, c_i64, c_i64, vp, vp, vp]
+    lib.lowbit_quantize_weight_f8.restype = ci
+    lib.lowbit_quantize_weight_f8.argtypes = [vp, ci, c_i64, c_i64, c_i64, vp, vp, vp]
+    lib.lowbit_linear_f8.restype = ci
+    lib.lowbit_linear_f8.argtypes = [vp, vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64, vp]
+    lib.lowbit_linear_f8_grouped.restype = ci
+    lib.lowbit_linear_f8_grouped.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64,
+                                             c_i64, c_i64, vp]
     if lib.lowbit_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{path} has ABI version {lib.lowbit_abi_version()}, this binding "
                            f"expects {ABI_VERSION}: rebuild it with __graft_entry__.build()")
@@ -499,6 +514,192 @@ def lowbit_linear_a8(xq: torch.Tensor, ascale: torch.Tensor, packed: torch.Tenso
                                   _ptr(bias), _ptr(y), _DTYPE_ENUM[dt], bits, group, M, N, K,
                                   _stream_handle(xq.device, stream))
     _check(st, "lowbit_linear_a8")
+    return y
+
+
+_F8 = torch.float8_e4m3fn
+
+
+def _f8_blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+def _expect_tensor(t: torch.Tensor, name: str, shape: Tuple[int, ...], dtype: torch.dtype) -> None:
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, fmt: int,
+                          residual: Optional[torch.Tensor] = None, want_y: bool = False,
+                          q: Optional[torch.Tensor] = None, qscale: Optional[torch.Tensor] = None,
+                          h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                          stream=None):
+    """RMS norm of the rows of x[M, K] (+ residual) with an 8-bit output.
+
+    h = x + residual (rounded to x's dtype), y = h / sqrt(mean(h^2) + eps) * weight; `fmt` says
+    what is made of y: Q8_I8 (int8 codes, one fp32 scale a row: the input of lowbit_linear_a8),
+    Q8_F8 (e4m3 codes, one fp32 scale a block of 128: the input of lowbit_linear_f8) or Q8_NONE.
+    Returns (q, qscale, h, y): q and qscale are None with Q8_NONE, h is None without a residual,
+    y (x's dtype) is None unless `want_y`, `y` or Q8_NONE asks for it.  `h` may be the residual
+    (or x) itself: the residual stream is then updated in place.
+    """
+    lib = load()
+    _expect(x.dim() == 2, "x must be 2-D [M, K]")
+    dt = x.dtype
+    _expect(dt in _DTYPE_ENUM, f"x dtype {dt} is not float32, float16 or bfloat16")
+    _expect(fmt in (Q8_NONE, Q8_I8, Q8_F8), f"fmt must be Q8_NONE, Q8_I8 or Q8_F8, got {fmt}")
+    M, K = x.shape
+    if weight is not None:
+        _expect_tensor(weight, "weight", (K,), dt)
+    if residual is not None:
+        _expect_tensor(residual, "residual", (M, K), dt)
+        if h is None:
+            h = torch.empty((M, K), dtype=dt, device=x.device)
+        else:
+            _expect_tensor(h, "h", (M, K), dt)
+    else:
+        _expect(h is None, "h is the output x + residual: no residual was given")
+    if fmt == Q8_NONE:
+        _expect(q is None and qscale is None, "q and qscale have no meaning with Q8_NONE")
+    else:
+        code, spans = (torch.int8, (M,)) if fmt == Q8_I8 else (_F8, (M, _f8_blocks(K)))
+        if q is None:
+            q = torch.empty((M, K), dtype=code, device=x.device)
+        else:
+            _expect_tensor(q, "q", (M, K), code)
+        if qscale is None:
+            qscale = torch.empty(spans, dtype=torch.float32, device=x.device)
+        else:
+            _expect_tensor(qscale, "qscale", spans, torch.float32)
+    if y is not None:
+        _expect_tensor(y, "y", (M, K), dt)
+    elif want_y or fmt == Q8_NONE:
+        y = torch.empty((M, K), dtype=dt, device=x.device)
+    _require_cuda(x, weight, residual, q, qscale, h, y)
+    with torch.cuda.device(x.device):
+        st = lib.lowbit_add_rmsnorm_q8(_ptr(x), _ptr(residual), _ptr(weight), eps, _DTYPE_ENUM[dt], M, K,
+                                       fmt, _ptr(q), _ptr(qscale), _ptr(h), _ptr(y),
+                                       _stream_handle(x.device, stream))
+    _check(st, "lowbit_add_rmsnorm_q8")
+    return q, qscale, h, y
+
+
+def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
+                           xscale: Optional[torch.Tensor] = None, stream=None):
+    """e4m3 codes of x[M, K] and the fp32 scale of each block of 128 of a row (on the GPU).
+
+    Returns (xq float8_e4m3fn [M, K], xscale float32 [M, ceil(K/128)])."""
+    lib = load()
+    _expect(x.dim() == 2, "x must be 2-D [M, K]")
+    _expect(x.dtype in _DTYPE_ENUM, f"x dtype {x.dtype} is not float32, float16 or bfloat16")
+    M, K = x.shape
+    if xq is None:
+        xq = torch.empty((M, K), dtype=_F8, device=x.device)
+    if xscale is None:
+        xscale = torch.empty((M, _f8_blocks(K)), dtype=torch.float32, device=x.device)
+    _expect_tensor(xq, "xq", (M, K), _F8)
+    _expect_tensor(xscale, "xscale", (M, _f8_blocks(K)), torch.float32)
+    _require_cuda(x, xq, xscale)
+    with torch.cuda.device(x.device):
+        st = lib.lowbit_quantize_act_f8(_ptr(x), _DTYPE_ENUM[x.dtype], M, K, _ptr(xq), _ptr(xscale),
+                                        _stream_handle(x.device, stream))
+    _check(st, "lowbit_quantize_act_f8")
+    return xq, xscale
+
+
+def lowbit_quantize_weight_f8(w: torch.Tensor, wq: Optional[torch.Tensor] = None,
+                              wscale: Optional[torch.Tensor] = None, stream=None):
+    """e4m3 codes of w[N, K] (or of E experts' w[E, N, K]) and the fp32 scale of each block of
+    128 x 128.  Returns (wq float8_e4m3fn, wscale float32 [(E,) ceil(N/128), ceil(K/128)])."""
+    lib = load()
+    _expect(w.dim() in (2, 3), "w must be [N, K] or [E, N, K]")
+    _expect(w.dtype in _DTYPE_ENUM, f"w must be float32, float16 or bfloat16, got {w.dtype}")
+    N, K = w.shape[-2:]
+    E = w.shape[0] if w.dim() == 3 else 1
+    shape = tuple(w.shape)
+    spans = shape[:-2] + (_f8_blocks(N), _f8_blocks(K))
+    if wq is None:
+        wq = torch.empty(shape, dtype=_F8, device=w.device)
+    if wscale is None:
+        wscale = torch.empty(spans, dtype=torch.float32, device=w.device)
+    _expect_tensor(wq, "wq", shape, _F8)
+    _expect_tensor(wscale, "wscale", spans, torch.float32)
+    _require_cuda(w, wq, wscale)
+    with torch.cuda.device(w.device):
+        st = lib.lowbit_quantize_weight_f8(_ptr(w), _DTYPE_ENUM[w.dtype], E, N, K, _ptr(wq), _ptr(wscale),
+                                           _stream_handle(w.device, stream))
+    _check(st, "lowbit_quantize_weight_f8")
+    return wq, wscale
+
+
+def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor,
+                     bias: Optional[torch.Tensor], dtype: torch.dtype,
+                     y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[M, N] = dequant(xq, xscale) . dequant(wq, wscale)^T (+ bias) on the fp8 matrix cores:
+    e4m3 codes, fp32 scales per block of 128 (activations) and 128 x 128 (weights), fp32 sums;
+    y and bias in `dtype`."""
+    lib = load()
+    _expect(xq.dim() == 2 and wq.dim() == 2, "xq must be [M, K] and wq [N, K]")
+    _expect(dtype in _DTYPE_ENUM, f"dtype {dtype} is not float32, float16 or bfloat16")
+    M, K = xq.shape
+    N = wq.shape[0]
+    kb = _f8_blocks(K)
+    _expect_tensor(xq, "xq", (M, K), _F8)
+    _expect_tensor(xscale, "xscale", (M, kb), torch.float32)
+    _expect_tensor(wq, "wq", (N, K), _F8)
+    _expect_tensor(wscale, "wscale", (_f8_blocks(N), kb), torch.float32)
+    if bias is not None:
+        _expect_tensor(bias, "bias", (N,), dtype)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=xq.device)
+    else:
+        _expect_tensor(y, "y", (M, N), dtype)
+    _require_cuda(xq, xscale, wq, wscale, bias, y)
+    with torch.cuda.device(xq.device):
+        st = lib.lowbit_linear_f8(_ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(y),
+                                  _DTYPE_ENUM[dtype], M, N, K, _stream_handle(xq.device, stream))
+    _check(st, "lowbit_linear_f8")
+    return y
+
+
+def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: torch.Tensor,
+                             wq: torch.Tensor, wscale: torch.Tensor, bias: Optional[torch.Tensor],
+                             dtype: torch.dtype, rows: Optional[torch.Tensor] = None,
+                             y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """lowbit_linear_f8 for rows grouped by expert: row t of y, offsets[e] <= t < offsets[e + 1],
+    is row t of xq (or row rows[t]) times expert e's weight wq[e] (+ bias[e]).
+
+    offsets: int32 [E + 1] on the GPU, not decreasing, within 0..T.  rows: int32 [T], or None
+    (T = M).  Rows of y outside offsets[0] .. offsets[E] are left as they are (a y made here
+    starts out undefined there); an index outside xq makes its row NaN."""
+    lib = load()
+    _expect(xq.dim() == 2 and wq.dim() == 3, "xq must be [M, K] and wq [E, N, K]")
+    _expect(dtype in _DTYPE_ENUM, f"dtype {dtype} is not float32, float16 or bfloat16")
+    M, K = xq.shape
+    E, N = wq.shape[:2]
+    kb = _f8_blocks(K)
+    _expect_tensor(xq, "xq", (M, K), _F8)
+    _expect_tensor(xscale, "xscale", (M, kb), torch.float32)
+    _expect_tensor(wq, "wq", (E, N, K), _F8)
+    _expect_tensor(wscale, "wscale", (E, _f8_blocks(N), kb), torch.float32)
+    _expect_tensor(offsets, "offsets", (E + 1,), torch.int32)
+    T = M
+    if rows is not None:
+        _expect(rows.dim() == 1, "rows must be 1-D [T]")
+        T = rows.shape[0]
+        _expect_tensor(rows, "rows", (T,), torch.int32)
+    if bias is not None:
+        _expect_tensor(bias, "bias", (E, N), dtype)
+    if y is None:
+        y = torch.empty((T, N), dtype=dtype, device=xq.device)
+    else:
+        _expect_tensor(y, "y", (T, N), dtype)
+    _require_cuda(xq, xscale, offsets, wq, wscale, bias, rows, y)
+    with torch.cuda.device(xq.device):
+        st = lib.lowbit_linear_f8_grouped(_ptr(xq), _ptr(xscale), _ptr(rows), _ptr(offsets), _ptr(wq),
+                                          _ptr(wscale), _ptr(bias), _ptr(y), _DTYPE_ENUM[dtype], M, T, E,
+                                          N, K, _stream_handle(xq.device, stream))
+    _check(st, "lowbit_linear_f8_grouped")
     return y
 
 

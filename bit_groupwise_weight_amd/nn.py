@@ -24,9 +24,23 @@ Ops (namespace ``lowbit``):
   fp32 scale (symmetric, max |x| / 127), and the linear runs over the codes
   on the int8 matrix cores (the export mode with 8-bit dynamic activations
   and 4-bit weights in groups of 32 of "[MPS] Add support for Int4 groupwise
-  quantization").
+  quantization");
+* ``lowbit::rmsnorm_q8(Tensor x, Tensor? weight, float eps, int fmt) ->
+  (Tensor q, Tensor qscale)`` and ``lowbit::add_rmsnorm_q8(Tensor x, Tensor
+  residual, Tensor? weight, float eps, int fmt) -> (Tensor q, Tensor qscale,
+  Tensor h)`` -- RMS norm of ``x`` (of ``h = x + residual``) straight to 8-bit
+  codes and scales: ``lowbit.Q8_I8`` (the input of ``lowbit_linear_a8``) or
+  ``lowbit.Q8_F8`` (the input of the ops below);
+* ``lowbit::quantize_act_f8``, ``lowbit::quantize_weight_f8`` -- e4m3 codes
+  with an fp32 scale for each block of 128 (128 x 128);
+* ``lowbit::linear_f8(Tensor xq, Tensor xscale, Tensor wq, Tensor wscale,
+  Tensor? bias, ScalarType dtype) -> Tensor`` -- the linear over such codes on
+  the fp8 matrix cores;
+* ``lowbit::linear_f8_grouped(Tensor xq, Tensor xscale, Tensor? rows, Tensor
+  offsets, Tensor wq, Tensor wscale, Tensor? bias, ScalarType dtype) ->
+  Tensor`` -- the same for rows grouped by expert.
 
-Both run in liblowbit.so through :mod:`bit_groupwise_weight_amd.lowbit`;
+All run in liblowbit.so through :mod:`bit_groupwise_weight_amd.lowbit`;
 nothing here computes on the CPU.
 """
 from __future__ import annotations
@@ -131,6 +145,152 @@ def linear_a8(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
 def _linear_a8_fake(x, packed, scales, zeros, bias, bits, group):
     N, _ = _check_linear_shapes(x, packed, scales, zeros, bias, bits, group)
     return x.new_empty((*x.shape[:-1], N))
+
+
+# ------------------------------------------------------ ops, 8-bit path --
+
+def _check_norm(x: torch.Tensor, weight: Optional[torch.Tensor], fmt: int) -> None:
+    if x.dim() < 1 or x.dtype not in _SZ_DTYPES:
+        raise ValueError(f"x must be [..., K] in one of {_SZ_DTYPES}")
+    if fmt not in (_lb.Q8_I8, _lb.Q8_F8):
+        raise ValueError(f"fmt must be Q8_I8 or Q8_F8, got {fmt}")
+    unit = 32 if fmt == _lb.Q8_I8 else 16
+    if x.shape[-1] == 0 or x.shape[-1] % unit:
+        raise ValueError(f"K={x.shape[-1]} must be a positive multiple of {unit}")
+    if weight is not None and (weight.shape != x.shape[-1:] or weight.dtype != x.dtype):
+        raise ValueError("weight must be [K] in x's dtype")
+
+
+def _norm_out(x: torch.Tensor, fmt: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    lead, K = x.shape[:-1], x.shape[-1]
+    if fmt == _lb.Q8_I8:
+        return x.new_empty(x.shape, dtype=torch.int8), x.new_empty(lead, dtype=torch.float32)
+    return (x.new_empty(x.shape, dtype=torch.float8_e4m3fn),
+            x.new_empty((*lead, _lb._f8_blocks(K)), dtype=torch.float32))
+
+
+@torch.library.custom_op("lowbit::rmsnorm_q8", mutates_args=())
+def rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float,
+               fmt: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    _check_norm(x, weight, fmt)
+    q, s = _norm_out(x, fmt)
+    K = x.shape[-1]
+    _lb.lowbit_add_rmsnorm_q8(x.reshape(-1, K).contiguous(), None if weight is None else weight.contiguous(),
+                              eps, fmt, q=q.view(-1, K),
+                              qscale=s.view(-1) if fmt == _lb.Q8_I8 else s.view(-1, s.shape[-1]))
+    return q, s
+
+
+@rmsnorm_q8.register_fake
+def _rmsnorm_q8_fake(x, weight, eps, fmt):
+    _check_norm(x, weight, fmt)
+    return _norm_out(x, fmt)
+
+
+@torch.library.custom_op("lowbit::add_rmsnorm_q8", mutates_args=())
+def add_rmsnorm_q8(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor], eps: float,
+                   fmt: int) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    _check_norm(x, weight, fmt)
+    if residual.shape != x.shape or residual.dtype != x.dtype:
+        raise ValueError("residual must have x's shape and dtype")
+    q, s = _norm_out(x, fmt)
+    K = x.shape[-1]
+    h = x.new_empty(x.shape)
+    _lb.lowbit_add_rmsnorm_q8(x.reshape(-1, K).contiguous(), None if weight is None else weight.contiguous(),
+                              eps, fmt, residual=residual.reshape(-1, K).contiguous(), q=q.view(-1, K),
+                              qscale=s.view(-1) if fmt == _lb.Q8_I8 else s.view(-1, s.shape[-1]),
+                              h=h.view(-1, K))
+    return q, s, h
+
+
+@add_rmsnorm_q8.register_fake
+def _add_rmsnorm_q8_fake(x, residual, weight, eps, fmt):
+    _check_norm(x, weight, fmt)
+    if residual.shape != x.shape or residual.dtype != x.dtype:
+        raise ValueError("residual must have x's shape and dtype")
+    return (*_norm_out(x, fmt), x.new_empty(x.shape))
+
+
+@torch.library.custom_op("lowbit::quantize_act_f8", mutates_args=())
+def quantize_act_f8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    _check_norm(x, None, _lb.Q8_F8)
+    q, s = _norm_out(x, _lb.Q8_F8)
+    K = x.shape[-1]
+    _lb.lowbit_quantize_act_f8(x.reshape(-1, K).contiguous(), q.view(-1, K), s.view(-1, s.shape[-1]))
+    return q, s
+
+
+@quantize_act_f8.register_fake
+def _quantize_act_f8_fake(x):
+    _check_norm(x, None, _lb.Q8_F8)
+    return _norm_out(x, _lb.Q8_F8)
+
+
+@torch.library.custom_op("lowbit::quantize_weight_f8", mutates_args=())
+def quantize_weight_f8(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    if w.dtype not in _SZ_DTYPES:
+        w = w.float()
+    return _lb.lowbit_quantize_weight_f8(w.contiguous())
+
+
+@quantize_weight_f8.register_fake
+def _quantize_weight_f8_fake(w):
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    N, K = w.shape[-2:]
+    spans = (*w.shape[:-2], _lb._f8_blocks(N), _lb._f8_blocks(K))
+    return w.new_empty(w.shape, dtype=torch.float8_e4m3fn), w.new_empty(spans, dtype=torch.float32)
+
+
+def _check_f8(xq, xscale, wq, wscale, bias, dtype) -> None:
+    K = xq.shape[-1]
+    if wq.shape[-1] != K:
+        raise ValueError(f"xq has K={K}, wq has K={wq.shape[-1]}")
+    if xq.dtype != torch.float8_e4m3fn or wq.dtype != torch.float8_e4m3fn:
+        raise ValueError("xq and wq must be float8_e4m3fn")
+    if xscale.shape != (*xq.shape[:-1], _lb._f8_blocks(K)) or xscale.dtype != torch.float32:
+        raise ValueError("xscale must be float32 [..., ceil(K/128)]")
+    if (wscale.shape != (*wq.shape[:-2], _lb._f8_blocks(wq.shape[-2]), _lb._f8_blocks(K))
+            or wscale.dtype != torch.float32):
+        raise ValueError("wscale must be float32 [(E,) ceil(N/128), ceil(K/128)]")
+    if dtype not in _SZ_DTYPES:
+        raise ValueError(f"dtype must be one of {_SZ_DTYPES}")
+    if bias is not None and (bias.shape != wq.shape[:-1] or bias.dtype != dtype):
+        raise ValueError("bias must be [(E,) N] in the output dtype")
+
+
+@torch.library.custom_op("lowbit::linear_f8", mutates_args=())
+def linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor,
+              bias: Optional[torch.Tensor], dtype: torch.dtype) -> torch.Tensor:
+    _check_f8(xq, xscale, wq, wscale, bias, dtype)
+    K, N = xq.shape[-1], wq.shape[0]
+    y = _lb.lowbit_linear_f8(xq.reshape(-1, K).contiguous(), xscale.reshape(-1, xscale.shape[-1]).contiguous(),
+                             wq.contiguous(), wscale.contiguous(),
+                             None if bias is None else bias.contiguous(), dtype)
+    return y.reshape(*xq.shape[:-1], N)
+
+
+@linear_f8.register_fake
+def _linear_f8_fake(xq, xscale, wq, wscale, bias, dtype):
+    _check_f8(xq, xscale, wq, wscale, bias, dtype)
+    return xq.new_empty((*xq.shape[:-1], wq.shape[0]), dtype=dtype)
+
+
+@torch.library.custom_op("lowbit::linear_f8_grouped", mutates_args=())
+def linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, rows: Optional[torch.Tensor],
+                      offsets: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor,
+                      bias: Optional[torch.Tensor], dtype: torch.dtype) -> torch.Tensor:
+    _check_f8(xq, xscale, wq, wscale, bias, dtype)
+    return _lb.lowbit_linear_f8_grouped(xq.contiguous(), xscale.contiguous(), offsets, wq.contiguous(),
+                                        wscale.contiguous(), None if bias is None else bias.contiguous(),
+                                        dtype, rows=rows)
+
+
+@linear_f8_grouped.register_fake
+def _linear_f8_grouped_fake(xq, xscale, rows, offsets, wq, wscale, bias, dtype):
+    _check_f8(xq, xscale, wq, wscale, bias, dtype)
+    T = xq.shape[0] if rows is None else rows.shape[0]
+    return xq.new_empty((T, wq.shape[1]), dtype=dtype)
 
 
 # --------------------------------------------------------------- module --
@@ -249,3 +409,148 @@ def _swap(parent, name, child, qual, bits, group_size, dtype, filter_fn, act_bit
         return
     for n, c in list(child.named_children()):
         _swap(child, n, c, f"{qual}.{n}", bits, group_size, dtype, filter_fn, act_bits)
+
+
+class F8Linear(torch.nn.Module):
+    """``nn.Linear`` with e4m3 weights and activations, an fp32 scale for each block of 128 x 128
+    weights and of 128 activations of a row.
+
+    Buffers: ``wq`` (float8_e4m3fn, ``[N, K]``), ``wscale`` (fp32, ``[ceil(N/128), ceil(K/128)]``)
+    and optional ``bias`` (``[N]``).  ``forward(x)`` quantizes x's rows on the fly; where a norm
+    made the codes already (``lowbit::add_rmsnorm_q8``), ``forward_codes(xq, xscale)`` takes them.
+    """
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True,
+                 dtype: torch.dtype = torch.bfloat16, device: Optional[torch.device] = None):
+        super().__init__()
+        if dtype not in _SZ_DTYPES:
+            raise ValueError(f"dtype must be one of {_SZ_DTYPES}")
+        if in_features <= 0 or in_features % 16 != 0:
+            raise ValueError(f"in_features={in_features} is not a positive multiple of 16")
+        self.in_features, self.out_features, self.dtype = in_features, out_features, dtype
+        self.register_buffer("wq", torch.zeros((out_features, in_features), dtype=torch.float8_e4m3fn,
+                                               device=device))
+        self.register_buffer("wscale", torch.zeros((_lb._f8_blocks(out_features), _lb._f8_blocks(in_features)),
+                                                   dtype=torch.float32, device=device))
+        if bias:
+            self.register_buffer("bias", torch.zeros((out_features,), dtype=dtype, device=device))
+        else:
+            self.bias = None
+
+    @torch.no_grad()
+    def set_weight(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None) -> "F8Linear":
+        """Quantize a float ``weight[N, K]`` (on the GPU) into this module."""
+        if tuple(weight.shape) != (self.out_features, self.in_features):
+            raise ValueError(f"weight must be [{self.out_features}, {self.in_features}]")
+        wq, wscale = torch.ops.lowbit.quantize_weight_f8(weight.detach())
+        self.wq.copy_(wq)
+        self.wscale.copy_(wscale)
+        if self.bias is not None:
+            if bias is None:
+                self.bias.zero_()
+            else:
+                self.bias.copy_(bias.detach().to(self.dtype))
+        return self
+
+    @classmethod
+    def from_linear(cls, lin: torch.nn.Linear, dtype: Optional[torch.dtype] = None) -> "F8Linear":
+        """Quantize ``lin`` on the fly (its weight must live on the GPU)."""
+        dt = dtype or (lin.weight.dtype if lin.weight.dtype in _SZ_DTYPES else torch.bfloat16)
+        m = cls(lin.in_features, lin.out_features, bias=lin.bias is not None, dtype=dt,
+                device=lin.weight.device)
+        return m.set_weight(lin.weight, lin.bias)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        xq, xscale = torch.ops.lowbit.quantize_act_f8(x)
+        return self.forward_codes(xq, xscale)
+
+    def forward_codes(self, xq: torch.Tensor, xscale: torch.Tensor) -> torch.Tensor:
+        return torch.ops.lowbit.linear_f8(xq, xscale, self.wq, self.wscale, self.bias, self.dtype)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, dtype={self.dtype}, "
+                f"bias={self.bias is not None}")
+
+
+def quantize_linears_f8(model: torch.nn.Module, dtype: Optional[torch.dtype] = None,
+                        filter_fn: Optional[Callable[[torch.nn.Module, str], bool]] = None
+                        ) -> torch.nn.Module:
+    """Replace every ``nn.Linear`` of ``model`` (in place) by an F8Linear; layers whose in_features
+    is not a multiple of 16, and those that ``filter_fn(module, qualified_name)`` excludes, are left
+    as they are."""
+    for qual, child in [(n, c) for n, c in model.named_modules() if isinstance(c, torch.nn.Linear) and n]:
+        if child.in_features % 16 == 0 and (filter_fn is None or filter_fn(child, qual)):
+            parent, _, name = qual.rpartition(".")
+            setattr(model.get_submodule(parent), name, F8Linear.from_linear(child, dtype))
+    return model
+
+
+class F8Experts(torch.nn.Module):
+    """The experts of a mixture-of-experts block in the e4m3 format: for a token x and each of its
+    experts e with routing weight r,
+
+        out += r * down[e] (silu(gate[e] x) * (up[e] x))
+
+    Buffers: ``gate_up`` (``[E, 2 I, H]``, gate rows first) and ``down`` (``[E, H, I]``) as e4m3
+    codes with their block scales.  The tokens' codes are made once whatever number of experts a
+    token goes to, and nothing waits for the routing on the host.
+    """
+
+    def __init__(self, num_experts: int, hidden: int, intermediate: int,
+                 dtype: torch.dtype = torch.bfloat16, device: Optional[torch.device] = None):
+        super().__init__()
+        if dtype not in _SZ_DTYPES:
+            raise ValueError(f"dtype must be one of {_SZ_DTYPES}")
+        if num_experts < 1 or hidden <= 0 or intermediate <= 0 or hidden % 16 or intermediate % 16:
+            raise ValueError("hidden and intermediate must be positive multiples of 16, num_experts >= 1")
+        self.num_experts, self.hidden, self.intermediate, self.dtype = num_experts, hidden, intermediate, dtype
+        b = _lb._f8_blocks
+        for name, n, k in (("gate_up", 2 * intermediate, hidden), ("down", hidden, intermediate)):
+            self.register_buffer(name, torch.zeros((num_experts, n, k), dtype=torch.float8_e4m3fn,
+                                                   device=device))
+            self.register_buffer(name + "_scale", torch.zeros((num_experts, b(n), b(k)),
+                                                              dtype=torch.float32, device=device))
+
+    @torch.no_grad()
+    def set_weight(self, gate_up: torch.Tensor, down: torch.Tensor) -> "F8Experts":
+        """Quantize float ``gate_up[E, 2 I, H]`` and ``down[E, H, I]`` (on the GPU) into this module."""
+        for name, w in (("gate_up", gate_up), ("down", down)):
+            if w.shape != getattr(self, name).shape:
+                raise ValueError(f"{name} must be {list(getattr(self, name).shape)}, got {list(w.shape)}")
+            q, s = torch.ops.lowbit.quantize_weight_f8(w.detach())
+            getattr(self, name).copy_(q)
+            getattr(self, name + "_scale").copy_(s)
+        return self
+
+    def forward(self, x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
+        """x[..., H] (the module's dtype); experts (integer) and weights, both [..., k]: each
+        token's experts and their routing weights."""
+        xq, xscale = torch.ops.lowbit.quantize_act_f8(x.reshape(-1, self.hidden))
+        return self.forward_codes(xq, xscale, experts, weights).reshape(x.shape)
+
+    def forward_codes(self, xq: torch.Tensor, xscale: torch.Tensor, experts: torch.Tensor,
+                      weights: torch.Tensor) -> torch.Tensor:
+        """The same for tokens' codes and scales as ``lowbit::add_rmsnorm_q8`` makes them: [T, H]."""
+        T, k = xq.shape[0], experts.shape[-1]
+        if experts.shape != weights.shape or experts.numel() != T * k:
+            raise ValueError("experts and weights must both be [T, k]")
+        ids = experts.reshape(-1)
+        order = torch.argsort(ids, stable=True)
+        # rows of the experts below each bound: where every expert's rows begin and end
+        bounds = torch.arange(self.num_experts + 1, device=ids.device, dtype=ids.dtype)
+        offsets = torch.searchsorted(ids[order], bounds).to(torch.int32)
+        rows = torch.div(order, k, rounding_mode="floor").to(torch.int32)
+        gu = torch.ops.lowbit.linear_f8_grouped(xq, xscale, rows, offsets, self.gate_up, self.gate_up_scale,
+                                                None, self.dtype)
+        gate, up = gu.split(self.intermediate, dim=-1)
+        aq, ascale = torch.ops.lowbit.quantize_act_f8(torch.nn.functional.silu(gate) * up)
+        slots = torch.ops.lowbit.linear_f8_grouped(aq, ascale, None, offsets, self.down, self.down_scale,
+                                                   None, self.dtype)
+        back = torch.empty_like(order)
+        back[order] = torch.arange(order.numel(), device=order.device)
+        out = slots[back].view(T, k, self.hidden).float() * weights.reshape(T, k, 1).float()
+        return out.sum(1).to(self.dtype)
+
+    def extra_repr(self) -> str:
+        return (f"num_experts={self.num_experts}, hidden={self.hidden}, intermediate={self.intermediate}, "
+                f"dtype={self.dtype}")

@@ -276,6 +276,133 @@ lowbit_status lowbit_linear_a8(const int8_t* xq, const float* ascale, const uint
                                lowbit_dtype dtype, int bits, int group, int64_t M, int64_t N,
                                int64_t K, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit path: a residual-add RMS norm whose output is 8-bit codes with
+ * scales (int8 rows for lowbit_linear_a8, or e4m3 blocks), and linears over
+ * e4m3 codes with fp32 scales, dense and grouped by expert.
+ *
+ * Formats of 8-bit codes, a span of values sharing one fp32 scale s:
+ *   - int8 rows:   a span is a row; s = max |v| / 127,
+ *                  code = rint_half_even(v / s), in -127..127;
+ *   - e4m3 blocks: a span is 128 consecutive K elements of a row (weights:
+ *                  128 rows x 128 K elements of one matrix), the last one of a
+ *                  row or column possibly shorter; s = max |v| / 448, code =
+ *                  the OCP e4m3 number (4 significant bits, at most 448)
+ *                  nearest to v / s, ties to even.
+ * v / s is computed as v * (top / max |v|) in fp32 (top = 127 or 448).  A
+ * span whose max |v| is below 2^-110 gets scale 0 and codes 0; a span holding
+ * a NaN or an infinity gets scale NaN and codes 0, so that every output it
+ * enters is NaN.  Codes and scales are bitwise determined by the input.
+ * ---------------------------------------------------------------------- */
+
+/* What lowbit_add_rmsnorm_q8 writes besides the sum and the normalized rows. */
+typedef enum lowbit_q8_format {
+  LOWBIT_Q8_NONE = 0,  /* no codes: y is the output                             */
+  LOWBIT_Q8_I8 = 1,    /* int8 rows, the input of lowbit_linear_a8              */
+  LOWBIT_Q8_F8 = 2     /* e4m3 blocks, the input of lowbit_linear_f8[_grouped]  */
+} lowbit_q8_format;
+
+/* Root-mean-square norm of rows, with the residual's addition and an 8-bit
+ * output.  Per row, in fp32:
+ *   h = x + residual, rounded to dtype      (h = x without a residual)
+ *   y = h / sqrt(sum_k h[k]^2 / K + eps) * weight
+ * and the codes and scales of the unrounded y in `format`.
+ *
+ *   x         device, M x K row-major, dtype, 16-byte aligned.
+ *   residual  device, M x K, dtype, 16-byte aligned, or NULL.
+ *   weight    device, K elements of dtype, 16-byte aligned, or NULL (ones).
+ *   eps       1e-20 .. 1.
+ *   M >= 0 (0 is a no-op; at most 2^23), K > 0 and a multiple of 16 (of 32
+ *             with LOWBIT_Q8_I8, as lowbit_linear_a8 takes it), K <= 2^23.
+ *   q         device, M x K codes, 16-byte aligned.  Written.  NULL with
+ *             LOWBIT_Q8_NONE.
+ *   qscale    device, fp32, 4-byte aligned: M (int8) or M x ceil(K / 128)
+ *             (e4m3).  Written.  NULL with LOWBIT_Q8_NONE.
+ *   sum       device, M x K, dtype, 16-byte aligned: h.  Written.  Required
+ *             with a residual, NULL without; may be x or residual itself
+ *             (in place), must not overlap them otherwise.
+ *   y         device, M x K, dtype, 16-byte aligned: the normalized rows
+ *             rounded to dtype, or NULL (required with LOWBIT_Q8_NONE).
+ *   q, qscale and y must not overlap an input or each other.
+ *
+ * A row of h holding a NaN or an infinity: its scales and its row of y are
+ * NaN, its codes 0.  A finite row whose squares overflow fp32 is normalized
+ * exactly as any other.  Asynchronous, one launch, deterministic. */
+lowbit_status lowbit_add_rmsnorm_q8(const void* x, const void* residual, const void* weight, float eps,
+                                    lowbit_dtype dtype, int64_t M, int64_t K, lowbit_q8_format format,
+                                    void* q, float* qscale, void* sum, void* y, void* stream);
+
+/* e4m3 blocks of activation rows that no norm precedes.
+ *
+ *   x        device, M x K row-major, dtype, 16-byte aligned.
+ *   M >= 0 (0 is a no-op), K > 0 and a multiple of 16, K <= 2^23,
+ *            M * ceil(K / 128) < 2^28.
+ *   xq       device, M x K e4m3 codes, 16-byte aligned.  Written.
+ *   xscale   device, M x ceil(K / 128) fp32, 4-byte aligned.  Written.
+ * Asynchronous. */
+lowbit_status lowbit_quantize_act_f8(const void* x, lowbit_dtype dtype, int64_t M, int64_t K, uint8_t* xq,
+                                     float* xscale, void* stream);
+
+/* e4m3 blocks (128 x 128) of one or several weight matrices (one-off).
+ *
+ *   w        device, E x N x K row-major ([expert,] out, in), dtype, 16-byte
+ *            aligned.
+ *   E, N, K > 0, K a multiple of 16, K <= 2^23, N <= 2^30,
+ *            E * ceil(N / 128) * ceil(K / 128) < 2^24.
+ *   wq       device, E x N x K e4m3 codes, 16-byte aligned.  Written.
+ *   wscale   device, E x ceil(N / 128) x ceil(K / 128) fp32.  Written.
+ * Asynchronous; a block holding a NaN or an infinity is marked by a NaN
+ * scale. */
+lowbit_status lowbit_quantize_weight_f8(const void* w, lowbit_dtype dtype, int64_t E, int64_t N, int64_t K,
+                                        uint8_t* wq, float* wscale, void* stream);
+
+/* y[m, n] = sum_b xscale[m, b] * wscale[n / 128, b] * P_b[m, n] (+ bias[n]),
+ * P_b the sum of xq * wq over K block b, on the fp8 matrix cores.
+ *
+ *   xq, xscale   as written by lowbit_quantize_act_f8 or lowbit_add_rmsnorm_q8
+ *            (any e4m3 codes and fp32 scales of that layout): M x K, M x
+ *            ceil(K / 128).
+ *   wq, wscale   as written by lowbit_quantize_weight_f8 with E = 1.
+ *   bias     device, N elements of dtype, or NULL.
+ *   y        device, M x N row-major, dtype, aligned to its element size.
+ *            Overwritten; must not alias an input.
+ *   dtype    type of bias and y (fp32, fp16, bf16).
+ *   M >= 0 (0 is a no-op; at most 2^30), N > 0 (at most 2^30), K as above.
+ *   xq and wq 16-byte aligned, the scales 4-byte aligned.
+ *
+ * Products accumulate in fp32; the bias is added in fp32 and the result
+ * rounded once to dtype, nearest even.  Asynchronous and deterministic: no
+ * atomics, and every output is summed in an order fixed by the shape. */
+lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uint8_t* wq,
+                               const float* wscale, const void* bias, void* y, lowbit_dtype dtype,
+                               int64_t M, int64_t N, int64_t K, void* stream);
+
+/* The same product for rows grouped by expert: row t of y, with
+ * offsets[e] <= t < offsets[e + 1], is computed with weight, scales and bias
+ * e from row t of xq, or from row rows[t] where `rows` is given (so that a
+ * token's codes are made once however many experts it goes to).
+ *
+ *   xq, xscale   M x K codes and M x ceil(K / 128) scales.
+ *   rows     device, T int32, 4-byte aligned, or NULL (then M == T).  An
+ *            index outside 0 .. M - 1 makes its row of y NaN.
+ *   offsets  device, E + 1 int32, 4-byte aligned, not decreasing, within
+ *            0 .. T; equal neighbours are an expert without rows.  Rows of y
+ *            before offsets[0] and from offsets[E] on are left as they are.
+ *            (Offsets are read on the device and cannot be refused: bounds
+ *            out of range or decreasing leave unspecified values in y, and
+ *            nothing outside the arrays is read or written.)
+ *   wq, wscale   E matrices as written by lowbit_quantize_weight_f8.
+ *   bias     device, E x N elements of dtype, or NULL.
+ *   y        device, T x N row-major, dtype.
+ *   T >= 0 (0 is a no-op; at most 2^30), M >= 1 where T > 0, 1 <= E <= 2^16;
+ *   N, K, alignment, accumulation and order as for lowbit_linear_f8.
+ *
+ * Asynchronous, no workspace; nothing waits for the offsets on the host. */
+lowbit_status lowbit_linear_f8_grouped(const uint8_t* xq, const float* xscale, const int32_t* rows,
+                                       const int32_t* offsets, const uint8_t* wq, const float* wscale,
+                                       const void* bias, void* y, lowbit_dtype dtype, int64_t M, int64_t T,
+                                       int64_t E, int64_t N, int64_t K, void* stream);
+
 /* Static text for a status code. */
 const char* lowbit_status_string(lowbit_status status);
 
