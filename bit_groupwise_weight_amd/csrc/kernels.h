@@ -235,8 +235,22 @@ struct LinearF8Params {
   int N, K, E;            // K % 16 == 0
   int kb, nb;             // ceil(K / 128), ceil(N / 128)
   int tiles_n;            // column tiles
+  float* partials;        // K splits: planes of T x n_pad fp32 (workspace)
+  int n_pad;              // N rounded up to a multiple of 4
+  int kb_split;           // K blocks of a split
 };
-hipError_t launch_linear_f8(const LinearF8Params&, int out, hipStream_t);
+// Variants: few rows (16 rows and 16, 32 or 64 columns a block, the weights
+// straight from memory); tiles of columns x rows through LDS, their K range
+// split over the grid where there are few (partial sums in the workspace);
+// and 256 x 256 tiles (16-bit outputs).
+enum LinearF8Kind : int {
+  F8_ROWS_NT1, F8_ROWS_NT2, F8_ROWS_NT4, F8_TILE_64X32, F8_TILE_64X64, F8_TILE_128X128, F8_TILE_256X256
+};
+struct LinearF8Plan {
+  LinearF8Kind kind;
+  int splits;             // K splits (tiles below 256 x 256; 1: no partial sums)
+};
+hipError_t launch_linear_f8(const LinearF8Params&, const LinearF8Plan&, int out, hipStream_t);
 
 // ------------------------------------------------- library-owned scratch --
 // Size of the device array behind lowbit_linear_noalloc (per device).  The

@@ -27,12 +27,52 @@ namespace {
 // different 4-bank groups.
 __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 
-__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// Direct global -> LDS loads and their waits in inline assembly: the compiler
+// drains every load before it reads LDS, the kernel waits only for the step
+// that it reads next.  Lane l writes LDS at m0 + 16 l; there is no
+// destination register.
+__device__ __forceinline__ void dma16(const void* vaddr, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               : : "v"(vaddr), "s"(m0) : "memory", "m0");
+}
+// At most N of this wave's loads still in flight and its LDS accesses done,
+// then meet the block's other waves.
+template <int N>
+__device__ __forceinline__ void wait_loads_then_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range (63: no wait for loads)");
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ uint32_t lds_address(T* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)p));
 }
 
-// The expert and rows of row tile `tile` of the launch (BM rows a tile).
+// Rows of expert e (clamped to 0 .. T; none past the last expert).
+__device__ __forceinline__ void expert_rows(const LinearF8Params& p, int e, int64_t* lo, int64_t* hi) {
+  *lo = *hi = 0;
+  if (e < p.E) {
+    *lo = min(max(static_cast<int64_t>(p.offsets[e]), int64_t{0}), p.T);
+    *hi = min(max(static_cast<int64_t>(p.offsets[e + 1]), *lo), p.T);
+  }
+}
+
+// Row tiles of BM rows that the call has in all (the same in every lane).
+template <int BM>
+__device__ __forceinline__ int64_t count_row_tiles(const LinearF8Params& p) {
+  if (p.offsets == nullptr) return (p.T + BM - 1) / BM;
+  int64_t n = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int64_t lo, hi;
+    expert_rows(p, e0 + (threadIdx.x & 63), &lo, &hi);
+    int own = static_cast<int>((hi - lo + BM - 1) / BM);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) own += __shfl_xor(own, o);
+    n += __builtin_amdgcn_readfirstlane(own);
+  }
+  return n;
+}
+
+// The expert and rows of row tile `tile` of the call.
 struct RowTile {
   int64_t begin, end;     // rows of y
   int expert;             // -1: none
@@ -51,12 +91,8 @@ __device__ __forceinline__ RowTile find_rows(const LinearF8Params& p, int64_t ti
   const int lane = threadIdx.x & 63;
   int64_t before = 0;     // tiles of the experts already passed
   for (int e0 = 0; e0 < p.E; e0 += 64) {
-    const int e = e0 + lane;
-    int64_t lo = 0, hi = 0;
-    if (e < p.E) {
-      lo = min(max(static_cast<int64_t>(p.offsets[e]), int64_t{0}), p.T);
-      hi = min(max(static_cast<int64_t>(p.offsets[e + 1]), lo), p.T);
-    }
+    int64_t lo, hi;
+    expert_rows(p, e0 + lane, &lo, &hi);
     const int own = static_cast<int>((hi - lo + BM - 1) / BM);
     int upto = own;       // inclusive prefix sum over the lanes
 #pragma unroll
@@ -68,16 +104,34 @@ __device__ __forceinline__ RowTile find_rows(const LinearF8Params& p, int64_t ti
     const uint64_t hit = __ballot(tile >= first && tile < first + own);
     if (hit != 0) {       // one lane at most: the ranges do not overlap
       const int src = __builtin_ctzll(hit);
-      const int64_t at = __shfl(static_cast<int>(tile - first), src);
-      const int64_t lo_s = __shfl(static_cast<int>(lo), src), hi_s = __shfl(static_cast<int>(hi), src);
-      t.begin = lo_s + at * BM;
-      t.end = min(t.begin + BM, hi_s);
+      const int at = __builtin_amdgcn_readlane(static_cast<int>(tile - first), src);
+      const int lo_s = __builtin_amdgcn_readlane(static_cast<int>(lo), src);
+      const int hi_s = __builtin_amdgcn_readlane(static_cast<int>(hi), src);
+      t.begin = lo_s + static_cast<int64_t>(at) * BM;
+      t.end = min(t.begin + BM, static_cast<int64_t>(hi_s));
       t.expert = e0 + src;
       return t;
     }
-    before += __shfl(upto, 63);
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
   return t;
+}
+
+// Tile of this block among tiles_m x tiles_n: blocks go to the 8 XCDs in turn,
+// so each XCD takes a contiguous run of the tiles, and the runs go through
+// patches GM row tiles high, so that the tiles an XCD has in flight share
+// rows of both operands in its L2.
+template <int GM>
+__device__ __forceinline__ bool tile_of_block(int64_t tiles_m, int64_t tiles_n, int64_t* tm, int* tn) {
+  const int64_t all = tiles_m * tiles_n, id = blockIdx.x;
+  if (id >= all) return false;
+  const int64_t q = all / 8, r = all % 8, xcd = id % 8;
+  const int64_t at = xcd * q + min(xcd, r) + id / 8;
+  const int64_t patch = at / (GM * tiles_n), rest = at - patch * (GM * tiles_n);
+  const int64_t high = min(static_cast<int64_t>(GM), tiles_m - patch * GM);
+  *tm = patch * GM + rest % high;
+  *tn = static_cast<int>(rest / high);
+  return true;
 }
 
 // Four consecutive outputs of row m from column n on (n % 4 == 0).
@@ -102,120 +156,207 @@ __device__ __forceinline__ void store4(const LinearF8Params& p, int64_t m, int n
 
 }  // namespace
 
-// Block of WN x WM waves over BN columns (n) and BM rows (t) of y; K steps of
-// 128 staged through two LDS buffers by direct loads one step ahead.
-template <int BN, int BM, int WN, int WM, int OUT>
+// Two fp32 values -> two values of a 16-bit type, nearest even, in one word.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {lo, hi};
+  if constexpr (OUT == ACT_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf162_t));
+}
+
+// A wave's outputs (NT x MT tiles, rows m0 .., columns n0 ..) rounded and
+// turned through LDS, so that they leave as whole 16-byte pieces of y's rows
+// from a short loop (unrolled stores of the accumulators with their edge cases
+// are some 80 KB of code a wave runs once: 20 us of instruction fetches).
+template <int OUT, int NT>
+constexpr int kOutPitch = NT * 16 * Act<OUT>::bytes + 16;   // bytes of a row in LDS: 16 rows hit 16 bank groups
+template <int OUT, int NT, int MT>
+constexpr int kOutBytes = MT * 16 * kOutPitch<OUT, NT>;
+template <int OUT, int NT, int MT>
+__device__ __forceinline__ void store_outputs(const LinearF8Params& p, const f32x4_t (&acc)[NT][MT],
+                                              uint8_t* lds, int expert, int64_t m0, int64_t m_end, int n0) {
+  constexpr int E = Act<OUT>::bytes, PITCH = kOutPitch<OUT, NT>;
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    float bias[4] = {};
+    if (p.bias) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        bias[q] = load_act<OUT>(p.bias, static_cast<size_t>(expert) * p.N + min(n0 + 16 * i + 4 * g + q, p.N - 1));
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      uint8_t* at = lds + (16 * j + c16) * PITCH + (16 * i + 4 * g) * E;
+      const f32x4_t v = acc[i][j];
+      if constexpr (OUT == ACT_F32) {
+        *reinterpret_cast<f32x4_t*>(at) = f32x4_t{v[0] + bias[0], v[1] + bias[1], v[2] + bias[2], v[3] + bias[3]};
+      } else {
+        *reinterpret_cast<u32v2_t*>(at) =
+            u32v2_t{pack2<OUT>(v[0] + bias[0], v[1] + bias[1]), pack2<OUT>(v[2] + bias[2], v[3] + bias[3])};
+      }
+    }
+  }
+  constexpr int PIECE = 16 / E;        // outputs of 16 bytes
+  constexpr int LANES = NT * 16 / PIECE;                // lanes of a row
+  const bool wide = p.N % PIECE == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+  const int n = n0 + lane % LANES * PIECE;
+#pragma unroll 1
+  for (int r = lane / LANES; r < MT * 16; r += 64 / LANES) {
+    const int64_t m = m0 + r;
+    if (m >= m_end || n >= p.N) continue;
+    const uint8_t* at = lds + r * PITCH + lane % LANES * 16;
+    const u32v4_t v = *reinterpret_cast<const u32v4_t*>(at);
+    typedef typename Act<OUT>::bits_t T;
+    T* to = static_cast<T*>(p.y) + static_cast<size_t>(m) * p.N + n;
+    if (wide) {
+      *reinterpret_cast<u32v4_t*>(to) = v;
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < PIECE && n + k < p.N; ++k) to[k] = reinterpret_cast<const T*>(at)[k];
+    }
+  }
+}
+
+// What the activations past a row's end in its last, partial block are read
+// from (the weights there read the block's first chunk: finite or NaN as the
+// products they meet anyway), and a gathered row outside xq its scales.
+__device__ __attribute__((aligned(16))) const uint32_t kZeroCodes[4] = {0u, 0u, 0u, 0u};
+__device__ __attribute__((aligned(16))) const float kNanScales[4] = {
+    __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+
+// Block of WN x WM waves over BN columns (n) and BM rows (t) of y.  K steps of
+// 128 go through a ring of S LDS stages, loaded S - 1 steps ahead; a step has
+// one barrier, before which a wave waits for its own loads of that step.
+// SPLIT: blockIdx.y takes a run of K blocks and writes fp32 partial sums.
+template <int BN, int BM, int WN, int WM, int S, bool SPLIT, int OUT>
 __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Params p) {
-  constexpr int NW = WN * WM;
   constexpr bool EXACT = OUT == ACT_F32;
+  constexpr int NW = WN * WM;
   constexpr int NT = BN / WN / 16, MT = BM / WM / 16;   // 16-wide tiles of a wave
   constexpr int ROWS = BN + BM;
   constexpr int LOADS = ROWS / 8 / NW;                  // 1 KiB loads of a wave per step
   static_assert(ROWS % (8 * NW) == 0 && BN % 8 == 0, "whole loads");
-  static_assert(BM <= 64 * NW && kF8Block % BN == 0, "one scale row a block of columns");
-  __shared__ __attribute__((aligned(16))) uint8_t s_codes[2][ROWS * kF8Block];
-  __shared__ float s_xs[2][BM];
+  static_assert(BM <= 64 * NW, "one scale load a wave");
+  static_assert((16 * NT) <= kF8Block && kF8Block % (16 * NT) == 0, "a wave's columns share a scale");
+  constexpr int STAGE = ROWS * kF8Block;
+  constexpr int OUT_BYTES = SPLIT ? 0 : NW * kOutBytes<OUT, NT, MT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[S * STAGE > OUT_BYTES ? S * STAGE : OUT_BYTES];
+  __shared__ __attribute__((aligned(1024))) float s_xs[2][64 * NW][4];
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tile_n = blockIdx.x % p.tiles_n;
-  const RowTile rt = find_rows<BM>(p, blockIdx.x / p.tiles_n);
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t tile_m;
+  int tile_n;
+  if (!tile_of_block<BM >= 128 ? 8 : 16>(count_row_tiles<BM>(p), p.tiles_n, &tile_m, &tile_n)) return;
+  const RowTile rt = find_rows<BM>(p, tile_m);
   if (rt.expert < 0) return;
   const int n0 = tile_n * BN;
+  const int wn = wv % WN, wm = wv / WN;
   const uint8_t* wq = p.wq + static_cast<size_t>(rt.expert) * p.N * p.K;
-  const float* ws = p.ws + (static_cast<size_t>(rt.expert) * p.nb + n0 / kF8Block) * p.kb;
-
-  // source row of output row t (clamped to the tile); ok: inside xq
-  auto source_row = [&](int64_t t, bool* ok) -> int64_t {
-    t = min(t, rt.end - 1);
-    if (p.rows == nullptr) {
-      *ok = true;
-      return t;
-    }
-    const int64_t r = p.rows[t];
-    *ok = r >= 0 && r < p.M;
-    return *ok ? r : 0;
-  };
+  // (a wave past N has no columns and takes the last scale row)
+  // in the constant address space: scalar loads, which no vector load waits for
+  typedef const __attribute__((address_space(4))) float* scalar_floats;
+  const scalar_floats ws = (scalar_floats)(p.ws + (static_cast<size_t>(rt.expert) * p.nb +
+                            min((n0 + wn * NT * 16) / kF8Block, p.nb - 1)) * p.kb);
+  const int b_begin = SPLIT ? static_cast<int>(blockIdx.y) * p.kb_split : 0;
+  const int b_end = SPLIT ? min(b_begin + p.kb_split, p.kb) : p.kb;
 
   // load i of this wave: rows 8 (wv LOADS + i) .. + 7 of the step's BN weight
-  // rows and BM activation rows; lane l fills position l % 8 of row l / 8
-  const uint8_t* src[LOADS];
+  // rows and BM activation rows; lane l fills position l % 8 of row l / 8.
+  // The scale load's lane takes row 64 wv + lane (rows past BM: padding of
+  // s_xs).  Rows past the tile's end are its last row again.
+  int64_t from[LOADS + 1];
   int chunk[LOADS];
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int r = 8 * (wv * LOADS + i) + (lane >> 3);
-    chunk[i] = (lane & 7) ^ swizzle(r);
-    if (r < BN) {
-      src[i] = wq + static_cast<size_t>(min(n0 + r, p.N - 1)) * p.K;
-    } else {
-      bool ok;
-      src[i] = p.xq + static_cast<size_t>(source_row(rt.begin + (r - BN), &ok)) * p.K;
+  for (int i = 0; i <= LOADS; ++i) {
+    const int r = i == LOADS ? BN + min(64 * wv + lane, BM - 1) : 8 * (wv * LOADS + i) + (lane >> 3);
+    if (i < LOADS) chunk[i] = (lane & 7) ^ swizzle(r);
+    from[i] = r < BN ? min(n0 + r, p.N - 1) : min(rt.begin + (r - BN), rt.end - 1);
+  }
+  if (p.rows) {                        // (all index loads before the first use)
+    int32_t at[LOADS + 1];
+#pragma unroll
+    for (int i = 0; i <= LOADS; ++i) {
+      const bool x = i == LOADS || 8 * (wv * LOADS + i) + (lane >> 3) >= BN;
+      at[i] = p.rows[x ? from[i] : rt.begin];
+    }
+#pragma unroll
+    for (int i = 0; i <= LOADS; ++i) {
+      const bool x = i == LOADS || 8 * (wv * LOADS + i) + (lane >> 3) >= BN;
+      if (x) from[i] = at[i];
     }
   }
-  const int tail = (p.K & (kF8Block - 1)) / 16;         // chunks of a last, partial step (0: none)
-  auto load_step = [&](int b, int buf) {
-    const int valid = (tail != 0 && b == p.kb - 1) ? tail : 8;
+  const uint8_t* src[LOADS];
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      // past the row's end: the step's first chunk again (masked out below)
-      const int c = chunk[i] < valid ? chunk[i] : 0;
-      load_lds16(src[i] + static_cast<size_t>(b) * kF8Block + 16 * c,
-                 &s_codes[buf][(wv * LOADS + i) * 8 * kF8Block]);
+  for (int i = 0; i < LOADS; ++i) {
+    const bool x = 8 * (wv * LOADS + i) + (lane >> 3) >= BN;
+    const int64_t r = x && (from[i] < 0 || from[i] >= p.M) ? 0 : from[i];
+    src[i] = (x ? p.xq : wq) + static_cast<size_t>(r) * p.K + 16 * chunk[i] +
+             static_cast<size_t>(b_begin) * kF8Block;
+  }
+  const bool xs_ok = from[LOADS] >= 0 && from[LOADS] < p.M;
+  const float* xs = p.xs + (xs_ok ? from[LOADS] : 0) * p.kb;
+  const int tail = (p.K & (kF8Block - 1)) / 16;         // chunks of a last, partial block (0: none)
+  const uint32_t codes0 = lds_address(s_mem) + wv * LOADS * 8 * kF8Block;
+  const uint32_t xs0 = lds_address(&s_xs[0][0][0]) + wv * 64 * 16;
+  auto load_step = [&](int b, int stage) {
+    const uint32_t dst = codes0 + stage * STAGE;
+    if (tail != 0 && b == p.kb - 1) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const bool x = 8 * (wv * LOADS + i) >= BN;
+        const uint8_t* past = x ? reinterpret_cast<const uint8_t*>(kZeroCodes) : src[i] - 16 * chunk[i];
+        dma16(chunk[i] < tail ? src[i] : past, dst + i * 8 * kF8Block);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        dma16(src[i], dst + i * 8 * kF8Block);
+        src[i] += kF8Block;
+      }
     }
   };
-  const float* xs_row = nullptr;
-  bool xs_ok = true;
-  if (tid < BM) xs_row = p.xs + source_row(rt.begin + tid, &xs_ok) * p.kb;
-  auto load_scale = [&](int b) -> float {
-    return tid >= BM ? 0.0f : xs_ok ? xs_row[b] : __builtin_nanf("");
+  // Scales of four K blocks q .. q + 3 at once (a row's scales lie kb apart:
+  // every lane reads a line of its own): one 16-byte load a lane, shifted back
+  // inside the row at its end, or four single ones in rows shorter than that.
+  auto xs_first = [&](int q) { return max(min(q, p.kb - 4), 0); };
+  auto load_scales = [&](int q, int half) {
+    if (p.kb >= 4) {
+      dma16(xs_ok ? xs + xs_first(q) : kNanScales, xs0 + half * (64 * NW * 16));
+    } else {
+      for (int k = 0; k < p.kb; ++k) s_xs[half][64 * wv + lane][k] = xs_ok ? xs[k] : kNanScales[k];
+    }
   };
 
-  const int wn = wv % WN, wm = wv / WN;
   const int c16 = lane & 15, g = lane >> 4;
-  // 32 bytes of row r: chunks g and g + 4 (lane group g's K positions), those
-  // from chunk `valid` on as zeros
-  auto fragment = [&](int buf, int r, int valid) -> F8Fragment<EXACT> {
-    const uint8_t* row = &s_codes[buf][r * kF8Block];
-    u32v4_t lo = *reinterpret_cast<const u32v4_t*>(row + 16 * (g ^ swizzle(r)));
-    u32v4_t hi = *reinterpret_cast<const u32v4_t*>(row + 16 * ((g + 4) ^ swizzle(r)));
-    if (valid < 8) {
-      if (g >= valid) lo = u32v4_t{0u, 0u, 0u, 0u};
-      if (g + 4 >= valid) hi = u32v4_t{0u, 0u, 0u, 0u};
-    }
-    F8Fragment<EXACT> f;
-    f.set(lo, hi);
-    return f;
-  };
-
   f32x4_t acc[NT][MT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  load_step(0, 0);
-  if (tid < BM) s_xs[0][tid] = load_scale(0);
-  __syncthreads();
-  for (int b = 0; b < p.kb; ++b) {
-    const int buf = b & 1;
-    float xs_next = 0.0f;
-    if (b + 1 < p.kb) {
-      load_step(b + 1, buf ^ 1);
-      xs_next = load_scale(b + 1);
-    }
-    const float w_scale = ws[b];
-    const int valid = (tail != 0 && b == p.kb - 1) ? tail : 8;
+  // chunks g and g + 4 (lane group g's K positions) of row 16 i + c16, whose
+  // swizzle is that of row c16
+  const int lo_at = c16 * kF8Block + 16 * (g ^ swizzle(c16));
+  const int hi_at = c16 * kF8Block + 16 * ((g + 4) ^ swizzle(c16));
+  auto compute = [&](int stage, const float* x_scale, float w_scale) {
+    const uint8_t* wrow = s_mem + stage * STAGE + wn * NT * 16 * kF8Block;
+    const uint8_t* xrow = s_mem + stage * STAGE + (BN + wm * MT * 16) * kF8Block;
     F8Fragment<EXACT> xf[MT];
     float s[MT];
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      const int r = (wm * MT + j) * 16 + c16;
-      xf[j] = fragment(buf, BN + r, valid);
-      s[j] = w_scale * s_xs[buf][r];
+      xf[j].set(*reinterpret_cast<const u32v4_t*>(xrow + lo_at + j * 16 * kF8Block),
+                *reinterpret_cast<const u32v4_t*>(xrow + hi_at + j * 16 * kF8Block));
+      s[j] = w_scale * x_scale[((wm * MT + j) * 16 + c16) * 4];
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const F8Fragment<EXACT> wf = fragment(buf, (wn * NT + i) * 16 + c16, 8);
+      F8Fragment<EXACT> wf;
+      wf.set(*reinterpret_cast<const u32v4_t*>(wrow + lo_at + i * 16 * kF8Block),
+             *reinterpret_cast<const u32v4_t*>(wrow + hi_at + i * 16 * kF8Block));
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         const f32x4_t P = mfma_f8(wf, xf[j]);
@@ -223,57 +364,502 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
         for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s[j], P[q], acc[i][j][q]);
       }
     }
-    if (b + 1 < p.kb && tid < BM) s_xs[buf ^ 1][tid] = xs_next;
-    __syncthreads();                   // the next step has landed; this buffer's readers are done
+  };
+
+  load_scales(b_begin, 0);
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k)
+    if (b_begin + k < b_end) load_step(b_begin + k, k);
+  int stage = 0, half = 0, first = xs_first(b_begin);
+  float w_scale = ws[b_begin];
+  // step b has landed (the code loads of the S - 2 steps after it may be in
+  // flight, while there are that many) and every wave has read step b - 1
+  auto arrive = [&](int b) {
+    if (b + S - 1 <= b_end) wait_loads_then_barrier<(S - 2) * LOADS>();
+    else wait_loads_then_barrier<0>();
+    if (((b - b_begin) & 3) == 0) {
+      if (b != b_begin) {
+        half ^= 1;
+        first = xs_first(b);
+      }
+      if (b + 4 < b_end) load_scales(b + 4, half ^ 1);
+    }
+  };
+  for (int b = b_begin; b < b_end; ++b) {
+    arrive(b);
+    if (b + S - 1 < b_end) load_step(b + S - 1, stage == 0 ? S - 1 : stage - 1);
+    const float w_next = ws[min(b + 1, b_end - 1)];
+    compute(stage, &s_xs[half][0][b - first], w_scale);
+    w_scale = w_next;
+    stage = stage == S - 1 ? 0 : stage + 1;
   }
 
-  const bool wide = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * Act<OUT>::bytes) == 0;
+  if constexpr (SPLIT) {
+    // planes of T rows of n_pad (a multiple of 4) columns
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int n = n0 + (wn * NT + i) * 16 + 4 * g;
-    if (n >= p.N) continue;
-    float bias[4] = {};
-    if (p.bias) {
+    for (int i = 0; i < NT; ++i) {
+      const int n = n0 + (wn * NT + i) * 16 + 4 * g;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        bias[q] = load_act<OUT>(p.bias, static_cast<size_t>(rt.expert) * p.N + min(n + q, p.N - 1));
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int64_t m = rt.begin + (wm * MT + j) * 16 + c16;
-      if (m < rt.end) {
-        float v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q] + bias[q];
-        store4<OUT>(p, m, n, v, wide);
+      for (int j = 0; j < MT; ++j) {
+        const int64_t m = rt.begin + (wm * MT + j) * 16 + c16;
+        if (m < rt.end && n < p.N)
+          *reinterpret_cast<f32x4_t*>(p.partials + (blockIdx.y * p.T + m) * p.n_pad + n) = acc[i][j];
       }
     }
+  } else {
+    wait_loads_then_barrier<0>();      // every wave has read the last stage
+    store_outputs<OUT>(p, acc, s_mem + wv * kOutBytes<OUT, NT, MT>, rt.expert, rt.begin + wm * MT * 16, rt.end,
+                       n0 + wn * NT * 16);
   }
 }
 
-template <int BN, int BM, int WN, int WM, int OUT>
-hipError_t launch_tile(LinearF8Params p, hipStream_t s) {
+// Many rows: 256 x 256 tiles, 8 waves of 128 (n) x 64 (t), the ring two
+// stages of 64 KiB.  Direct loads through buffer descriptors: a lane offset per
+// load (row and chunk) and a scalar base that moves on by 128 bytes a step, so
+// that no wave keeps 64-bit addresses; rows past N or past the tile's end lie
+// past the descriptor's end and read nothing.
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4_t buffer_of(const void* base, uint64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return i32x4_t{static_cast<int32_t>(a), static_cast<int32_t>((a >> 32) & 0xffff),
+                 static_cast<int32_t>(min(bytes, uint64_t{0xffffffff})), 0x00020000};
+}
+__device__ __forceinline__ void dma16_buffer(uint32_t voff, i32x4_t buf, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               : : "v"(voff), "s"(buf), "s"(m0) : "memory", "m0");
+}
+
+template <int OUT>
+__global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p) {
+  static_assert(OUT != ACT_F32, "fp8 MFMA sums are not fp32");
+  constexpr int BN = 256, BM = 256, WN = 2, NT = 8, MT = 4;
+  constexpr int STAGE = (BN + BM) * kF8Block;
+  constexpr int OUT_BYTES = 8 * kOutBytes<OUT, NT, MT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[2 * STAGE > OUT_BYTES ? 2 * STAGE : OUT_BYTES];
+  __shared__ __attribute__((aligned(1024))) float s_xs[2][BM][4];
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t tile_m;
+  int tile_n;
+  if (!tile_of_block<8>(count_row_tiles<BM>(p), p.tiles_n, &tile_m, &tile_n)) return;
+  const RowTile rt = find_rows<BM>(p, tile_m);
+  if (rt.expert < 0) return;
+  const int n0 = tile_n * BN;
+  const int wn = wv % WN, wm = wv / WN;
+  // the weights' scales of 64 K blocks, one a lane: a scalar load in the loop
+  // would make every wait for LDS a wait for all of it
+  const float* ws = p.ws + (static_cast<size_t>(rt.expert) * p.nb +
+                            min((n0 + wn * NT * 16) / kF8Block, p.nb - 1)) * p.kb;
+  float ws64 = ws[min(lane, p.kb - 1)];
+  const uint8_t* wbase = p.wq + (static_cast<size_t>(rt.expert) * p.N + n0) * p.K;
+  const uint8_t* xbase = p.rows ? p.xq : p.xq + static_cast<size_t>(rt.begin) * p.K;
+  const uint64_t wbytes = static_cast<uint64_t>(p.N - n0) * p.K;
+  const uint64_t xbytes = static_cast<uint64_t>(p.rows ? p.M : rt.end - rt.begin) * p.K;
+  const int last_chunks = (p.K - (p.kb - 1) * kF8Block) / 16;   // of the last block: 1 .. 8
+
+  // piece k < 4 of a step, for a wave: its weight rows 32 wv + 8 k .. + 7 and
+  // the same of its activation rows; lane l fills position l % 8 of row l / 8
+  const int sub = lane >> 3;
+  const int chunk0 = (lane & 7) ^ swizzle(sub);         // of even pieces; odd ones: ^ 4
+  const uint32_t woff = (32 * wv + sub) * p.K;
+  uint32_t xoff[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 32 * wv + 8 * k + sub;
+    int from = r;
+    if (p.rows) {
+      from = p.rows[min(rt.begin + r, rt.end - 1)];
+      if (from < 0 || from >= p.M) from = 0;
+    }
+    xoff[k] = static_cast<uint32_t>(from) * p.K;
+  }
+  const float* xs = kNanScales;        // of row 64 wv + lane; waves 0 .. 3 load them
+  bool xs_ok = false;
+  if (wv < BM / 64) {
+    int64_t from = min(rt.begin + 64 * wv + lane, rt.end - 1);
+    if (p.rows) from = p.rows[from];
+    xs_ok = from >= 0 && from < p.M;
+    if (xs_ok) xs = p.xs + from * p.kb;
+  }
+  const uint32_t codes0 = lds_address(s_mem) + wv * 32 * kF8Block;
+  const uint32_t xs0 = lds_address(&s_xs[0][0][0]) + wv * 64 * 16;
+  // (without branches, so that the loads can stand between a step's MFMAs: a
+  // step past the last one reads nothing, from a descriptor of no bytes)
+  auto load_piece = [&](int b, int k) {
+    const uint32_t dst = codes0 + (b & 1) * STAGE + k * 8 * kF8Block;
+    const uint64_t at = static_cast<uint64_t>(b) * kF8Block;
+    const bool some = b < p.kb;
+    const i32x4_t wbuf = buffer_of(wbase + at, some ? wbytes - at : 0);
+    const i32x4_t xbuf = buffer_of(xbase + at, some ? xbytes - at : 0);
+    const int chunk = k & 1 ? chunk0 ^ 4 : chunk0;
+    // past the row's end in the last block: zeros for the activations (an offset
+    // past the buffer), the block's first chunk for the weights they meet
+    const bool past = b == p.kb - 1 && chunk >= last_chunks;
+    dma16_buffer(past ? 0xfffffff0u : xoff[k] + 16 * chunk, xbuf, dst + BN * kF8Block);
+    dma16_buffer(woff + 8 * k * p.K + (past ? 0 : 16 * chunk), wbuf, dst);
+  };
+  auto xs_first = [&](int q) { return max(min(q, p.kb - 4), 0); };
+  auto load_four_scales = [&](int q, int half) {
+    if (wv < BM / 64) dma16(xs_ok ? xs + xs_first(q) : xs, xs0 + half * (BM * 16));
+  };
+
+  const int c16 = lane & 15, g = lane >> 4;
+  f32x4_t acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int lo_at = c16 * kF8Block + 16 * (g ^ swizzle(c16));
+  const int hi_at = c16 * kF8Block + 16 * ((g + 4) ^ swizzle(c16));
+  F8Fragment<false> xf[MT], wf[2];
+  f32x4_t P[MT];                       // the products of the tile before
+  float s[MT], s_last[MT];             // the scales of this step and of the one before
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    P[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    s[j] = 0.0f;
+  }
+  auto read_x = [&](int stage) {
+    const uint8_t* xrow = s_mem + stage * STAGE + (BN + wm * MT * 16) * kF8Block;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      xf[j].set(*reinterpret_cast<const u32v4_t*>(xrow + lo_at + j * 16 * kF8Block),
+                *reinterpret_cast<const u32v4_t*>(xrow + hi_at + j * 16 * kF8Block));
+  };
+  auto read_w = [&](int i, int stage) {
+    const uint8_t* wrow = s_mem + stage * STAGE + wn * NT * 16 * kF8Block;
+    wf[i & 1].set(*reinterpret_cast<const u32v4_t*>(wrow + lo_at + i * 16 * kF8Block),
+                  *reinterpret_cast<const u32v4_t*>(wrow + hi_at + i * 16 * kF8Block));
+  };
+  auto read_scales = [&](const float* x_scale, int b) {
+    const float w_scale = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws64), b & 63));
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      s_last[j] = s[j];
+      s[j] = w_scale * x_scale[((wm * MT + j) * 16 + c16) * 4];
+    }
+  };
+  // The MFMAs of column tile i, each behind the scaling of the products that it
+  // replaces (those of tile i - 1, in the shadow of the MFMA before).
+  auto tile = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int before = i == 0 ? NT - 1 : i - 1;
+      const float sj = i == 0 ? s_last[j] : s[j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[before][j][q] = fmaf(sj, P[j][q], acc[before][j][q]);
+      P[j] = mfma_f8(wf[i & 1], xf[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Column tiles 0 .. NT - 2 of step b: a tile's weights are read one tile
+  // ahead; the next step's loads go out a piece at a time (all at once they
+  // would hold up the wave that issues them).
+  auto most_tiles = [&](int b) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NT - 1; ++i) {
+      if (i < 3) load_piece(b + 1, i + 1);
+      read_w(i + 1, b & 1);
+      __builtin_amdgcn_sched_barrier(0);
+      tile(i);
+    }
+  };
+
+  // (keeps the compiler from sinking the sums below the branches that follow,
+  // which would keep every product in a register until then)
+  auto settle_sums = [&]() {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+  };
+
+  // The step's barrier stands before its last tile, whose operands are then in
+  // registers: past it the step's stage is free for the loads two steps on,
+  // the next stage has landed, and the last tile's MFMAs cover the reads of the
+  // next step's first fragments.
+  int half = 0, first = xs_first(0);
+  if (p.kb >= 4) {
+    load_four_scales(0, 0);
+  } else if (wv < BM / 64) {           // rows shorter than one 16-byte load
+    for (int k = 0; k < p.kb; ++k) s_xs[0][64 * wv + lane][k] = xs[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) load_piece(0, k);
+  wait_loads_then_barrier<0>();
+  if (p.kb > 4) load_four_scales(4, 1);
+  load_piece(1, 0);
+  read_w(0, 0);
+  read_x(0);
+  read_scales(&s_xs[0][0][0], 0);
+  for (int b = 0; b < p.kb - 1; ++b) {
+    const int nb = b + 1;
+    most_tiles(b);
+    settle_sums();
+    wait_loads_then_barrier<0>();
+    if ((nb & 3) == 0) {
+      half ^= 1;
+      first = xs_first(nb);
+      if (nb + 4 < p.kb) load_four_scales(nb + 4, half ^ 1);
+      if ((nb & 63) == 0) {
+        ws64 = ws[min(nb + lane, p.kb - 1)];
+        asm volatile("" : "+v"(ws64));                  // waited for here, not at each use
+      }
+    }
+    tile(NT - 1);
+    load_piece(nb + 1, 0);
+    read_w(0, nb & 1);
+    read_x(nb & 1);
+    read_scales(&s_xs[half][0][nb - first], nb);
+  }
+  most_tiles(p.kb - 1);
+  tile(NT - 1);
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[NT - 1][j][q] = fmaf(s[j], P[j][q], acc[NT - 1][j][q]);
+  settle_sums();
+
+  wait_loads_then_barrier<0>();        // every wave has read the last stage
+  store_outputs<OUT>(p, acc, s_mem + wv * kOutBytes<OUT, NT, MT>, rt.expert, rt.begin + wm * MT * 16, rt.end,
+                     n0 + wn * NT * 16);
+}
+
+template <int OUT>
+hipError_t launch_big(LinearF8Params p, hipStream_t s) {
+  p.tiles_n = (p.N + 255) / 256;
+  int64_t tiles_m = (p.T + 255) / 256;
+  if (p.offsets) tiles_m = p.T / 256 + (p.T < p.E ? p.T : p.E);
+  const int64_t blocks = tiles_m * p.tiles_n;
+  if (blocks > 0x7fffffff / 512) return hipErrorInvalidConfiguration;
+  linear_f8_big_kernel<OUT><<<dim3(static_cast<unsigned>(blocks)), dim3(512), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// Sum of the K splits' planes, in their order, and the bias, for the rows of the
+// call (of the experts): four columns a thread.
+template <int OUT>
+__global__ __launch_bounds__(256) void linear_f8_reduce_kernel(LinearF8Params p, int splits) {
+  int64_t lo = 0, hi = p.T;
+  if (p.offsets) {
+    lo = min(max(static_cast<int64_t>(p.offsets[0]), int64_t{0}), p.T);
+    hi = min(max(static_cast<int64_t>(p.offsets[p.E]), lo), p.T);
+  }
+  const int quads = p.n_pad / 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = id / quads;
+  if (m < lo || m >= hi) return;
+  const int n = static_cast<int>(id - m * quads) * 4;
+  f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < splits; ++k)
+    sum += *reinterpret_cast<const f32x4_t*>(p.partials + (k * p.T + m) * p.n_pad + n);
+  if (p.bias) {
+    int e = 0;                         // the last expert that begins at or before row m
+    for (int end = p.offsets ? p.E : 1; end - e > 1;) {
+      const int mid = (e + end) / 2;
+      if (p.offsets[mid] <= m) e = mid;
+      else end = mid;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sum[q] += load_act<OUT>(p.bias, static_cast<size_t>(e) * p.N + min(n + q, p.N - 1));
+  }
+  const bool wide = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * Act<OUT>::bytes) == 0;
+  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  store4<OUT>(p, m, n, v, wide);
+}
+
+// Few rows: a block computes 16 NT columns of 16 MT rows over all of K, its W
+// waves each a run of K blocks; their sums meet in LDS in a fixed order.  The
+// weights go straight from memory to the MFMA operand (a step of a row is 128
+// consecutive bytes, two 16-byte loads of four lanes each), U steps ahead.
+template <int NT, int MT, int W, int U, int OUT>
+__global__ __launch_bounds__(64 * W) void linear_f8_rows_kernel(LinearF8Params p) {
+  constexpr bool EXACT = OUT == ACT_F32;
+  __shared__ f32x4_t s_acc[W][NT][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = (blockIdx.x % p.tiles_n) * 16 * NT;
+  const RowTile rt = find_rows<16 * MT>(p, blockIdx.x / p.tiles_n);
+  if (rt.expert < 0) return;
+  const int c16 = lane & 15, g = lane >> 4;
+  const uint8_t* wrow[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    wrow[i] = p.wq + (static_cast<size_t>(rt.expert) * p.N + min(n0 + 16 * i + c16, p.N - 1)) * p.K;
+  const float* ws = p.ws + (static_cast<size_t>(rt.expert) * p.nb + n0 / kF8Block) * p.kb;
+  const uint8_t* xrow[MT];
+  const float* xs[MT];
+  bool ok[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t t = min(rt.begin + 16 * j + c16, rt.end - 1);
+    int64_t r = p.rows ? p.rows[t] : t;
+    ok[j] = r >= 0 && r < p.M;
+    r = ok[j] ? r : 0;
+    xrow[j] = p.xq + static_cast<size_t>(r) * p.K;
+    xs[j] = p.xs + r * p.kb;
+  }
+  const int tail = (p.K & (kF8Block - 1)) / 16;
+  const int per = (p.kb + W - 1) / W;
+  const int begin = wv * per, end = min(begin + per, p.kb);
+
+  struct Steps {
+    u32v4_t w[U][NT][2], x[U][MT][2];
+    float xs[U][MT], ws[U];
+  };
+  // (a step past the run loads the run's last block again, with scale 0)
+  auto load = [&](int b0, Steps& st) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = min(b0 + u, end - 1);
+      const int valid = (tail != 0 && b == p.kb - 1) ? tail : 8;
+      const size_t at = static_cast<size_t>(b) * kF8Block;
+      const int c0 = g < valid ? g : 0, c1 = g + 4 < valid ? g + 4 : 0;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        st.w[u][i][0] = *reinterpret_cast<const u32v4_t*>(wrow[i] + at + 16 * c0);
+        st.w[u][i][1] = *reinterpret_cast<const u32v4_t*>(wrow[i] + at + 16 * c1);
+      }
+      st.ws[u] = ws[b];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        st.x[u][j][0] = *reinterpret_cast<const u32v4_t*>(xrow[j] + at + 16 * c0);
+        st.x[u][j][1] = *reinterpret_cast<const u32v4_t*>(xrow[j] + at + 16 * c1);
+        st.xs[u][j] = xs[j][b];
+      }
+    }
+  };
+  f32x4_t acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  if (begin < end) {
+    Steps cur;
+    load(begin, cur);
+    for (int b0 = begin; b0 < end; b0 += U) {
+      Steps nxt;
+      if (b0 + U < end) load(b0 + U, nxt);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + u;
+        const int valid = (tail != 0 && b >= p.kb - 1) ? tail : 8;
+        F8Fragment<EXACT> wf[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) wf[i].set(cur.w[u][i][0], cur.w[u][i][1]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          u32v4_t lo = cur.x[u][j][0], hi = cur.x[u][j][1];
+          if (valid < 8) {
+            if (g >= valid) lo = u32v4_t{0u, 0u, 0u, 0u};
+            if (g + 4 >= valid) hi = u32v4_t{0u, 0u, 0u, 0u};
+          }
+          F8Fragment<EXACT> xf;
+          xf.set(lo, hi);
+          const float s = b < end ? cur.ws[u] * cur.xs[u][j] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const f32x4_t P = mfma_f8(wf[i], xf);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, P[q], acc[i][j][q]);
+          }
+        }
+      }
+      cur = nxt;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) s_acc[wv][i][j][lane] = acc[i][j];
+  __syncthreads();
+  const bool wide = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * Act<OUT>::bytes) == 0;
+#pragma unroll
+  for (int f = 0; f < NT * MT; ++f) {
+    if (f % W != wv) continue;
+    const int i = f / MT, j = f % MT;
+    const int n = n0 + 16 * i + 4 * g;
+    const int64_t m = rt.begin + 16 * j + c16;
+    if (n >= p.N || m >= rt.end) continue;
+    f32x4_t sum = s_acc[0][i][j][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += s_acc[w][i][j][lane];
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = sum[q];
+      if (p.bias) v[q] += load_act<OUT>(p.bias, static_cast<size_t>(rt.expert) * p.N + min(n + q, p.N - 1));
+      if (!ok[j]) v[q] = __builtin_nanf("");
+    }
+    store4<OUT>(p, m, n, v, wide);
+  }
+}
+
+template <int NT, int MT, int W, int U, int OUT>
+hipError_t launch_rows(LinearF8Params p, hipStream_t s) {
+  p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
+  int64_t tiles_m = (p.T + 16 * MT - 1) / (16 * MT);
+  if (p.offsets) tiles_m = p.T / (16 * MT) + (p.T < p.E ? p.T : p.E);
+  const int64_t blocks = tiles_m * p.tiles_n;
+  if (blocks > 0x7fffffff / (64 * W)) return hipErrorInvalidConfiguration;
+  linear_f8_rows_kernel<NT, MT, W, U, OUT><<<dim3(static_cast<unsigned>(blocks)), dim3(64 * W), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int BN, int BM, int WN, int WM, int S, int OUT>
+hipError_t launch_tile(LinearF8Params p, int splits, hipStream_t s) {
   p.tiles_n = (p.N + BN - 1) / BN;
   // row tiles: with experts, each adds less than one tile to T / BM
   int64_t tiles_m = (p.T + BM - 1) / BM;
   if (p.offsets) tiles_m = p.T / BM + (p.T < p.E ? p.T : p.E);
   const int64_t blocks = tiles_m * p.tiles_n;
   if (blocks > 0x7fffffff / (64 * WN * WM)) return hipErrorInvalidConfiguration;
-  linear_f8_tile_kernel<BN, BM, WN, WM, OUT>
-      <<<dim3(static_cast<unsigned>(blocks)), dim3(64 * WN * WM), 0, s>>>(p);
+  const dim3 block(64 * WN * WM);
+  if (splits <= 1) {
+    linear_f8_tile_kernel<BN, BM, WN, WM, S, false, OUT>
+        <<<dim3(static_cast<unsigned>(blocks)), block, 0, s>>>(p);
+    return hipGetLastError();
+  }
+  p.kb_split = (p.kb + splits - 1) / splits;
+  splits = (p.kb + p.kb_split - 1) / p.kb_split;
+  p.n_pad = (p.N + 3) / 4 * 4;
+  linear_f8_tile_kernel<BN, BM, WN, WM, S, true, OUT>
+      <<<dim3(static_cast<unsigned>(blocks), splits), block, 0, s>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t quads = p.T * (p.n_pad / 4);
+  linear_f8_reduce_kernel<OUT><<<dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, s>>>(p, splits);
   return hipGetLastError();
 }
 
+// One entry per output type and variant (LinearF8Plan, chosen by the host).
 template <int OUT>
-hipError_t launch_out(const LinearF8Params& p, hipStream_t s) {
-  return launch_tile<64, 64, 2, 2, OUT>(p, s);
+hipError_t launch_out(const LinearF8Params& p, const LinearF8Plan& plan, hipStream_t s) {
+  switch (plan.kind) {
+    case F8_ROWS_NT1: return launch_rows<1, 1, 8, 2, OUT>(p, s);
+    case F8_ROWS_NT2: return launch_rows<2, 1, 8, 1, OUT>(p, s);
+    case F8_ROWS_NT4: return launch_rows<4, 1, 4, 1, OUT>(p, s);
+    case F8_TILE_64X32: return launch_tile<64, 32, 4, 1, 4, OUT>(p, plan.splits, s);
+    case F8_TILE_64X64: return launch_tile<64, 64, 2, 2, 2, OUT>(p, plan.splits, s);
+    case F8_TILE_128X128: return launch_tile<128, 128, 2, 4, 2, OUT>(p, plan.splits, s);
+    default:
+      if constexpr (OUT == ACT_F32) return hipErrorInvalidValue;
+      else return launch_big<OUT>(p, s);
+  }
 }
 
-hipError_t launch_linear_f8(const LinearF8Params& p, int out, hipStream_t s) {
+hipError_t launch_linear_f8(const LinearF8Params& p, const LinearF8Plan& plan, int out, hipStream_t s) {
   switch (out) {
-    case ACT_F32: return launch_out<ACT_F32>(p, s);
-    case ACT_F16: return launch_out<ACT_F16>(p, s);
-    default: return launch_out<ACT_BF16>(p, s);
+    case ACT_F32: return launch_out<ACT_F32>(p, plan, s);
+    case ACT_F16: return launch_out<ACT_F16>(p, plan, s);
+    default: return launch_out<ACT_BF16>(p, plan, s);
   }
 }
 

@@ -560,12 +560,85 @@ lowbit_status check_q8_row(int64_t K, int unit) {
   return LOWBIT_OK;
 }
 
-// Arguments of a block-scaled e4m3 product (shared by the dense and the
-// grouped call; offsets == nullptr with E == 0 is the dense one).
+// Variant and K split of a block-scaled e4m3 product: T rows of y, E experts
+// (0: dense), rows of xq gathered from M.  Times below: us on MI355X, bf16
+// outputs, the variants forced in turn on one box (M, N, K; "64 x 8 of 64" is
+// 64 tokens to 8 of 64 experts each).
+lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64_t N, int64_t K,
+                             lowbit_dtype dtype) {
+  using namespace lowbit;
+  const int64_t cus = device_cus(), kb = f8_blocks(K);
+  const bool grouped = E > 0;
+  const int64_t used = grouped ? std::min(E, T) : 1;    // experts with rows, at most
+  const int64_t per = (T + used - 1) / used;            // rows of one, on average
+  // row tiles, with half a tile of waste an expert
+  auto tiles = [&](int64_t bn, int64_t bm) {
+    const int64_t tm = grouped ? T / bm + (used + 1) / 2 : (T + bm - 1) / bm;
+    return tm * ((N + bn - 1) / bn);
+  };
+  LinearF8Plan plan{F8_ROWS_NT1, 1};
+  auto split_to = [&](int64_t target, int64_t n, int64_t min_blocks) {
+    plan.splits = static_cast<int>(std::max<int64_t>(1, std::min({target / n, kb / min_blocks, int64_t{64}})));
+  };
+  // Up to 16 rows the weights are streamed past them.  Wider blocks load the
+  // activations once for more weights, narrower ones are more: 64 columns from
+  // two blocks a CU on (64 x 8 of 64, 1408, 2048: 38 against 42 and 50; 1,
+  // 16384, 16384, one block a CU: 67 against 50 and 46), 32 columns from 7/8
+  // of a block a CU on (8, 8192, 2048: 5.6 against 6.3 with 16; 8, 4096, 4096:
+  // 8.2 against 6.8).  Grouped rows are uneven: from 10 an expert on average
+  // too many have a second tile of 16 (16 an expert: 49 against 43 of 64 x 32).
+  if (per <= (grouped ? 10 : 16)) {
+    const int64_t units = used * ((N + 15) / 16);       // 16 x 16 tiles
+    if (units >= 4 * 2 * cus) plan.kind = F8_ROWS_NT4;
+    else if (units >= 2 * (cus * 7 / 8)) plan.kind = F8_ROWS_NT2;
+    // (16-column blocks read more activations than they can hide from 9 rows on
+    // where K is long: 16, 4096, 14336: 18.3 against 15.7 of 64 x 32 in splits)
+    if (plan.kind != F8_ROWS_NT1 || per <= 8 || kb < 64) return plan;
+  }
+  // 256 x 256 tiles where they fill the CUs evenly (8192, 14336, 4096: 456
+  // against 567 of 128 x 128; 1536, 14336, 4096, 1.3 tiles a CU: 122 against
+  // 117); their sums are those of the fp8 MFMA, and their offsets into a
+  // gathered xq 32 bits.
+  const int64_t t256 = tiles(256, 256), rounds = (t256 + cus - 1) / cus;
+  if (dtype != LOWBIT_F32 && per >= 192 && t256 * 8 >= cus * 7 && t256 * 4 >= rounds * cus * 3 &&
+      !(gather && M * K > int64_t{0xffffffff})) {
+    plan.kind = F8_TILE_256X256;
+    return plan;
+  }
+  // 128 x 128 where that many fill the CUs, splits of at least 28 K blocks
+  // counted (256, 14336, 4096: 27 against 37 of 64 x 64; 512, 4096, 4096: 23
+  // against 20; 1024 x 8 of 64, 1408, 2048: 66 against 81).
+  const int64_t t128 = tiles(128, 128);
+  if (per >= (grouped ? 64 : 129) && t128 * std::max<int64_t>(1, kb / 28) * 8 >= cus * 7) {
+    plan.kind = F8_TILE_128X128;
+    split_to(2 * cus, t128, 28);
+    return plan;
+  }
+  // Then 64 x 64, or 64 x 32 up to 32 rows (20 on average), in as many splits
+  // as give two blocks a CU and leave eight K blocks each (128, 4096, 14336:
+  // 23 in four against 57 in one).
+  if (per <= (grouped ? 20 : 32)) {
+    plan.kind = F8_TILE_64X32;
+    split_to(cus * 7 / 4, tiles(64, 32), 8);
+  } else {
+    plan.kind = F8_TILE_64X64;
+    split_to(2 * cus, tiles(64, 64), 8);
+  }
+  return plan;
+}
+
+size_t f8_partial_bytes(const lowbit::LinearF8Plan& plan, int64_t T, int64_t N) {
+  if (plan.splits <= 1) return 0;
+  return static_cast<size_t>(plan.splits) * static_cast<size_t>(T) * static_cast<size_t>((N + 3) / 4 * 4) *
+         sizeof(float);
+}
+
+// The block-scaled e4m3 product (shared by the dense and the grouped call;
+// offsets == nullptr with E == 0 is the dense one).
 lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_t* rows,
                             const int32_t* offsets, const uint8_t* wq, const float* wscale,
                             const void* bias, void* y, lowbit_dtype dtype, int64_t M, int64_t T, int64_t E,
-                            int64_t N, int64_t K, void* stream) {
+                            int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
   lowbit_status st = check_q8_row(K, 16);
   if (st != LOWBIT_OK) return st;
   if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
@@ -573,6 +646,10 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
   if (M < 0 || M > kMaxDim || T < 0 || T > kMaxDim)
     return fail(LOWBIT_ERR_INVALID_ARG, "rows M=%lld, T=%lld must be in 0..2^30", (long long)M, (long long)T);
   if (!wq || !wscale) return fail(LOWBIT_ERR_INVALID_ARG, "NULL weight pointer");
+  if (workspace == nullptr && workspace_bytes != 0)
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace_bytes > 0 with a NULL workspace");
+  if (workspace != nullptr && !aligned(workspace, 256))
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (T == 0) return LOWBIT_OK;
   if (M == 0) return fail(LOWBIT_ERR_INVALID_ARG, "M=0 rows of xq for T=%lld rows of y", (long long)T);
   if (!xq || !xscale || !y) return fail(LOWBIT_ERR_INVALID_ARG, "NULL xq, xscale or y");
@@ -599,7 +676,12 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
   p.E = static_cast<int>(E);
   p.kb = static_cast<int>(f8_blocks(K));
   p.nb = static_cast<int>(f8_blocks(N));
-  const hipError_t he = lowbit::launch_linear_f8(p, act_kind(dtype), static_cast<hipStream_t>(stream));
+  lowbit::LinearF8Plan plan = f8_plan(M, T, E, rows != nullptr, N, K, dtype);
+  if (workspace_bytes < f8_partial_bytes(plan, T, N)) plan.splits = 1;   // one block a tile over all of K
+  p.partials = static_cast<float*>(workspace);
+  const hipError_t he = lowbit::launch_linear_f8(p, plan, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (he == hipErrorInvalidConfiguration)
+    return fail(LOWBIT_ERR_INVALID_ARG, "problem too large: T=%lld N=%lld", (long long)T, (long long)N);
   if (he != hipSuccess) return hip_fail(he, "linear_f8 launch");
   return LOWBIT_OK;
 }
@@ -917,23 +999,35 @@ lowbit_status lowbit_quantize_weight_f8(const void* w, lowbit_dtype dtype, int64
   return LOWBIT_OK;
 }
 
+size_t lowbit_linear_f8_workspace_bytes(int64_t M, int64_t T, int64_t E, int64_t N, int64_t K,
+                                        lowbit_dtype dtype) {
+  if (K <= 0 || K > kQ8MaxK || K % 16 != 0 || N <= 0 || N > kMaxDim || T <= 0 || T > kMaxDim || M <= 0 ||
+      M > kMaxDim || E < 0 || E > kF8MaxExperts || !valid_dtype(dtype))
+    return 0;
+  return f8_partial_bytes(f8_plan(M, T, E, false, N, K, dtype), T, N);
+}
+
 lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uint8_t* wq,
                                const float* wscale, const void* bias, void* y, lowbit_dtype dtype,
-                               int64_t M, int64_t N, int64_t K, void* stream) {
+                               int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                               void* stream) {
   g_last_error.clear();
-  return run_linear_f8(xq, xscale, nullptr, nullptr, wq, wscale, bias, y, dtype, M, M, 0, N, K, stream);
+  return run_linear_f8(xq, xscale, nullptr, nullptr, wq, wscale, bias, y, dtype, M, M, 0, N, K, workspace,
+                       workspace_bytes, stream);
 }
 
 lowbit_status lowbit_linear_f8_grouped(const uint8_t* xq, const float* xscale, const int32_t* rows,
                                        const int32_t* offsets, const uint8_t* wq, const float* wscale,
                                        const void* bias, void* y, lowbit_dtype dtype, int64_t M, int64_t T,
-                                       int64_t E, int64_t N, int64_t K, void* stream) {
+                                       int64_t E, int64_t N, int64_t K, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
   g_last_error.clear();
   if (E <= 0 || E > kF8MaxExperts) return fail(LOWBIT_ERR_INVALID_ARG, "E=%lld not in 1..2^16", (long long)E);
   if (!offsets) return fail(LOWBIT_ERR_INVALID_ARG, "NULL offsets");
   if (!rows && M != T && T != 0)
     return fail(LOWBIT_ERR_INVALID_ARG, "without rows, xq's M=%lld must be y's T=%lld", (long long)M, (long long)T);
-  return run_linear_f8(xq, xscale, rows, offsets, wq, wscale, bias, y, dtype, M, T, E, N, K, stream);
+  return run_linear_f8(xq, xscale, rows, offsets, wq, wscale, bias, y, dtype, M, T, E, N, K, workspace,
+                       workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -36,6 +36,7 @@ EXPORTED_SYMBOLS = (
     "lowbit_status_string", "lowbit_last_error", "lowbit_linear_noalloc", "lowbit_set_tuning",
     "lowbit_quantize_act_i8", "lowbit_linear_a8", "lowbit_add_rmsnorm_q8", "lowbit_quantize_act_f8",
     "lowbit_quantize_weight_f8", "lowbit_linear_f8", "lowbit_linear_f8_grouped",
+    "lowbit_linear_f8_workspace_bytes",
 )
 ABI_VERSION = 3
 # schedule overrides (include/lowbit_tuning.h)
@@ -119,10 +120,12 @@ def load() -> ctypes.CDLL:
     lib.lowbit_quantize_weight_f8.restype = ci
     lib.lowbit_quantize_weight_f8.argtypes = [vp, ci, c_i64, c_i64, c_i64, vp, vp, vp]
     lib.lowbit_linear_f8.restype = ci
-    lib.lowbit_linear_f8.argtypes = [vp, vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64, vp]
+    lib.lowbit_linear_f8.argtypes = [vp, vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64, vp, c_sz, vp]
     lib.lowbit_linear_f8_grouped.restype = ci
     lib.lowbit_linear_f8_grouped.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64,
-                                             c_i64, c_i64, vp]
+                                             c_i64, c_i64, vp, c_sz, vp]
+    lib.lowbit_linear_f8_workspace_bytes.restype = c_sz
+    lib.lowbit_linear_f8_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64, c_i64, ci]
     if lib.lowbit_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{path} has ABI version {lib.lowbit_abi_version()}, this binding "
                            f"expects {ABI_VERSION}: rebuild it with __graft_entry__.build()")
@@ -584,6 +587,29 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     return q, qscale, h, y
 
 
+def lowbit_linear_f8_workspace_bytes(M: int, T: int, E: int, N: int, K: int, dtype: torch.dtype) -> int:
+    """Bytes lowbit_linear_f8 (T = M, E = 0) or lowbit_linear_f8_grouped can use as workspace."""
+    return load().lowbit_linear_f8_workspace_bytes(M, T, E, N, K, _DTYPE_ENUM[dtype])
+
+
+def _f8_workspace(workspace: Optional[torch.Tensor], M: int, T: int, E: int, N: int, K: int, dtype,
+                  device, stream) -> Optional[torch.Tensor]:
+    """The caller's workspace, or one made for this call on the call's stream: torch's allocator
+    reuses it there only (and keeps it for a graph that captures the call), so no two calls or
+    graphs share it."""
+    if workspace is not None:
+        return workspace
+    need = load().lowbit_linear_f8_workspace_bytes(M, T, E, N, K, _DTYPE_ENUM[dtype])
+    if need == 0:
+        return None
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
                            xscale: Optional[torch.Tensor] = None, stream=None):
     """e4m3 codes of x[M, K] and the fp32 scale of each block of 128 of a row (on the GPU).
@@ -634,7 +660,8 @@ def lowbit_quantize_weight_f8(w: torch.Tensor, wq: Optional[torch.Tensor] = None
 
 def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor,
                      bias: Optional[torch.Tensor], dtype: torch.dtype,
-                     y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                     y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
     """y[M, N] = dequant(xq, xscale) . dequant(wq, wscale)^T (+ bias) on the fp8 matrix cores:
     e4m3 codes, fp32 scales per block of 128 (activations) and 128 x 128 (weights), fp32 sums;
     y and bias in `dtype`."""
@@ -654,10 +681,14 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
         y = torch.empty((M, N), dtype=dtype, device=xq.device)
     else:
         _expect_tensor(y, "y", (M, N), dtype)
-    _require_cuda(xq, xscale, wq, wscale, bias, y)
+    if workspace is not None:
+        _expect(workspace.dtype is torch.uint8, "workspace must be uint8")
+    _require_cuda(xq, xscale, wq, wscale, bias, y, workspace)
     with torch.cuda.device(xq.device):
+        ws = _f8_workspace(workspace, M, M, 0, N, K, dtype, xq.device, stream)
         st = lib.lowbit_linear_f8(_ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(y),
-                                  _DTYPE_ENUM[dtype], M, N, K, _stream_handle(xq.device, stream))
+                                  _DTYPE_ENUM[dtype], M, N, K, _ptr(ws), 0 if ws is None else ws.numel(),
+                                  _stream_handle(xq.device, stream))
     _check(st, "lowbit_linear_f8")
     return y
 
@@ -665,7 +696,8 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
 def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: torch.Tensor,
                              wq: torch.Tensor, wscale: torch.Tensor, bias: Optional[torch.Tensor],
                              dtype: torch.dtype, rows: Optional[torch.Tensor] = None,
-                             y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                             y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
     """lowbit_linear_f8 for rows grouped by expert: row t of y, offsets[e] <= t < offsets[e + 1],
     is row t of xq (or row rows[t]) times expert e's weight wq[e] (+ bias[e]).
 
@@ -694,11 +726,15 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
         y = torch.empty((T, N), dtype=dtype, device=xq.device)
     else:
         _expect_tensor(y, "y", (T, N), dtype)
-    _require_cuda(xq, xscale, offsets, wq, wscale, bias, rows, y)
+    if workspace is not None:
+        _expect(workspace.dtype is torch.uint8, "workspace must be uint8")
+    _require_cuda(xq, xscale, offsets, wq, wscale, bias, rows, y, workspace)
     with torch.cuda.device(xq.device):
+        ws = _f8_workspace(workspace, M, T, E, N, K, dtype, xq.device, stream)
         st = lib.lowbit_linear_f8_grouped(_ptr(xq), _ptr(xscale), _ptr(rows), _ptr(offsets), _ptr(wq),
                                           _ptr(wscale), _ptr(bias), _ptr(y), _DTYPE_ENUM[dtype], M, T, E,
-                                          N, K, _stream_handle(xq.device, stream))
+                                          N, K, _ptr(ws), 0 if ws is None else ws.numel(),
+                                          _stream_handle(xq.device, stream))
     _check(st, "lowbit_linear_f8_grouped")
     return y
 

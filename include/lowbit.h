@@ -370,12 +370,29 @@ lowbit_status lowbit_quantize_weight_f8(const void* w, lowbit_dtype dtype, int64
  *   M >= 0 (0 is a no-op; at most 2^30), N > 0 (at most 2^30), K as above.
  *   xq and wq 16-byte aligned, the scales 4-byte aligned.
  *
- * Products accumulate in fp32; the bias is added in fp32 and the result
- * rounded once to dtype, nearest even.  Asynchronous and deterministic: no
- * atomics, and every output is summed in an order fixed by the shape. */
+ *   workspace/workspace_bytes: device scratch or NULL/0, at least
+ *            lowbit_linear_f8_workspace_bytes() to be used; when non-NULL it
+ *            must be 256-byte aligned.  Its contents on entry do not matter;
+ *            calls that may run at the same time must not share one.
+ *
+ * A block's 128 products are summed by the matrix core: for fp32 outputs with
+ * 24 bits kept throughout; for 16-bit outputs by the fp8 instruction, which
+ * cuts products below 2^-13 of the largest of each eight (off by at most
+ * 7 * 2^-13 of the sum of their magnitudes, about 2^-16 for random ones).  The
+ * blocks accumulate in fp32; the bias is added in fp32 and the result rounded
+ * once to dtype, nearest even.  Asynchronous and deterministic: no atomics,
+ * and every output is summed in an order fixed by the shape and by whether the
+ * workspace suffices. */
 lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uint8_t* wq,
                                const float* wscale, const void* bias, void* y, lowbit_dtype dtype,
-                               int64_t M, int64_t N, int64_t K, void* stream);
+                               int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Bytes of workspace that lowbit_linear_f8 (T = M, E = 0) or
+ * lowbit_linear_f8_grouped can use (0 when the shape's schedule needs none).
+ * With less, the call runs without a K split. */
+size_t lowbit_linear_f8_workspace_bytes(int64_t M, int64_t T, int64_t E, int64_t N, int64_t K,
+                                        lowbit_dtype dtype);
 
 /* The same product for rows grouped by expert: row t of y, with
  * offsets[e] <= t < offsets[e + 1], is computed with weight, scales and bias
@@ -395,13 +412,14 @@ lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uin
  *   bias     device, E x N elements of dtype, or NULL.
  *   y        device, T x N row-major, dtype.
  *   T >= 0 (0 is a no-op; at most 2^30), M >= 1 where T > 0, 1 <= E <= 2^16;
- *   N, K, alignment, accumulation and order as for lowbit_linear_f8.
+ *   N, K, alignment, workspace, accumulation and order as for lowbit_linear_f8.
  *
- * Asynchronous, no workspace; nothing waits for the offsets on the host. */
+ * Asynchronous; nothing waits for the offsets on the host. */
 lowbit_status lowbit_linear_f8_grouped(const uint8_t* xq, const float* xscale, const int32_t* rows,
                                        const int32_t* offsets, const uint8_t* wq, const float* wscale,
                                        const void* bias, void* y, lowbit_dtype dtype, int64_t M, int64_t T,
-                                       int64_t E, int64_t N, int64_t K, void* stream);
+                                       int64_t E, int64_t N, int64_t K, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* lowbit_status_string(lowbit_status status);

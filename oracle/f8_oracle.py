@@ -105,34 +105,38 @@ def rmsnorm(h: np.ndarray, weight: Optional[np.ndarray], eps: float) -> np.ndarr
 
 
 def linear_f8(xq: np.ndarray, xs: np.ndarray, wq: np.ndarray, ws: np.ndarray,
-              bias: Optional[np.ndarray] = None) -> Tuple[np.ndarray, np.ndarray]:
-    """(y, A) in float64 from patterns and scales; A sums the magnitudes of the products."""
-    M, K = xq.shape
-    N = wq.shape[0]
-    y, A = np.zeros((M, N)), np.zeros((M, N))
-    x, w = E4M3[xq], E4M3[wq]
-    row_block = np.arange(N) // BLOCK
+              bias: Optional[np.ndarray] = None,
+              columns: Optional[np.ndarray] = None) -> Tuple[np.ndarray, np.ndarray]:
+    """(y, A) in float64 from patterns and scales; A sums the magnitudes of the products.
+    `columns`: the weight rows to compute (all by default)."""
+    columns = np.arange(wq.shape[0]) if columns is None else columns
+    y, A = np.zeros((xq.shape[0], len(columns))), np.zeros((xq.shape[0], len(columns)))
+    x, w = E4M3[xq], E4M3[wq[columns]]
     with np.errstate(all="ignore"):
         for b in range(xs.shape[1]):
             at = np.s_[:, b * BLOCK:(b + 1) * BLOCK]
-            s = xs[:, b:b + 1].astype(np.float64) * ws[row_block, b].astype(np.float64)[None, :]
+            s = xs[:, b:b + 1].astype(np.float64) * ws[columns // BLOCK, b].astype(np.float64)[None, :]
             y += s * (x[at] @ w[at].T)
             A += np.abs(s) * (np.abs(x[at]) @ np.abs(w[at]).T)
     if bias is not None:
-        y = y + bias.astype(np.float64)
-        A = A + np.abs(bias.astype(np.float64))
+        b = bias[columns].astype(np.float64)
+        y, A = y + b, A + np.abs(b)
     return y, A
 
 
-def linear_f8_grouped(xq, xs, rows, offsets, wq, ws, bias, y0) -> Tuple[np.ndarray, np.ndarray]:
+def linear_f8_grouped(xq, xs, rows, offsets, wq, ws, bias, y0,
+                      columns: Optional[np.ndarray] = None) -> Tuple[np.ndarray, np.ndarray]:
     """(y, A): y0 with the rows of every expert replaced; rows == None reads row t for row t."""
-    y, A = y0.astype(np.float64).copy(), np.zeros(y0.shape)
+    columns = np.arange(wq.shape[1]) if columns is None else columns
+    y = y0[:, columns].astype(np.float64)
+    A = np.zeros(y.shape)
+    source = np.arange(y.shape[0]) if rows is None else rows
     for e in range(wq.shape[0]):
-        for t in range(offsets[e], offsets[e + 1]):
-            r = t if rows is None else rows[t]
-            if r < 0 or r >= xq.shape[0]:
-                y[t] = np.nan
-                continue
-            yt, At = linear_f8(xq[r:r + 1], xs[r:r + 1], wq[e], ws[e], None if bias is None else bias[e])
-            y[t], A[t] = yt[0], At[0]
+        t = np.arange(offsets[e], offsets[e + 1])
+        out = (source[t] < 0) | (source[t] >= xq.shape[0])
+        y[t[out]] = np.nan
+        t = t[~out]
+        if len(t):
+            r = source[t]
+            y[t], A[t] = linear_f8(xq[r], xs[r], wq[e], ws[e], None if bias is None else bias[e], columns)
     return y, A

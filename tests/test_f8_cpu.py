@@ -8,7 +8,7 @@ import torch
 from bit_groupwise_weight_amd import lowbit as lb
 from bit_groupwise_weight_amd import nn as lnn
 
-OK, INVALID, UNSUPPORTED, MISALIGNED = 0, 1, 2, 3
+OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 0, 1, 2, 3, 6
 F32, F16, BF16 = 0, 1, 2
 A = 0x10000          # a fake, 256-byte aligned "device" address: never dereferenced
 F8 = torch.float8_e4m3fn
@@ -71,6 +71,7 @@ LINEAR_CASES = [
     (dict(xs=None), INVALID), (dict(wq=None), INVALID), (dict(ws=None), INVALID), (dict(y=None), INVALID),
     (dict(xq=A + 8), MISALIGNED), (dict(wq=A + 8), MISALIGNED), (dict(xs=A + 2), MISALIGNED),
     (dict(ws=A + 2), MISALIGNED), (dict(y=A + 1), MISALIGNED), (dict(bias=A + 1), MISALIGNED),
+    (dict(wkb=64), WORKSPACE), (dict(wk=A + 16, wkb=64), WORKSPACE),
 ]
 
 
@@ -78,10 +79,10 @@ LINEAR_CASES = [
     (dict(M=-1), INVALID), (dict(M=(1 << 30) + 1), INVALID), (dict(M=0), OK),
     (dict(M=0, xq=None, xs=None, y=None), OK), (dict(M=0, wq=None), INVALID)])
 def test_linear_f8_validation(lowbit_lib, kw, status):
-    a = dict(xq=A, xs=A, wq=A, ws=A, bias=None, y=A, dt=BF16, M=4, N=64, K=256)
+    a = dict(xq=A, xs=A, wq=A, ws=A, bias=None, y=A, dt=BF16, M=4, N=64, K=256, wk=None, wkb=0)
     a.update(kw)
     st = lowbit_lib.lowbit_linear_f8(a["xq"], a["xs"], a["wq"], a["ws"], a["bias"], a["y"], a["dt"], a["M"],
-                                     a["N"], a["K"], None)
+                                     a["N"], a["K"], a["wk"], a["wkb"], None)
     assert st == status
     assert (lb.lowbit_last_error() == "") == (status == OK)
 
@@ -92,12 +93,29 @@ def test_linear_f8_validation(lowbit_lib, kw, status):
     (dict(rows=A + 2), MISALIGNED), (dict(off=A + 2), MISALIGNED), (dict(rows=A, M=9, dt=7), UNSUPPORTED),
     (dict(T=0, M=0), OK), (dict(T=0, M=7, rows=A), OK)])
 def test_linear_f8_grouped_validation(lowbit_lib, kw, status):
-    a = dict(xq=A, xs=A, rows=None, off=A, wq=A, ws=A, bias=None, y=A, dt=BF16, M=4, T=4, E=2, N=64, K=256)
+    a = dict(xq=A, xs=A, rows=None, off=A, wq=A, ws=A, bias=None, y=A, dt=BF16, M=4, T=4, E=2, N=64, K=256,
+             wk=None, wkb=0)
     a.update(kw)
     st = lowbit_lib.lowbit_linear_f8_grouped(a["xq"], a["xs"], a["rows"], a["off"], a["wq"], a["ws"],
                                              a["bias"], a["y"], a["dt"], a["M"], a["T"], a["E"], a["N"],
-                                             a["K"], None)
+                                             a["K"], a["wk"], a["wkb"], None)
     assert st == status
+
+
+@pytest.mark.parametrize("M, T, E, N, K, dtype, splits", [
+    (1, 1, 0, 14336, 4096, "bf16", 0),        # few rows: no workspace
+    (64, 64, 0, 4096, 14336, "bf16", 8),      # 64 tiles of 64 x 64
+    (128, 128, 0, 4096, 14336, "f32", 4),
+    (20, 20, 0, 4096, 4096, "f16", 4),        # 64 x 32, at least 8 K blocks a split
+    (8192, 8192, 0, 14336, 4096, "bf16", 0),  # 256 x 256: none
+    (64, 64, 0, 4098, 14336, "bf16", 7),      # planes padded to a multiple of 4 columns
+    (30, 60, 2, 1024, 8192, "bf16", 8),       # grouped: planes of T rows
+    (4, 0, 2, 64, 256, "bf16", 0), (4, 4, 0, 64, 40, "bf16", 0),
+])
+def test_workspace_bytes(lowbit_lib, M, T, E, N, K, dtype, splits):
+    """The schedule on a 256-CU device, seen through its fp32 planes of T x N."""
+    dt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    assert lb.lowbit_linear_f8_workspace_bytes(M, T, E, N, K, dt) == splits * T * -(-N // 4) * 4 * 4
 
 
 def test_signatures_are_declared(lowbit_lib):

@@ -330,6 +330,50 @@ def test_linear_exact(M, N, K):
     assert np.array_equal(f64(y), ref)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("M, N, K", [
+    (12, 300, 8336), (20, 300, 4096), (31, 2000, 8208), (70, 300, 8208), (128, 1030, 2064),  # K splits
+    (512, 2050, 14336), (300, 4608, 3600),                # 128 x 128 tiles, in splits and whole
+    (300, 28700, 272), (257, 28673, 16), (300, 28700, 400), (259, 28700, 8336), (512, 14336, 528),  # 256 x 256
+    (1100, 14340, 1168),
+])
+def test_linear_variants(M, N, K, dtype):
+    """Every kernel variant at ragged edges: exact inputs, every column near a tile's edge and a
+    sample of the rest; twice with the same result; a workspace that is too small changes nothing."""
+    xq, xs, wq, ws = exact_inputs(M + K, M, N, K)
+    rng = np.random.default_rng(N)
+    cols = np.unique(np.concatenate([np.arange(min(N, 20)), np.arange(max(0, N - 300), N),
+                                     rng.integers(0, N, 200)]))
+    bias = (rng.integers(-8, 9, N) * 0.5).astype(np.float32)
+    ref, A = o.linear_f8(xq, xs, wq, ws, bias, cols)
+    a = [up8(xq), up(xs), up8(wq), up(ws), up(bias).to(DT[dtype])]
+    y = lb.lowbit_linear_f8(*a, DT[dtype])
+    assert torch.equal(y, lb.lowbit_linear_f8(*a, DT[dtype]))
+    assert A.max() < 2 ** 18                   # steps of 2^-6: below 2^24 of them, exact in fp32
+    got = f64(y[:, torch.from_numpy(cols).to(DEV)])
+    want = ref if dtype == "f32" else f64(torch.from_numpy(ref).to(DT[dtype]))
+    assert np.array_equal(got, want)
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)
+    assert torch.equal(y, lb.lowbit_linear_f8(*a, DT[dtype], workspace=small))
+
+
+def test_linear_split_on_another_stream():
+    """The workspace made for a call lives on the call's stream."""
+    xq, xs, wq, ws = exact_inputs(5, 64, 4096, 8192)
+    a = [up8(xq), up(xs), up8(wq), up(ws)]
+    want = lb.lowbit_linear_f8(*a, None, torch.float32)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    ys = [torch.zeros_like(want) for _ in range(12)]
+    torch.cuda.synchronize()
+    for i, y in enumerate(ys):
+        s = streams[i % 3]
+        lb.lowbit_linear_f8(*a, None, torch.float32, y=y, stream=s if i % 2 else s.cuda_stream)
+        torch.empty(1 << 20, device=DEV).fill_(float("nan"))     # what a freed workspace might become
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in ys)
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 @pytest.mark.parametrize("K", [144, 1040])
 def test_linear_one_hot_reads_the_right_column(M, K):
@@ -467,6 +511,40 @@ def test_grouped_exact_and_equal_to_dense(counts):
     for e in range(4):
         ref, _ = o.linear_f8(xq, xs, wq[e], ws[e])
         assert np.array_equal(f64(y[off[e]:off[e + 1]]), ref[rows[off[e]:off[e + 1]]])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("counts, N, K", [
+    ([30, 0, 25], 200, 4112), ([60, 0, 70], 300, 2064),   # K splits, 64 x 32 and 64 x 64
+    ([200, 100, 0, 130], 6000, 272),                      # 128 x 128
+    ([300, 260, 0, 208], 14356, 400), ([257, 1, 600, 0, 300], 14356, 144),                  # 256 x 256
+])
+@pytest.mark.parametrize("gather", [True, False])
+def test_grouped_variants(counts, N, K, dtype, gather):
+    rng = np.random.default_rng(N + K)
+    E, first, behind = len(counts), 3, 9
+    off = (first + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)
+    T = int(off[-1]) + behind
+    M = 41 if gather else T
+    xq, xs, wq, ws = exact_inputs(K, M, N, K, E=E)
+    rows = rng.integers(0, M, T).astype(np.int32) if gather else None
+    if gather:
+        rows[[first, T - behind - 1]] = [-3, M]
+    bias = (rng.integers(-8, 9, (E, N)) * 0.5).astype(np.float32)
+    y0 = torch.full((T, N), 3.0, dtype=DT[dtype], device=DEV)
+    a = [up8(xq), up(xs), up(off), up8(wq), up(ws), up(bias).to(DT[dtype]), DT[dtype]]
+    r = up(rows) if gather else None
+    y = lb.lowbit_linear_f8_grouped(*a, rows=r, y=y0.clone())
+    cols = np.unique(np.concatenate([np.arange(min(N, 10)), np.arange(max(0, N - 280), N),
+                                     rng.integers(0, N, 100)]))
+    ref, A = o.linear_f8_grouped(xq, xs, rows, off, wq, ws, bias, f64(y0), cols)
+    assert A.max() < 2 ** 18
+    want = ref if dtype == "f32" else f64(torch.from_numpy(ref).to(DT[dtype]))
+    assert np.array_equal(f64(y[:, torch.from_numpy(cols).to(DEV)]), want, equal_nan=True)
+    assert (y[:first] == 3.0).all() and (y[T - behind:] == 3.0).all()
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)
+    z = lb.lowbit_linear_f8_grouped(*a, rows=r, y=y0.clone(), workspace=small)
+    assert torch.equal(y.nan_to_num(9.0), z.nan_to_num(9.0))
 
 
 def test_grouped_rows_out_of_range_are_nan():
