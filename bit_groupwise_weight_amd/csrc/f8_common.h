@@ -106,6 +106,15 @@ __device__ __forceinline__ uint32_t pack4_i8(float a, float b, float c, float d)
   return code(a) | (code(b) << 8) | (code(c) << 16) | (code(d) << 24);
 }
 
+// Two fp32 values -> two values of a 16-bit type, nearest even, in one word.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {lo, hi};
+  if constexpr (OUT == ACT_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf162_t));
+}
+
 // Eight consecutive values of a row (chunk c) as fp32, exact for every type.
 template <int ACT>
 __device__ __forceinline__ void load8(const void* row, int64_t c, float (&v)[8]) {
@@ -144,10 +153,9 @@ __device__ __forceinline__ void store8(void* row, int64_t c, float (&v)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = float_to_act_bits<ACT>(v[2 * i]), hi = float_to_act_bits<ACT>(v[2 * i + 1]);
-      w[i] = lo | (hi << 16);
-      v[2 * i] = act_bits_to_float<ACT>(lo);
-      v[2 * i + 1] = act_bits_to_float<ACT>(hi);
+      w[i] = pack2<ACT>(v[2 * i], v[2 * i + 1]);
+      v[2 * i] = act_bits_to_float<ACT>(w[i] & 0xffffu);
+      v[2 * i + 1] = act_bits_to_float<ACT>(w[i] >> 16);
     }
     dst[c] = u32v4_t{w[0], w[1], w[2], w[3]};
   }

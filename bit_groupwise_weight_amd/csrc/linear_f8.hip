@@ -156,15 +156,6 @@ __device__ __forceinline__ void store4(const LinearF8Params& p, int64_t m, int n
 
 }  // namespace
 
-// Two fp32 values -> two values of a 16-bit type, nearest even, in one word.
-template <int OUT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const f32x2 v = {lo, hi};
-  if constexpr (OUT == ACT_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
-  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf162_t));
-}
-
 // A wave's outputs (NT x MT tiles, rows m0 .., columns n0 ..) rounded and
 // turned through LDS, so that they leave as whole 16-byte pieces of y's rows
 // from a short loop (unrolled stores of the accumulators with their edge cases

@@ -32,52 +32,68 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   return v;
 }
 
-constexpr int kNormThreads = 256;
-
-// Sum over the block's threads (every thread gets it), in one fixed order.
-__device__ __forceinline__ float block_sum(float v, float* lds) {
+// Sum and maximum over the T threads of a row (every thread gets them), in one
+// fixed order; lds: T / 64 words that nothing else uses in the kernel.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
   v = wave_sum(v);
-  __syncthreads();                     // the array's last readers are done
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kNormThreads / 64; ++w) s += lds[w];
-  return s;
+    for (int w = 0; w < T / 64; ++w) v += lds[w];
+  }
+  return v;
 }
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* lds) {
+template <int T>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* lds) {
   v = lanes_max<64>(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  uint32_t m = 0;
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
 #pragma unroll
-  for (int w = 0; w < kNormThreads / 64; ++w) m = max(m, lds[w]);
-  return m;
+    for (int w = 0; w < T / 64; ++w) v = max(v, lds[w]);
+  }
+  return v;
+}
+
+// Eight codes of the values v / scale.
+template <int FMT>
+__device__ __forceinline__ u32v2_t codes8(const float (&v)[8], const SpanScale& s) {
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = s.finite ? v[i] * s.factor : 0.0f;
+  if constexpr (FMT == Q8_I8) return u32v2_t{pack4_i8(t[0], t[1], t[2], t[3]), pack4_i8(t[4], t[5], t[6], t[7])};
+  else return u32v2_t{pack4_e4m3(t[0], t[1], t[2], t[3]), pack4_e4m3(t[4], t[5], t[6], t[7])};
 }
 
 }  // namespace
 
-// One block per row; each thread takes 8-value chunks tid, tid + 256, ...;
-// the chunks are read again (from cache) once the row's sum is known.  The 16
-// lanes of an aligned group hold the 16 chunks of one block of 128.
-template <int ACT, int FMT>
-__global__ __launch_bounds__(kNormThreads) void norm_q8_kernel(NormQ8Params p) {
-  __shared__ float s_sum[kNormThreads / 64];
-  __shared__ uint32_t s_max[kNormThreads / 64];
-  const int64_t m = blockIdx.x;
-  const int tid = threadIdx.x;
+// T threads a row, each with the 8-value chunks tid, tid + T, ... of it in
+// registers (C of them; C == 0: any number, read again from cache for each
+// use).  The 16 lanes of an aligned group hold the chunks of one block of 128.
+// Rows of one wave go four to a block.
+template <int ACT, int FMT, int T, int C>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_q8_kernel(NormQ8Params p) {
+  __shared__ float s_sum[2][T / 64];
+  __shared__ uint32_t s_max[2][T / 64];
+  const int64_t m = T == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (T == 64 && m >= p.M) return;     // (no barrier in that form)
+  const int tid = threadIdx.x & (T - 1);
   const int chunks = p.K / 8;
+  const int n = C ? C : (chunks + T - 1) / T;           // chunks of a thread, past the row's end included
   const size_t row_bytes = static_cast<size_t>(p.K) * Act<ACT>::bytes;
   const char* x = static_cast<const char*>(p.x) + m * row_bytes;
   const char* r = p.residual ? static_cast<const char*>(p.residual) + m * row_bytes : nullptr;
   char* sum = p.sum ? static_cast<char*>(p.sum) + m * row_bytes : nullptr;
-  const char* h_row = sum ? sum : x;   // a thread reads back what it wrote itself
+  char* y = p.y ? static_cast<char*>(p.y) + m * row_bytes : nullptr;
+  float kept[C ? C : 1][8];
 
-  float ss = 0.0f;
-  uint32_t top = 0;
-  for (int c = tid; c < chunks; c += kNormThreads) {
-    float v[8];
+  // h of chunk c: made and written once, then kept or read back (a thread reads
+  // what it wrote itself)
+  auto make_h = [&](int c, float (&v)[8]) {
     load8<ACT>(x, c, v);
     if (r) {
       float w[8];
@@ -86,115 +102,157 @@ __global__ __launch_bounds__(kNormThreads) void norm_q8_kernel(NormQ8Params p) {
       for (int i = 0; i < 8; ++i) v[i] += w[i];
       store8<ACT>(sum, c, v);
     }
+  };
+  float ss = 0.0f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < (C ? C : n); ++k) {
+    float (&v)[8] = kept[C ? k : 0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (tid + k * T < chunks) make_h(tid + k * T, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       ss = fmaf(v[i], v[i], ss);
       top = max(top, magnitude_bits(v[i]));
     }
   }
-  ss = block_sum(ss, s_sum);
+  auto h_of = [&](int k, float (&v)[8]) {
+    if constexpr (C != 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = kept[k][i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      if (tid + k * T < chunks) load8<ACT>(sum ? sum : x, tid + k * T, v);
+    }
+  };
+  ss = row_sum<T>(ss, s_sum[0]);
   float inv = 1.0f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
-  if (!(ss < __builtin_inff())) {      // the same for every thread of the block
-    if (block_max(top, s_max) >= 0x7f800000u) {
+  if (!(ss < __builtin_inff())) {      // the same for every thread of the row
+    if (row_max<T>(top, s_max[0]) >= 0x7f800000u) {
       inv = __builtin_nanf("");
     } else {
       float s2 = 0.0f;
-      for (int c = tid; c < chunks; c += kNormThreads) {
+#pragma unroll
+      for (int k = 0; k < (C ? C : n); ++k) {
         float v[8];
-        load8<ACT>(h_row, c, v);
+        h_of(k, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s2 = fmaf(v[i] * 0x1p-96f, v[i] * 0x1p-96f, s2);
       }
-      s2 = block_sum(s2, s_sum);
-      inv = 0x1p-96f / sqrtf(s2 / static_cast<float>(p.K));
+      inv = 0x1p-96f / sqrtf(row_sum<T>(s2, s_sum[1]) / static_cast<float>(p.K));
     }
   }
 
-  auto normed = [&](int c, float (&v)[8]) {
-    load8<ACT>(h_row, c, v);
+  auto normed = [&](int k, float (&v)[8]) {
+    h_of(k, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inv;
-    if (p.weight) {
+    const int c = tid + k * T;
+    if (p.weight && c < chunks) {
       float g[8];
       load8<ACT>(p.weight, c, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= g[i];
     }
   };
-  auto write_y = [&](int c, const float (&v)[8]) {
-    if (p.y) {
-      float t[8];
+  auto top_of = [&](const float (&v)[8]) {
+    uint32_t a = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = v[i];
-      store8<ACT>(static_cast<char*>(p.y) + m * row_bytes, c, t);
-    }
+    for (int i = 0; i < 8; ++i) a = max(a, magnitude_bits(v[i]));
+    return a;
+  };
+  auto write_y = [&](int c, const float (&v)[8]) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i];
+    store8<ACT>(y, c, t);
   };
   uint8_t* q = static_cast<uint8_t*>(p.q) + m * p.K;
   if constexpr (FMT == Q8_I8) {
     uint32_t amax = 0;
-    for (int c = tid; c < chunks; c += kNormThreads) {
-      float v[8];
-      normed(c, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max(amax, magnitude_bits(v[i]));
+    for (int k = 0; k < (C ? C : n); ++k) {
+      float v[8];
+      normed(k, v);
+      // (lanes past the row hold 0 * inv: a NaN where the whole row is one)
+      amax = max(amax, top_of(v));
+      if constexpr (C != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kept[k][i] = v[i];
+      }
     }
-    amax = block_max(amax, s_max);
-    const SpanScale s = span_scale(amax, kI8Max);
+    const SpanScale s = span_scale(row_max<T>(amax, s_max[1]), kI8Max);
     if (tid == 0) p.qscale[m] = s.scale;
-    for (int c = tid; c < chunks; c += kNormThreads) {
-      float v[8];
-      normed(c, v);
-      write_y(c, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = s.finite ? v[i] * s.factor : 0.0f;
-      *reinterpret_cast<u32v2_t*>(q + 8 * c) =
-          u32v2_t{pack4_i8(v[0], v[1], v[2], v[3]), pack4_i8(v[4], v[5], v[6], v[7])};
+    for (int k = 0; k < (C ? C : n); ++k) {
+      const int c = tid + k * T;
+      float v[8];
+      if constexpr (C != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = kept[k][i];
+      } else {
+        normed(k, v);
+      }
+      if (c < chunks) {
+        if (y) write_y(c, v);
+        *reinterpret_cast<u32v2_t*>(q + 8 * c) = codes8<Q8_I8>(v, s);
+      }
     }
   } else {
     const int kb = (p.K + kF8Block - 1) / kF8Block;
-    // whole groups of 16 lanes run each round; the last one's lanes past the
-    // row take no part in its maximum
-    for (int c0 = tid & ~15; c0 < chunks; c0 += kNormThreads) {
-      const int c = c0 + (tid & 15);
-      float v[8] = {};
-      uint32_t amax = 0;
-      if (c < chunks) {
-        normed(c, v);
-        write_y(c, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, magnitude_bits(v[i]));
-      }
+    for (int k = 0; k < (C ? C : n); ++k) {
+      const int c = tid + k * T;
+      float v[8];
+      normed(k, v);
+      if (y && c < chunks) write_y(c, v);
       if constexpr (FMT == Q8_F8) {
-        amax = lanes_max<16>(amax);
-        const SpanScale s = span_scale(amax, kE4m3Max);
-        if ((tid & 15) == 0) p.qscale[m * kb + (c0 >> 4)] = s.scale;
-        if (c < chunks) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = s.finite ? v[i] * s.factor : 0.0f;
-          *reinterpret_cast<u32v2_t*>(q + 8 * c) =
-              u32v2_t{pack4_e4m3(v[0], v[1], v[2], v[3]), pack4_e4m3(v[4], v[5], v[6], v[7])};
-        }
+        // (lanes past the row's end take no part in the maximum of its last block)
+        const SpanScale s = span_scale(lanes_max<16>(c < chunks ? top_of(v) : 0u), kE4m3Max);
+        if ((tid & 15) == 0 && c < chunks) p.qscale[m * kb + (c >> 4)] = s.scale;
+        if (c < chunks) *reinterpret_cast<u32v2_t*>(q + 8 * c) = codes8<Q8_F8>(v, s);
       }
     }
   }
 }
 
-template <int ACT>
-hipError_t launch_norm(const NormQ8Params& p, int fmt, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.M)), block(kNormThreads);
-  switch (fmt) {
-    case Q8_NONE: norm_q8_kernel<ACT, Q8_NONE><<<grid, block, 0, s>>>(p); break;
-    case Q8_I8: norm_q8_kernel<ACT, Q8_I8><<<grid, block, 0, s>>>(p); break;
-    default: norm_q8_kernel<ACT, Q8_F8><<<grid, block, 0, s>>>(p); break;
-  }
+template <int ACT, int FMT, int T, int C>
+hipError_t launch_norm_rows(const NormQ8Params& p, hipStream_t s) {
+  const int64_t blocks = T == 64 ? (p.M + 3) / 4 : p.M;
+  norm_q8_kernel<ACT, FMT, T, C><<<dim3(static_cast<unsigned>(blocks)), dim3(T < 256 ? 256 : T), 0, s>>>(p);
   return hipGetLastError();
+}
+
+// The threads of a row by its length alone, so that a row's result does not
+// depend on how many there are.
+template <int ACT, int FMT>
+hipError_t launch_norm(const NormQ8Params& p, hipStream_t s) {
+  if (p.K <= 512) return launch_norm_rows<ACT, FMT, 64, 1>(p, s);
+  if (p.K <= 1024) return launch_norm_rows<ACT, FMT, 64, 2>(p, s);
+  if (p.K <= 2048) return launch_norm_rows<ACT, FMT, 256, 1>(p, s);
+  if (p.K <= 4096) return launch_norm_rows<ACT, FMT, 512, 1>(p, s);
+  if (p.K <= 8192) return launch_norm_rows<ACT, FMT, 1024, 1>(p, s);
+  if (p.K <= 16384) return launch_norm_rows<ACT, FMT, 1024, 2>(p, s);
+  if (p.K <= 32768) return launch_norm_rows<ACT, FMT, 1024, 4>(p, s);
+  return launch_norm_rows<ACT, FMT, 1024, 0>(p, s);
+}
+
+template <int ACT>
+hipError_t launch_norm_fmt(const NormQ8Params& p, int fmt, hipStream_t s) {
+  switch (fmt) {
+    case Q8_NONE: return launch_norm<ACT, Q8_NONE>(p, s);
+    case Q8_I8: return launch_norm<ACT, Q8_I8>(p, s);
+    default: return launch_norm<ACT, Q8_F8>(p, s);
+  }
 }
 
 hipError_t launch_norm_q8(const NormQ8Params& p, int act, int fmt, hipStream_t s) {
   switch (act) {
-    case ACT_F32: return launch_norm<ACT_F32>(p, fmt, s);
-    case ACT_F16: return launch_norm<ACT_F16>(p, fmt, s);
-    default: return launch_norm<ACT_BF16>(p, fmt, s);
+    case ACT_F32: return launch_norm_fmt<ACT_F32>(p, fmt, s);
+    case ACT_F16: return launch_norm_fmt<ACT_F16>(p, fmt, s);
+    default: return launch_norm_fmt<ACT_BF16>(p, fmt, s);
   }
 }
 
@@ -264,7 +322,7 @@ __global__ __launch_bounds__(256) void weight_quant_f8_kernel(WeightQuantF8Param
       for (int j = 0; j < 8; ++j) amax = max(amax, magnitude_bits(v[i][j]));
     }
   }
-  amax = block_max(amax, s_max);
+  amax = row_max<256>(amax, s_max);
   const SpanScale s = span_scale(amax, kE4m3Max);
   if (threadIdx.x == 0) p.wscale[blk] = s.scale;
 #pragma unroll

@@ -522,6 +522,51 @@ def lowbit_linear_a8(xq: torch.Tensor, ascale: torch.Tensor, packed: torch.Tenso
 
 _F8 = torch.float8_e4m3fn
 
+# Eager calls of the 8-bit path: (address, marshalling function) of an entry
+# point in the compiled module, or (None, ctypes function) without it.
+_entries = {}
+
+
+def _entry(name: str):
+    e = _entries.get(name)
+    if e is None:
+        lib = load()
+        fn = getattr(lib, name)
+        fc = getattr(_fastcall_module(), name, None)
+        e = (None, fn) if fc is None else (ctypes.cast(fn, ctypes.c_void_p).value, fc)
+        _entries[name] = e
+    return e
+
+
+def _call_on(device_index: int, name: str, *args) -> int:
+    """Call an entry point with its device current; pointers as ints or None."""
+    address, fn = _entry(name)
+    if torch.cuda.current_device() != device_index:
+        with torch.cuda.device(device_index):
+            return fn(*args) if address is None else fn(address, *args)
+    return fn(*args) if address is None else fn(address, *args)
+
+
+def _placed(x: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """Index of the one GPU that all the tensors live on, contiguous; raises otherwise."""
+    if not x.is_cuda:
+        _require_cuda(x)
+    dev = x.get_device()
+    if not x.is_contiguous():
+        _require_cuda(x)
+    for t in others:
+        if t is not None and (not t.is_cuda or t.get_device() != dev or not t.is_contiguous()):
+            _require_cuda(x, *others)
+    return dev
+
+
+def _stream_of(device_index: int, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if _raw_stream is not None:
+        return _raw_stream(device_index)
+    return torch.cuda.current_stream(device_index).cuda_stream
+
 
 def _f8_blocks(n: int) -> int:
     return -(-n // F8_BLOCK)
@@ -546,11 +591,13 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     y (x's dtype) is None unless `want_y`, `y` or Q8_NONE asks for it.  `h` may be the residual
     (or x) itself: the residual stream is then updated in place.
     """
-    lib = load()
-    _expect(x.dim() == 2, "x must be 2-D [M, K]")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
     dt = x.dtype
-    _expect(dt in _DTYPE_ENUM, f"x dtype {dt} is not float32, float16 or bfloat16")
-    _expect(fmt in (Q8_NONE, Q8_I8, Q8_F8), f"fmt must be Q8_NONE, Q8_I8 or Q8_F8, got {fmt}")
+    if dt not in _DTYPE_ENUM:
+        raise ValueError(f"x dtype {dt} is not float32, float16 or bfloat16")
+    if fmt not in (Q8_NONE, Q8_I8, Q8_F8):
+        raise ValueError(f"fmt must be Q8_NONE, Q8_I8 or Q8_F8, got {fmt}")
     M, K = x.shape
     if weight is not None:
         _expect_tensor(weight, "weight", (K,), dt)
@@ -578,12 +625,11 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
         _expect_tensor(y, "y", (M, K), dt)
     elif want_y or fmt == Q8_NONE:
         y = torch.empty((M, K), dtype=dt, device=x.device)
-    _require_cuda(x, weight, residual, q, qscale, h, y)
-    with torch.cuda.device(x.device):
-        st = lib.lowbit_add_rmsnorm_q8(_ptr(x), _ptr(residual), _ptr(weight), eps, _DTYPE_ENUM[dt], M, K,
-                                       fmt, _ptr(q), _ptr(qscale), _ptr(h), _ptr(y),
-                                       _stream_handle(x.device, stream))
-    _check(st, "lowbit_add_rmsnorm_q8")
+    dev = _placed(x, weight, residual, q, qscale, h, y)
+    st = _call_on(dev, "lowbit_add_rmsnorm_q8", _ptr(x), _ptr(residual), _ptr(weight), eps, _DTYPE_ENUM[dt], M,
+                  K, fmt, _ptr(q), _ptr(qscale), _ptr(h), _ptr(y), _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_add_rmsnorm_q8")
     return q, qscale, h, y
 
 
@@ -592,22 +638,20 @@ def lowbit_linear_f8_workspace_bytes(M: int, T: int, E: int, N: int, K: int, dty
     return load().lowbit_linear_f8_workspace_bytes(M, T, E, N, K, _DTYPE_ENUM[dtype])
 
 
-def _f8_workspace(workspace: Optional[torch.Tensor], M: int, T: int, E: int, N: int, K: int, dtype,
-                  device, stream) -> Optional[torch.Tensor]:
-    """The caller's workspace, or one made for this call on the call's stream: torch's allocator
-    reuses it there only (and keeps it for a graph that captures the call), so no two calls or
-    graphs share it."""
-    if workspace is not None:
-        return workspace
-    need = load().lowbit_linear_f8_workspace_bytes(M, T, E, N, K, _DTYPE_ENUM[dtype])
+def _f8_workspace(dev: int, M: int, T: int, E: int, N: int, K: int, act: int,
+                  stream) -> Optional[torch.Tensor]:
+    """A workspace made for one call, on the call's stream: torch's allocator reuses it there only
+    (and keeps it for a graph that captures the call), so no two calls or graphs share it."""
+    address, fn = _entry("lowbit_linear_f8_workspace_bytes")
+    need = fn(M, T, E, N, K, act) if address is None else fn(address, M, T, E, N, K, act)
     if need == 0:
         return None
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=dev)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
 def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
@@ -615,9 +659,10 @@ def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
     """e4m3 codes of x[M, K] and the fp32 scale of each block of 128 of a row (on the GPU).
 
     Returns (xq float8_e4m3fn [M, K], xscale float32 [M, ceil(K/128)])."""
-    lib = load()
-    _expect(x.dim() == 2, "x must be 2-D [M, K]")
-    _expect(x.dtype in _DTYPE_ENUM, f"x dtype {x.dtype} is not float32, float16 or bfloat16")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    if x.dtype not in _DTYPE_ENUM:
+        raise ValueError(f"x dtype {x.dtype} is not float32, float16 or bfloat16")
     M, K = x.shape
     if xq is None:
         xq = torch.empty((M, K), dtype=_F8, device=x.device)
@@ -625,11 +670,11 @@ def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
         xscale = torch.empty((M, _f8_blocks(K)), dtype=torch.float32, device=x.device)
     _expect_tensor(xq, "xq", (M, K), _F8)
     _expect_tensor(xscale, "xscale", (M, _f8_blocks(K)), torch.float32)
-    _require_cuda(x, xq, xscale)
-    with torch.cuda.device(x.device):
-        st = lib.lowbit_quantize_act_f8(_ptr(x), _DTYPE_ENUM[x.dtype], M, K, _ptr(xq), _ptr(xscale),
-                                        _stream_handle(x.device, stream))
-    _check(st, "lowbit_quantize_act_f8")
+    dev = _placed(x, xq, xscale)
+    st = _call_on(dev, "lowbit_quantize_act_f8", _ptr(x), _DTYPE_ENUM[x.dtype], M, K, _ptr(xq), _ptr(xscale),
+                  _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_quantize_act_f8")
     return xq, xscale
 
 
@@ -665,9 +710,10 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
     """y[M, N] = dequant(xq, xscale) . dequant(wq, wscale)^T (+ bias) on the fp8 matrix cores:
     e4m3 codes, fp32 scales per block of 128 (activations) and 128 x 128 (weights), fp32 sums;
     y and bias in `dtype`."""
-    lib = load()
-    _expect(xq.dim() == 2 and wq.dim() == 2, "xq must be [M, K] and wq [N, K]")
-    _expect(dtype in _DTYPE_ENUM, f"dtype {dtype} is not float32, float16 or bfloat16")
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("xq must be [M, K] and wq [N, K]")
+    if dtype not in _DTYPE_ENUM:
+        raise ValueError(f"dtype {dtype} is not float32, float16 or bfloat16")
     M, K = xq.shape
     N = wq.shape[0]
     kb = _f8_blocks(K)
@@ -681,15 +727,17 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
         y = torch.empty((M, N), dtype=dtype, device=xq.device)
     else:
         _expect_tensor(y, "y", (M, N), dtype)
-    if workspace is not None:
-        _expect(workspace.dtype is torch.uint8, "workspace must be uint8")
-    _require_cuda(xq, xscale, wq, wscale, bias, y, workspace)
-    with torch.cuda.device(xq.device):
-        ws = _f8_workspace(workspace, M, M, 0, N, K, dtype, xq.device, stream)
-        st = lib.lowbit_linear_f8(_ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(y),
-                                  _DTYPE_ENUM[dtype], M, N, K, _ptr(ws), 0 if ws is None else ws.numel(),
-                                  _stream_handle(xq.device, stream))
-    _check(st, "lowbit_linear_f8")
+    if workspace is not None and workspace.dtype is not torch.uint8:
+        raise ValueError("workspace must be uint8")
+    dev = _placed(xq, xscale, wq, wscale, bias, y, workspace)
+    act = _DTYPE_ENUM[dtype]
+    if workspace is None:
+        workspace = _f8_workspace(dev, M, M, 0, N, K, act, stream)
+    st = _call_on(dev, "lowbit_linear_f8", _ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(y),
+                  act, M, N, K, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                  _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_linear_f8")
     return y
 
 
@@ -704,9 +752,10 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
     offsets: int32 [E + 1] on the GPU, not decreasing, within 0..T.  rows: int32 [T], or None
     (T = M).  Rows of y outside offsets[0] .. offsets[E] are left as they are (a y made here
     starts out undefined there); an index outside xq makes its row NaN."""
-    lib = load()
-    _expect(xq.dim() == 2 and wq.dim() == 3, "xq must be [M, K] and wq [E, N, K]")
-    _expect(dtype in _DTYPE_ENUM, f"dtype {dtype} is not float32, float16 or bfloat16")
+    if xq.dim() != 2 or wq.dim() != 3:
+        raise ValueError("xq must be [M, K] and wq [E, N, K]")
+    if dtype not in _DTYPE_ENUM:
+        raise ValueError(f"dtype {dtype} is not float32, float16 or bfloat16")
     M, K = xq.shape
     E, N = wq.shape[:2]
     kb = _f8_blocks(K)
@@ -726,16 +775,17 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
         y = torch.empty((T, N), dtype=dtype, device=xq.device)
     else:
         _expect_tensor(y, "y", (T, N), dtype)
-    if workspace is not None:
-        _expect(workspace.dtype is torch.uint8, "workspace must be uint8")
-    _require_cuda(xq, xscale, offsets, wq, wscale, bias, rows, y, workspace)
-    with torch.cuda.device(xq.device):
-        ws = _f8_workspace(workspace, M, T, E, N, K, dtype, xq.device, stream)
-        st = lib.lowbit_linear_f8_grouped(_ptr(xq), _ptr(xscale), _ptr(rows), _ptr(offsets), _ptr(wq),
-                                          _ptr(wscale), _ptr(bias), _ptr(y), _DTYPE_ENUM[dtype], M, T, E,
-                                          N, K, _ptr(ws), 0 if ws is None else ws.numel(),
-                                          _stream_handle(xq.device, stream))
-    _check(st, "lowbit_linear_f8_grouped")
+    if workspace is not None and workspace.dtype is not torch.uint8:
+        raise ValueError("workspace must be uint8")
+    dev = _placed(xq, xscale, offsets, wq, wscale, bias, rows, y, workspace)
+    act = _DTYPE_ENUM[dtype]
+    if workspace is None:
+        workspace = _f8_workspace(dev, M, T, E, N, K, act, stream)
+    st = _call_on(dev, "lowbit_linear_f8_grouped", _ptr(xq), _ptr(xscale), _ptr(rows), _ptr(offsets), _ptr(wq),
+                  _ptr(wscale), _ptr(bias), _ptr(y), act, M, T, E, N, K, _ptr(workspace),
+                  0 if workspace is None else workspace.numel(), _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_linear_f8_grouped")
     return y
 
 
