@@ -284,8 +284,7 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   for (int i = 0; i < LOADS; ++i) {
     const bool x = 8 * (wv * LOADS + i) + (lane >> 3) >= BN;
     const int64_t r = x && (from[i] < 0 || from[i] >= p.M) ? 0 : from[i];
-    src[i] = (x ? p.xq : wq) + static_cast<size_t>(r) * p.K + 16 * chunk[i] +
-             static_cast<size_t>(b_begin) * kF8Block;
+    src[i] = (x ? p.xq : wq) + static_cast<size_t>(r) * p.K + 16 * chunk[i];
   }
   const bool xs_ok = from[LOADS] >= 0 && from[LOADS] < p.M;
   const float* xs = p.xs + (xs_ok ? from[LOADS] : 0) * p.kb;
@@ -294,31 +293,25 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   const uint32_t xs0 = lds_address(&s_xs[0][0][0]) + wv * 64 * 16;
   auto load_step = [&](int b, int stage) {
     const uint32_t dst = codes0 + stage * STAGE;
+    const size_t at = static_cast<size_t>(b) * kF8Block;
     if (tail != 0 && b == p.kb - 1) {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
         const bool x = 8 * (wv * LOADS + i) >= BN;
-        const uint8_t* past = x ? reinterpret_cast<const uint8_t*>(kZeroCodes) : src[i] - 16 * chunk[i];
-        dma16(chunk[i] < tail ? src[i] : past, dst + i * 8 * kF8Block);
+        const uint8_t* past = x ? reinterpret_cast<const uint8_t*>(kZeroCodes) : src[i] + at - 16 * chunk[i];
+        dma16(chunk[i] < tail ? src[i] + at : past, dst + i * 8 * kF8Block);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        dma16(src[i], dst + i * 8 * kF8Block);
-        src[i] += kF8Block;
-      }
+      for (int i = 0; i < LOADS; ++i) dma16(src[i] + at, dst + i * 8 * kF8Block);
     }
   };
   // Scales of four K blocks q .. q + 3 at once (a row's scales lie kb apart:
   // every lane reads a line of its own): one 16-byte load a lane, shifted back
-  // inside the row at its end, or four single ones in rows shorter than that.
+  // inside the row at its end.
   auto xs_first = [&](int q) { return max(min(q, p.kb - 4), 0); };
   auto load_scales = [&](int q, int half) {
-    if (p.kb >= 4) {
-      dma16(xs_ok ? xs + xs_first(q) : kNanScales, xs0 + half * (64 * NW * 16));
-    } else {
-      for (int k = 0; k < p.kb; ++k) s_xs[half][64 * wv + lane][k] = xs_ok ? xs[k] : kNanScales[k];
-    }
+    dma16(xs_ok ? xs + xs_first(q) : kNanScales, xs0 + half * (64 * NW * 16));
   };
 
   const int c16 = lane & 15, g = lane >> 4;
@@ -332,7 +325,7 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   // swizzle is that of row c16
   const int lo_at = c16 * kF8Block + 16 * (g ^ swizzle(c16));
   const int hi_at = c16 * kF8Block + 16 * ((g + 4) ^ swizzle(c16));
-  auto compute = [&](int stage, const float* x_scale, float w_scale) {
+  auto compute = [&](int stage, const float* x_scale, float w_scale, auto&& meanwhile) {
     const uint8_t* wrow = s_mem + stage * STAGE + wn * NT * 16 * kF8Block;
     const uint8_t* xrow = s_mem + stage * STAGE + (BN + wm * MT * 16) * kF8Block;
     F8Fragment<EXACT> xf[MT];
@@ -343,46 +336,56 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
                 *reinterpret_cast<const u32v4_t*>(xrow + hi_at + j * 16 * kF8Block));
       s[j] = w_scale * x_scale[((wm * MT + j) * 16 + c16) * 4];
     }
+    F8Fragment<EXACT> wf[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      wf[i].set(*reinterpret_cast<const u32v4_t*>(wrow + lo_at + i * 16 * kF8Block),
+                *reinterpret_cast<const u32v4_t*>(wrow + hi_at + i * 16 * kF8Block));
+    __builtin_amdgcn_sched_barrier(0);
+    meanwhile();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      F8Fragment<EXACT> wf;
-      wf.set(*reinterpret_cast<const u32v4_t*>(wrow + lo_at + i * 16 * kF8Block),
-             *reinterpret_cast<const u32v4_t*>(wrow + hi_at + i * 16 * kF8Block));
+      f32x4_t P[MT];
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const f32x4_t P = mfma_f8(wf, xf[j]);
+      for (int j = 0; j < MT; ++j) P[j] = mfma_f8(wf[i], xf[j]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s[j], P[q], acc[i][j][q]);
-      }
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s[j], P[j][q], acc[i][j][q]);
     }
   };
 
-  load_scales(b_begin, 0);
+  if (p.kb >= 4) {
+    load_scales(b_begin, 0);
+  } else {                             // rows shorter than one 16-byte load
+    for (int q = 0; q < p.kb; ++q) s_xs[0][64 * wv + lane][q] = xs_ok ? xs[q] : kNanScales[q];
+  }
 #pragma unroll
-  for (int k = 0; k < S - 1; ++k)
-    if (b_begin + k < b_end) load_step(b_begin + k, k);
-  int stage = 0, half = 0, first = xs_first(b_begin);
-  float w_scale = ws[b_begin];
-  // step b has landed (the code loads of the S - 2 steps after it may be in
-  // flight, while there are that many) and every wave has read step b - 1
-  auto arrive = [&](int b) {
-    if (b + S - 1 <= b_end) wait_loads_then_barrier<(S - 2) * LOADS>();
-    else wait_loads_then_barrier<0>();
-    if (((b - b_begin) & 3) == 0) {
-      if (b != b_begin) {
-        half ^= 1;
-        first = xs_first(b);
-      }
-      if (b + 4 < b_end) load_scales(b + 4, half ^ 1);
+  for (int n = 0; n < S - 1; ++n)
+    if (b_begin + n < b_end) load_step(b_begin + n, n);
+  // four K blocks a round: what a round needs once is done once, and stages and
+  // scale slots are constants
+  static_assert(4 % S == 0, "the ring's stages repeat every round");
+  int half = 0;
+  for (int q = b_begin; q < b_end; q += 4, half ^= 1) {
+    const float* x_scale = &s_xs[half][0][q - xs_first(q)];
+    float w_scale[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w_scale[u] = ws[min(q + u, b_end - 1)];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int b = q + u;
+      if (b >= b_end) break;
+      // step b has landed (the code loads of the S - 2 steps after it may be in
+      // flight, while there are that many) and every wave has read step b - 1
+      if (b + S - 1 <= b_end) wait_loads_then_barrier<(S - 2) * LOADS>();
+      else wait_loads_then_barrier<0>();
+      compute(u % S, x_scale + u, w_scale[u], [&]() {
+        if (u == 0 && q + 4 < b_end) load_scales(q + 4, half ^ 1);
+        if (b + S - 1 < b_end) load_step(b + S - 1, (u + S - 1) % S);
+      });
     }
-  };
-  for (int b = b_begin; b < b_end; ++b) {
-    arrive(b);
-    if (b + S - 1 < b_end) load_step(b + S - 1, stage == 0 ? S - 1 : stage - 1);
-    const float w_next = ws[min(b + 1, b_end - 1)];
-    compute(stage, &s_xs[half][0][b - first], w_scale);
-    w_scale = w_next;
-    stage = stage == S - 1 ? 0 : stage + 1;
   }
 
   if constexpr (SPLIT) {
@@ -412,8 +415,10 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4_t buffer_of(const void* base, uint64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return i32x4_t{static_cast<int32_t>(a), static_cast<int32_t>((a >> 32) & 0xffff),
-                 static_cast<int32_t>(min(bytes, uint64_t{0xffffffff})), 0x00020000};
+  const uint32_t size = (bytes >> 32) != 0 ? 0xffffffffu : static_cast<uint32_t>(bytes);
+  return i32x4_t{__builtin_amdgcn_readfirstlane(static_cast<int32_t>(a)),
+                 __builtin_amdgcn_readfirstlane(static_cast<int32_t>((a >> 32) & 0xffff)),
+                 __builtin_amdgcn_readfirstlane(static_cast<int32_t>(size)), 0x00020000};
 }
 __device__ __forceinline__ void dma16_buffer(uint32_t voff, i32x4_t buf, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
@@ -818,6 +823,8 @@ hipError_t launch_tile(LinearF8Params p, int splits, hipStream_t s) {
         <<<dim3(static_cast<unsigned>(blocks)), block, 0, s>>>(p);
     return hipGetLastError();
   }
+  const int64_t quads = p.T * ((p.N + 3) / 4);
+  if (quads > 0xffffff00ll) return hipErrorInvalidConfiguration;
   p.kb_split = (p.kb + splits - 1) / splits;
   splits = (p.kb + p.kb_split - 1) / p.kb_split;
   p.n_pad = (p.N + 3) / 4 * 4;
@@ -825,7 +832,6 @@ hipError_t launch_tile(LinearF8Params p, int splits, hipStream_t s) {
       <<<dim3(static_cast<unsigned>(blocks), splits), block, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t quads = p.T * (p.n_pad / 4);
   linear_f8_reduce_kernel<OUT><<<dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, s>>>(p, splits);
   return hipGetLastError();
 }
@@ -838,7 +844,7 @@ hipError_t launch_out(const LinearF8Params& p, const LinearF8Plan& plan, hipStre
     case F8_ROWS_NT2: return launch_rows<2, 1, 8, 1, OUT>(p, s);
     case F8_ROWS_NT4: return launch_rows<4, 1, 4, 1, OUT>(p, s);
     case F8_TILE_64X32: return launch_tile<64, 32, 4, 1, 4, OUT>(p, plan.splits, s);
-    case F8_TILE_64X64: return launch_tile<64, 64, 2, 2, 2, OUT>(p, plan.splits, s);
+    case F8_TILE_64X64: return launch_tile<64, 64, 2, 2, 4, OUT>(p, plan.splits, s);
     case F8_TILE_128X128: return launch_tile<128, 128, 2, 4, 2, OUT>(p, plan.splits, s);
     default:
       if constexpr (OUT == ACT_F32) return hipErrorInvalidValue;

@@ -7,12 +7,14 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <algorithm>
 #include <atomic>
+#include <limits>
 #include <mutex>
 #include <string>
 #include <utility>
@@ -549,7 +551,7 @@ void a8_tiles(int64_t M, int64_t N, int* mtt_out, int* nt_out) {
 // Limits of the 8-bit path: row lengths whose block counts and lane offsets
 // fit 32 bits, and launches of fewer than 2^32 threads (checked per call).
 constexpr int64_t kQ8MaxK = int64_t(1) << 23;
-constexpr int64_t kNormMaxM = int64_t(1) << 23;
+constexpr int64_t kNormMaxM = (int64_t(1) << 22) - 1;
 constexpr int64_t kF8MaxExperts = int64_t(1) << 16;
 int64_t f8_blocks(int64_t n) { return (n + 127) / 128; }
 
@@ -561,9 +563,45 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 }
 
 // Variant and K split of a block-scaled e4m3 product: T rows of y, E experts
-// (0: dense), rows of xq gathered from M.  Times below: us on MI355X, bf16
-// outputs, the variants forced in turn on one box (M, N, K; "64 x 8 of 64" is
-// 64 tokens to 8 of 64 experts each).
+// (0: dense), rows of xq gathered from M.  Times: us on MI355X, bf16 outputs,
+// the variants forced in turn on one box (M, N, K; "64 x 8 of 64" is 64 tokens
+// to 8 of 64 experts each).
+//
+// Up to 16 rows (10 an expert on average: grouped rows are uneven, and a second
+// tile of 16 costs more than one of 32; 13 an expert: 44 against 42 of 64 x 32)
+// the weights are streamed past them.  Wider blocks load the activations once
+// for more weights, narrower ones are more:
+// - 64 columns from 7/4 of a block a CU on (64 x 8 of 64, 1408, 2048: 39 against
+//   48 of 32 columns; 16, 28672, 4096: 27 against 30);
+// - 32 columns from 7/8 on (8, 8192, 2048: 5.7 against 6.3 of 16; 8, 4096, 4096,
+//   half a block: 8.1 against 6.7);
+// - 64 x 32 tiles, whose loads are further ahead, where they are 3/4 of a block
+//   to one a CU (8, 14336, 4096: 11.2 against 12.5; 8, 8192, 2048, half a block:
+//   6.8 against 5.7) and K is not long (8, 28672, 8192: 47 against 46);
+// - 16 columns read more activations than they can hide from 9 rows on where K
+//   is long (16, 4096, 14336: 18.4 against 14.4 of 64 x 32 tiles in splits).
+//
+// All other calls take the cheapest of the tiles by an estimate: a CU runs one
+// block's K step in `one`, the steps of two blocks in `two` (us, from 48 single
+// runs of each tile); splits of K of at least four steps add the write and the
+// read of their partial sums and a launch; weights come at 5 TB/s at best.  Over
+// 113 shapes (1 to 8192 rows, K of 1024 to 16384, dense and grouped) its choice
+// was 3 % (root mean square) slower than the fastest variant, 15 % at worst.
+// Where it changes over: 512, 4096, 4096: 17.4 of 64 x 64 against 25.6 of
+// 128 x 128; 1024, 4096, 4096: 33 against 27; 3000, 4096, 4096: 54 of 256 x 256
+// against 61; 1536, 14336, 4096: 120 against 110; 128, 4096, 14336 in 64 x 64
+// tiles: 20.6 in four splits against 51 in one.
+struct F8TileRate {
+  lowbit::LinearF8Kind kind;
+  int bn, bm;
+  double one, two;
+};
+constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 0.31, 0.38},
+                                   {lowbit::F8_TILE_64X64, 64, 64, 0.50, 0.54},
+                                   {lowbit::F8_TILE_128X128, 128, 128, 1.00, 1.34}};
+constexpr double kF8JoinUs = 3.2, kF8JoinUsPerByte = 0.48e-6, kF8BytesPerUs = 5e6;
+constexpr double kF8BigUs = 1.8, kF8BigStep = 1.82, kF8BigFullStep = 2.14;   // 256 x 256: one block a CU
+constexpr int kF8MaxSplits = 16, kF8MinSplitSteps = 4;
 lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64_t N, int64_t K,
                              lowbit_dtype dtype) {
   using namespace lowbit;
@@ -571,58 +609,46 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   const bool grouped = E > 0;
   const int64_t used = grouped ? std::min(E, T) : 1;    // experts with rows, at most
   const int64_t per = (T + used - 1) / used;            // rows of one, on average
-  // row tiles, with half a tile of waste an expert
-  auto tiles = [&](int64_t bn, int64_t bm) {
-    const int64_t tm = grouped ? T / bm + (used + 1) / 2 : (T + bm - 1) / bm;
-    return tm * ((N + bn - 1) / bn);
-  };
-  LinearF8Plan plan{F8_ROWS_NT1, 1};
-  auto split_to = [&](int64_t target, int64_t n, int64_t min_blocks) {
-    plan.splits = static_cast<int>(std::max<int64_t>(1, std::min({target / n, kb / min_blocks, int64_t{64}})));
-  };
-  // Up to 16 rows the weights are streamed past them.  Wider blocks load the
-  // activations once for more weights, narrower ones are more: 64 columns from
-  // two blocks a CU on (64 x 8 of 64, 1408, 2048: 38 against 42 and 50; 1,
-  // 16384, 16384, one block a CU: 67 against 50 and 46), 32 columns from 7/8
-  // of a block a CU on (8, 8192, 2048: 5.6 against 6.3 with 16; 8, 4096, 4096:
-  // 8.2 against 6.8).  Grouped rows are uneven: from 10 an expert on average
-  // too many have a second tile of 16 (16 an expert: 49 against 43 of 64 x 32).
   if (per <= (grouped ? 10 : 16)) {
-    const int64_t units = used * ((N + 15) / 16);       // 16 x 16 tiles
-    if (units >= 4 * 2 * cus) plan.kind = F8_ROWS_NT4;
-    else if (units >= 2 * (cus * 7 / 8)) plan.kind = F8_ROWS_NT2;
-    // (16-column blocks read more activations than they can hide from 9 rows on
-    // where K is long: 16, 4096, 14336: 18.3 against 15.7 of 64 x 32 in splits)
-    if (plan.kind != F8_ROWS_NT1 || per <= 8 || kb < 64) return plan;
+    const int64_t units = used * ((N + 15) / 16), wide = used * ((N + 63) / 64);
+    if (wide * 4 >= cus * 3 && wide <= cus && kb < 64) return {F8_TILE_64X32, 1};
+    if (units >= 4 * (cus * 7 / 4)) return {F8_ROWS_NT4, 1};
+    if (units >= 2 * (cus * 7 / 8)) return {F8_ROWS_NT2, 1};
+    if (per <= 8 || kb < 64) return {F8_ROWS_NT1, 1};
   }
-  // 256 x 256 tiles where they fill the CUs evenly (8192, 14336, 4096: 456
-  // against 567 of 128 x 128; 1536, 14336, 4096, 1.3 tiles a CU: 122 against
-  // 117); their sums are those of the fp8 MFMA, and their offsets into a
-  // gathered xq 32 bits.
-  const int64_t t256 = tiles(256, 256), rounds = (t256 + cus - 1) / cus;
-  if (dtype != LOWBIT_F32 && per >= 192 && t256 * 8 >= cus * 7 && t256 * 4 >= rounds * cus * 3 &&
-      !(gather && M * K > int64_t{0xffffffff})) {
-    plan.kind = F8_TILE_256X256;
-    return plan;
+  // blocks a CU (an expert's last row tile is half full, its first never missing)
+  auto load = [&](int64_t bn, int64_t bm) {
+    const int64_t tm = grouped ? std::max(used, T / bm + used / 2) : (T + bm - 1) / bm;
+    return static_cast<double>(tm) * static_cast<double>((N + bn - 1) / bn) / static_cast<double>(cus);
+  };
+  const double codes = (static_cast<double>(used) * static_cast<double>(N) + static_cast<double>(T)) *
+                       static_cast<double>(kb) * 128.0;
+  LinearF8Plan plan{F8_TILE_64X32, 1};
+  double best = std::numeric_limits<double>::infinity();
+  for (const F8TileRate& t : kF8Tiles) {
+    const double blocks = load(t.bn, t.bm);
+    for (int splits = 1; splits <= kF8MaxSplits; ++splits) {
+      const int64_t steps = (kb + splits - 1) / splits;
+      if (splits > 1 && (kb < int64_t{kF8MinSplitSteps} * splits || (kb + steps - 1) / steps != splits)) continue;
+      const double n = blocks * splits, rest = n - 2 * std::floor(n / 2);
+      double us = std::floor(n / 2) * t.two;
+      if (rest > 0) us += t.one + std::max(rest - 1, 0.0) * (t.two - t.one);
+      us *= static_cast<double>(steps);
+      if (splits > 1)
+        us = std::max(us, codes / kF8BytesPerUs) + kF8JoinUs +
+             kF8JoinUsPerByte * 4 * splits * static_cast<double>(T) * static_cast<double>(N);
+      if (us < best) {
+        best = us;
+        plan = {t.kind, splits};
+      }
+    }
   }
-  // 128 x 128 where that many fill the CUs, splits of at least 28 K blocks
-  // counted (256, 14336, 4096: 27 against 37 of 64 x 64; 512, 4096, 4096: 23
-  // against 20; 1024 x 8 of 64, 1408, 2048: 66 against 81).
-  const int64_t t128 = tiles(128, 128);
-  if (per >= (grouped ? 64 : 129) && t128 * std::max<int64_t>(1, kb / 28) * 8 >= cus * 7) {
-    plan.kind = F8_TILE_128X128;
-    split_to(2 * cus, t128, 28);
-    return plan;
-  }
-  // Then 64 x 64, or 64 x 32 up to 32 rows (20 on average), in as many splits
-  // as give two blocks a CU and leave eight K blocks each (128, 4096, 14336:
-  // 23 in four against 57 in one).
-  if (per <= (grouped ? 20 : 32)) {
-    plan.kind = F8_TILE_64X32;
-    split_to(cus * 7 / 4, tiles(64, 32), 8);
-  } else {
-    plan.kind = F8_TILE_64X64;
-    split_to(2 * cus, tiles(64, 64), 8);
+  // 256 x 256 tiles: their sums are those of the fp8 MFMA, and their offsets
+  // into a gathered xq 32 bits
+  if (dtype != LOWBIT_F32 && !(gather && M * K > int64_t{0xffffffff})) {
+    const double n = load(256, 256), whole = std::floor(n);
+    if (kF8BigUs + static_cast<double>(kb) * (whole * kF8BigFullStep + (n > whole ? kF8BigStep : 0)) < best)
+      plan = {F8_TILE_256X256, 1};
   }
   return plan;
 }
@@ -932,7 +958,7 @@ lowbit_status lowbit_add_rmsnorm_q8(const void* x, const void* residual, const v
     return fail(LOWBIT_ERR_UNSUPPORTED, "format=%d", (int)format);
   const lowbit_status st = check_q8_row(K, format == LOWBIT_Q8_I8 ? 32 : 16);
   if (st != LOWBIT_OK) return st;
-  if (M < 0 || M > kNormMaxM) return fail(LOWBIT_ERR_INVALID_ARG, "M=%lld not in 0..2^23", (long long)M);
+  if (M < 0 || M > kNormMaxM) return fail(LOWBIT_ERR_INVALID_ARG, "M=%lld not in 0..2^22 - 1", (long long)M);
   if (!(eps >= 1e-20f && eps <= 1.0f)) return fail(LOWBIT_ERR_INVALID_ARG, "eps=%g not in 1e-20..1", eps);
   if (M == 0) return LOWBIT_OK;
   if (!x) return fail(LOWBIT_ERR_INVALID_ARG, "NULL x");

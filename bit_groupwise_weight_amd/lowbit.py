@@ -604,7 +604,7 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     if residual is not None:
         _expect_tensor(residual, "residual", (M, K), dt)
         if h is None:
-            h = torch.empty((M, K), dtype=dt, device=x.device)
+            h = torch.empty_like(x)
         else:
             _expect_tensor(h, "h", (M, K), dt)
     else:
@@ -614,7 +614,7 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     else:
         code, spans = (torch.int8, (M,)) if fmt == Q8_I8 else (_F8, (M, _f8_blocks(K)))
         if q is None:
-            q = torch.empty((M, K), dtype=code, device=x.device)
+            q = torch.empty_like(x, dtype=code)
         else:
             _expect_tensor(q, "q", (M, K), code)
         if qscale is None:
@@ -624,7 +624,7 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     if y is not None:
         _expect_tensor(y, "y", (M, K), dt)
     elif want_y or fmt == Q8_NONE:
-        y = torch.empty((M, K), dtype=dt, device=x.device)
+        y = torch.empty_like(x)
     dev = _placed(x, weight, residual, q, qscale, h, y)
     st = _call_on(dev, "lowbit_add_rmsnorm_q8", _ptr(x), _ptr(residual), _ptr(weight), eps, _DTYPE_ENUM[dt], M,
                   K, fmt, _ptr(q), _ptr(qscale), _ptr(h), _ptr(y), _stream_of(dev, stream))
@@ -665,7 +665,7 @@ def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
         raise ValueError(f"x dtype {x.dtype} is not float32, float16 or bfloat16")
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=_F8, device=x.device)
+        xq = torch.empty_like(x, dtype=_F8)
     if xscale is None:
         xscale = torch.empty((M, _f8_blocks(K)), dtype=torch.float32, device=x.device)
     _expect_tensor(xq, "xq", (M, K), _F8)

@@ -312,7 +312,7 @@ typedef enum lowbit_q8_format {
  *   residual  device, M x K, dtype, 16-byte aligned, or NULL.
  *   weight    device, K elements of dtype, 16-byte aligned, or NULL (ones).
  *   eps       1e-20 .. 1.
- *   M >= 0 (0 is a no-op; at most 2^23), K > 0 and a multiple of 16 (of 32
+ *   M >= 0 (0 is a no-op; below 2^22), K > 0 and a multiple of 16 (of 32
  *             with LOWBIT_Q8_I8, as lowbit_linear_a8 takes it), K <= 2^23.
  *   q         device, M x K codes, 16-byte aligned.  Written.  NULL with
  *             LOWBIT_Q8_NONE.

@@ -335,7 +335,8 @@ def test_linear_exact(M, N, K):
     (12, 300, 8336), (20, 300, 4096), (31, 2000, 8208), (70, 300, 8208), (128, 1030, 2064),  # K splits
     (512, 2050, 14336), (300, 4608, 3600),                # 128 x 128 tiles, in splits and whole
     (300, 28700, 272), (257, 28673, 16), (300, 28700, 400), (259, 28700, 8336), (512, 14336, 528),  # 256 x 256
-    (1100, 14340, 1168),
+    (1100, 14340, 1168), (300, 28700, 528), (600, 14340, 1040), (600, 14340, 1168), (4100, 16400, 144),
+    (8192, 8192, 16), (300, 8200, 8208),
 ])
 def test_linear_variants(M, N, K, dtype):
     """Every kernel variant at ragged edges: exact inputs, every column near a tile's edge and a
@@ -401,6 +402,25 @@ def test_linear_nan_stays_in_its_rows_and_columns(M):
     ref[[0, M - 1]] = np.nan
     ref[:, 130] = np.nan
     close(y, ref, A, 4, torch.float32, f"NaN M={M}")
+
+
+def test_linear_nan_in_256_tiles():
+    """The same through 256 x 256 tiles: codes and scales of NaN beside each edge of K's partial block."""
+    M, N, K = 600, 14340, 1040
+    xq, xs, wq, ws = exact_inputs(6, M, N, K)
+    xq[599, K - 1], xq[255, K - 16], xq[300, 0] = 0x7f, 0xff, 0x7f
+    wq[N - 1, K - 1], wq[255, K - 16], wq[256, 1023] = 0x7f, 0xff, 0x7f
+    xs[31, 8], xs[512, 0], ws[5, 8] = np.nan, np.nan, np.nan
+    cols = np.unique(np.concatenate([np.arange(250, 260), np.arange(630, 780), np.arange(N - 9, N)]))
+    y = lb.lowbit_linear_f8(up8(xq), up(xs), up8(wq), up(ws), None, torch.float16)
+    ref, _ = o.linear_f8(np.where(xq & 0x7f == 0x7f, 0, xq), np.nan_to_num(xs),
+                         np.where(wq & 0x7f == 0x7f, 0, wq), np.nan_to_num(ws), None, cols)
+    ref[[31, 255, 300, 512, 599]] = np.nan
+    ref[:, (cols == N - 1) | (cols == 255) | (cols == 256) | (cols // 128 == 5)] = np.nan
+    got = f64(y[:, torch.from_numpy(cols).to(DEV)])
+    assert np.array_equal(got, f64(torch.from_numpy(ref).to(torch.float16)), equal_nan=True)
+    assert int(torch.isnan(y).any(0).sum()) == N and int(torch.isnan(y).all(0).sum()) == 3 + 128
+    assert int(torch.isnan(y).all(1).sum()) == 5
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
@@ -517,7 +537,9 @@ def test_grouped_exact_and_equal_to_dense(counts):
 @pytest.mark.parametrize("counts, N, K", [
     ([30, 0, 25], 200, 4112), ([60, 0, 70], 300, 2064),   # K splits, 64 x 32 and 64 x 64
     ([200, 100, 0, 130], 6000, 272),                      # 128 x 128
-    ([300, 260, 0, 208], 14356, 400), ([257, 1, 600, 0, 300], 14356, 144),                  # 256 x 256
+    ([200, 100, 0, 290], 4100, 8208),                     # 128 x 128 in splits
+    ([300, 260, 0, 208], 14356, 400), ([257, 1, 600, 0, 300], 14356, 144),
+    ([2000, 988], 14356, 272), ([1, 730, 257], 14356, 528),                                 # 256 x 256
 ])
 @pytest.mark.parametrize("gather", [True, False])
 def test_grouped_variants(counts, N, K, dtype, gather):
