@@ -412,6 +412,14 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
 // load (row and chunk) and a scalar base that moves on by 128 bytes a step, so
 // that no wave keeps 64-bit addresses; rows past N or past the tile's end lie
 // past the descriptor's end and read nothing.
+// A step has 2048 MFMA cycles a CU and as many of LDS traffic (192 KiB read, 64
+// KiB written, 128 bytes a cycle), and a scaling FMA a product in the MFMAs'
+// shadow.  8192 rows of K = 4096 into N = 14336: 421-435 us, 2.2-2.3 PFLOP/s
+// (a large unscaled e4m3 library product: 2.9-3.2); 352 us on codes of zero: the
+// rest is the clock that the card's power leaves (1.8 to 2.0 of 2.4 GHz).  What
+// each form measured (us, one box): one barrier a step and loads in pairs 452, a
+// load a tile 436; without loads 354.  MFMAs of 32 x 32 x 64 are no faster beside
+// the FMAs (registers only: 3.45 PFLOP/s against 3.80).
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4_t buffer_of(const void* base, uint64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -425,6 +433,7 @@ __device__ __forceinline__ void dma16_buffer(uint32_t voff, i32x4_t buf, uint32_
                : : "v"(voff), "s"(buf), "s"(m0) : "memory", "m0");
 }
 
+// (K of four blocks or more)
 template <int OUT>
 __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p) {
   static_assert(OUT != ACT_F32, "fp8 MFMA sums are not fp32");
@@ -454,11 +463,14 @@ __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p)
   const uint64_t xbytes = static_cast<uint64_t>(p.rows ? p.M : rt.end - rt.begin) * p.K;
   const int last_chunks = (p.K - (p.kb - 1) * kF8Block) / 16;   // of the last block: 1 .. 8
 
-  // piece k < 4 of a step, for a wave: its weight rows 32 wv + 8 k .. + 7 and
-  // the same of its activation rows; lane l fills position l % 8 of row l / 8
+  // A wave loads 32 activation rows and 32 weight rows of a step, 8 rows a load:
+  // activation rows 32 wv + 8 k; weight rows of pieces 0 and 1 in the upper half
+  // of a column wave's 128 rows, of pieces 2 and 3 in the lower half.  Lane l
+  // fills position l % 8 of row l / 8.
   const int sub = lane >> 3;
   const int chunk0 = (lane & 7) ^ swizzle(sub);         // of even pieces; odd ones: ^ 4
-  const uint32_t woff = (32 * wv + sub) * p.K;
+  const int wrow0 = (wv >> 2) * (BN / 2) + (wv & 3) * 16;
+  const uint32_t woff = (wrow0 + sub) * p.K;
   uint32_t xoff[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -478,24 +490,27 @@ __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p)
     xs_ok = from >= 0 && from < p.M;
     if (xs_ok) xs = p.xs + from * p.kb;
   }
-  const uint32_t codes0 = lds_address(s_mem) + wv * 32 * kF8Block;
+  const uint32_t wcodes0 = lds_address(s_mem) + wrow0 * kF8Block;
+  const uint32_t xcodes0 = lds_address(s_mem) + (BN + wv * 32) * kF8Block;
   const uint32_t xs0 = lds_address(&s_xs[0][0][0]) + wv * 64 * 16;
   // (without branches, so that the loads can stand between a step's MFMAs: a
-  // step past the last one reads nothing, from a descriptor of no bytes)
-  auto load_piece = [&](int b, int k) {
-    const uint32_t dst = codes0 + (b & 1) * STAGE + k * 8 * kF8Block;
+  // step past the last one reads nothing, from a descriptor of no bytes.  Past
+  // the row's end in the last block: zeros for the activations (an offset past
+  // the buffer), the block's first chunk for the weights they meet.)
+  auto past_row = [&](int b, int chunk) { return b == p.kb - 1 && chunk >= last_chunks; };
+  auto load_x = [&](int b, int k) {
     const uint64_t at = static_cast<uint64_t>(b) * kF8Block;
-    const bool some = b < p.kb;
-    const i32x4_t wbuf = buffer_of(wbase + at, some ? wbytes - at : 0);
-    const i32x4_t xbuf = buffer_of(xbase + at, some ? xbytes - at : 0);
     const int chunk = k & 1 ? chunk0 ^ 4 : chunk0;
-    // past the row's end in the last block: zeros for the activations (an offset
-    // past the buffer), the block's first chunk for the weights they meet
-    const bool past = b == p.kb - 1 && chunk >= last_chunks;
-    dma16_buffer(past ? 0xfffffff0u : xoff[k] + 16 * chunk, xbuf, dst + BN * kF8Block);
-    dma16_buffer(woff + 8 * k * p.K + (past ? 0 : 16 * chunk), wbuf, dst);
+    dma16_buffer(past_row(b, chunk) ? 0xfffffff0u : xoff[k] + 16 * chunk,
+                 buffer_of(xbase + at, b < p.kb ? xbytes - at : 0), xcodes0 + (b & 1) * STAGE + 8 * k * kF8Block);
   };
-  auto xs_first = [&](int q) { return max(min(q, p.kb - 4), 0); };
+  auto load_w = [&](int b, int k) {
+    const uint64_t at = static_cast<uint64_t>(b) * kF8Block;
+    const int chunk = k & 1 ? chunk0 ^ 4 : chunk0, r = (k >> 1) * (BN / 4) + (k & 1) * 8;
+    dma16_buffer(woff + r * p.K + (past_row(b, chunk) ? 0 : 16 * chunk),
+                 buffer_of(wbase + at, b < p.kb ? wbytes - at : 0), wcodes0 + (b & 1) * STAGE + r * kF8Block);
+  };
+  auto xs_first = [&](int q) { return min(q, p.kb - 4); };
   auto load_four_scales = [&](int q, int half) {
     if (wv < BM / 64) dma16(xs_ok ? xs + xs_first(q) : xs, xs0 + half * (BM * 16));
   };
@@ -508,25 +523,24 @@ __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p)
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int lo_at = c16 * kF8Block + 16 * (g ^ swizzle(c16));
   const int hi_at = c16 * kF8Block + 16 * ((g + 4) ^ swizzle(c16));
-  F8Fragment<false> xf[MT], wf[2];
-  f32x4_t P[MT];                       // the products of the tile before
+  F8Fragment<false> xf[MT], wf[3];
+  f32x4_t P[4];                        // the products of the last four MFMAs
   float s[MT], s_last[MT];             // the scales of this step and of the one before
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
+  for (int j = 0; j < 4; ++j) {
     P[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     s[j] = 0.0f;
   }
-  auto read_x = [&](int stage) {
-    const uint8_t* xrow = s_mem + stage * STAGE + (BN + wm * MT * 16) * kF8Block;
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-      xf[j].set(*reinterpret_cast<const u32v4_t*>(xrow + lo_at + j * 16 * kF8Block),
-                *reinterpret_cast<const u32v4_t*>(xrow + hi_at + j * 16 * kF8Block));
+  auto read_x = [&](int j, int stage) {
+    const uint8_t* xrow = s_mem + stage * STAGE + (BN + (wm * MT + j) * 16) * kF8Block;
+    xf[j].set(*reinterpret_cast<const u32v4_t*>(xrow + lo_at), *reinterpret_cast<const u32v4_t*>(xrow + hi_at));
   };
+  // (three fragments: the two last column tiles of a step and the first of the next)
+  auto w_slot = [](int i) { return i == 4 || i == 7 ? 2 : i == 1 || i == 3 || i == 6 ? 1 : 0; };
   auto read_w = [&](int i, int stage) {
-    const uint8_t* wrow = s_mem + stage * STAGE + wn * NT * 16 * kF8Block;
-    wf[i & 1].set(*reinterpret_cast<const u32v4_t*>(wrow + lo_at + i * 16 * kF8Block),
-                  *reinterpret_cast<const u32v4_t*>(wrow + hi_at + i * 16 * kF8Block));
+    const uint8_t* wrow = s_mem + stage * STAGE + (wn * NT + i) * 16 * kF8Block;
+    wf[w_slot(i)].set(*reinterpret_cast<const u32v4_t*>(wrow + lo_at),
+                      *reinterpret_cast<const u32v4_t*>(wrow + hi_at));
   };
   auto read_scales = [&](const float* x_scale, int b) {
     const float w_scale = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws64), b & 63));
@@ -536,36 +550,22 @@ __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p)
       s[j] = w_scale * x_scale[((wm * MT + j) * 16 + c16) * 4];
     }
   };
-  // The MFMAs of column tile i, each behind the scaling of the products that it
-  // replaces (those of tile i - 1, in the shadow of the MFMA before).
-  auto tile = [&](int i) {
+  // MFMA n of a step's 32: column tile by column tile, the last two together.
+  // Each stands behind the scaling of the products that it replaces (those of
+  // the fourth MFMA before it), in the shadow of the MFMA before.
+  auto tile_i = [](int n) { return n < 24 ? n / 4 : 6 + (n & 1); };
+  auto tile_j = [](int n) { return n < 24 ? n % 4 : (n - 24) / 2; };
+  auto add_products = [&](int n, const float (&sc)[MT]) {
+    const int i = tile_i(n), j = tile_j(n);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int before = i == 0 ? NT - 1 : i - 1;
-      const float sj = i == 0 ? s_last[j] : s[j];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[before][j][q] = fmaf(sj, P[j][q], acc[before][j][q]);
-      P[j] = mfma_f8(wf[i & 1], xf[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(sc[j], P[n & 3][q], acc[i][j][q]);
   };
-  // Column tiles 0 .. NT - 2 of step b: a tile's weights are read one tile
-  // ahead; the next step's loads go out a piece at a time (all at once they
-  // would hold up the wave that issues them).
-  auto most_tiles = [&](int b) {
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < NT - 1; ++i) {
-      if (i < 3) load_piece(b + 1, i + 1);
-      read_w(i + 1, b & 1);
-      __builtin_amdgcn_sched_barrier(0);
-      tile(i);
-    }
+  auto mfma = [&](int n) {
+    if (n < 4) add_products(n + 28, s_last);
+    else add_products(n - 4, s);
+    P[n & 3] = mfma_f8(wf[w_slot(tile_i(n))], xf[tile_j(n)]);
+    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
   };
 
   // (keeps the compiler from sinking the sums below the branches that follow,
@@ -576,29 +576,61 @@ __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p)
       asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
   };
 
-  // The step's barrier stands before its last tile, whose operands are then in
-  // registers: past it the step's stage is free for the loads two steps on,
-  // the next stage has landed, and the last tile's MFMAs cover the reads of the
-  // next step's first fragments.
-  int half = 0, first = xs_first(0);
-  if (p.kb >= 4) {
-    load_four_scales(0, 0);
-  } else if (wv < BM / 64) {           // rows shorter than one 16-byte load
-    for (int k = 0; k < p.kb; ++k) s_xs[0][64 * wv + lane][k] = xs[k];
+  // A step has two barriers.  Past the first, before its fourth column tile, its
+  // lower weight rows have landed, and its activations and upper weight rows are
+  // free for the step after next; past the second, before its last two tiles, the
+  // next step's activations and upper weight rows have landed, and its lower
+  // weight rows are free for the step after next.  So each wave issues one load a
+  // column tile (a load holds up the wave that issues it for some 50 cycles, more
+  // where all waves issue several at once), and six tiles or more pass before one
+  // is waited for.  The next step's activations are read between the MFMAs of the
+  // last two column tiles, each over a fragment that these need no more (all at
+  // once they would hold up every wave).
+  int half = 0, first = 0;
+  load_four_scales(0, 0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    load_x(0, k);
+    load_w(0, k);
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) load_piece(0, k);
-  wait_loads_then_barrier<0>();
+  for (int k = 0; k < 4; ++k) load_x(1, k);
+  load_w(1, 0);
+  wait_loads_then_barrier<5>();
   if (p.kb > 4) load_four_scales(4, 1);
-  load_piece(1, 0);
   read_w(0, 0);
-  read_x(0);
+#pragma unroll
+  for (int j = 0; j < MT; ++j) read_x(j, 0);
   read_scales(&s_xs[0][0][0], 0);
-  for (int b = 0; b < p.kb - 1; ++b) {
-    const int nb = b + 1;
-    most_tiles(b);
+  for (int b = 0; b < p.kb; ++b) {
+    const int nb = b + 1, stage = b & 1;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      if (i == 0) load_w(nb, 1);
+      if (i == 1 || i == 2) load_w(nb, 1 + i);
+      if (i == 3) wait_loads_then_barrier<8>();
+      if (i >= 3) load_x(nb + 1, i - 3);
+      read_w(i + 1, stage);
+      if (i == 5) read_w(7, stage);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) mfma(4 * i + j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_loads_then_barrier<5>();
+    load_x(nb + 1, 3);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      if (j == 2) load_w(nb + 1, 0);
+      mfma(24 + 2 * j);
+      mfma(25 + 2 * j);
+      __builtin_amdgcn_sched_barrier(0);
+      read_x(j, stage ^ 1);
+      if (j == 1) read_w(0, stage ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     settle_sums();
-    wait_loads_then_barrier<0>();
     if ((nb & 3) == 0) {
       half ^= 1;
       first = xs_first(nb);
@@ -608,18 +640,10 @@ __global__ __launch_bounds__(512, 2) void linear_f8_big_kernel(LinearF8Params p)
         asm volatile("" : "+v"(ws64));                  // waited for here, not at each use
       }
     }
-    tile(NT - 1);
-    load_piece(nb + 1, 0);
-    read_w(0, nb & 1);
-    read_x(nb & 1);
-    read_scales(&s_xs[half][0][nb - first], nb);
+    read_scales(&s_xs[half][0][min(nb, p.kb - 1) - first], nb);
   }
-  most_tiles(p.kb - 1);
-  tile(NT - 1);
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[NT - 1][j][q] = fmaf(s[j], P[j][q], acc[NT - 1][j][q]);
+  for (int n = 28; n < 32; ++n) add_products(n, s_last);
   settle_sums();
 
   wait_loads_then_barrier<0>();        // every wave has read the last stage

@@ -588,8 +588,8 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 // 113 shapes (1 to 8192 rows, K of 1024 to 16384, dense and grouped) its choice
 // was 3 % (root mean square) slower than the fastest variant, 15 % at worst.
 // Where it changes over: 512, 4096, 4096: 17.4 of 64 x 64 against 25.6 of
-// 128 x 128; 1024, 4096, 4096: 33 against 27; 3000, 4096, 4096: 54 of 256 x 256
-// against 61; 1536, 14336, 4096: 120 against 110; 128, 4096, 14336 in 64 x 64
+// 128 x 128; 1024, 4096, 4096: 33 against 27; 3000, 4096, 4096: 51 of 256 x 256
+// against 59; 2048, 4096, 4096: 50 against 37; 128, 4096, 14336 in 64 x 64
 // tiles: 20.6 in four splits against 51 in one.
 struct F8TileRate {
   lowbit::LinearF8Kind kind;
@@ -600,7 +600,8 @@ constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 0.31, 0.38},
                                    {lowbit::F8_TILE_64X64, 64, 64, 0.50, 0.54},
                                    {lowbit::F8_TILE_128X128, 128, 128, 1.00, 1.34}};
 constexpr double kF8JoinUs = 3.2, kF8JoinUsPerByte = 0.48e-6, kF8BytesPerUs = 5e6;
-constexpr double kF8BigUs = 1.8, kF8BigStep = 1.82, kF8BigFullStep = 2.14;   // 256 x 256: one block a CU
+// 256 x 256: one block a CU, a round's start and end, a step of few and of all CUs
+constexpr double kF8BigUs = 5.5, kF8BigStep = 1.35, kF8BigFullStep = 1.70;
 constexpr int kF8MaxSplits = 16, kF8MinSplitSteps = 4;
 lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64_t N, int64_t K,
                              lowbit_dtype dtype) {
@@ -643,12 +644,13 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
       }
     }
   }
-  // 256 x 256 tiles: their sums are those of the fp8 MFMA, and their offsets
-  // into a gathered xq 32 bits
-  if (dtype != LOWBIT_F32 && !(gather && M * K > int64_t{0xffffffff})) {
+  // 256 x 256 tiles: their sums are those of the fp8 MFMA, their offsets into a
+  // gathered xq 32 bits, and they load four blocks' scales at once
+  if (dtype != LOWBIT_F32 && kb >= 4 && !(gather && M * K > int64_t{0xffffffff})) {
     const double n = load(256, 256), whole = std::floor(n);
-    if (kF8BigUs + static_cast<double>(kb) * (whole * kF8BigFullStep + (n > whole ? kF8BigStep : 0)) < best)
-      plan = {F8_TILE_256X256, 1};
+    double us = whole * (kF8BigUs + static_cast<double>(kb) * kF8BigFullStep);
+    if (n > whole) us += kF8BigUs + static_cast<double>(kb) * kF8BigStep;
+    if (us < best) plan = {F8_TILE_256X256, 1};
   }
   return plan;
 }

@@ -335,7 +335,7 @@ def test_linear_exact(M, N, K):
     (12, 300, 8336), (20, 300, 4096), (31, 2000, 8208), (70, 300, 8208), (128, 1030, 2064),  # K splits
     (512, 2050, 14336), (300, 4608, 3600),                # 128 x 128 tiles, in splits and whole
     (300, 28700, 272), (257, 28673, 16), (300, 28700, 400), (259, 28700, 8336), (512, 14336, 528),  # 256 x 256
-    (1100, 14340, 1168), (300, 28700, 528), (600, 14340, 1040), (600, 14340, 1168), (4100, 16400, 144),
+    (1100, 14340, 1168), (300, 28700, 528), (600, 14340, 1040), (600, 14340, 1168), (4100, 16400, 144), (700, 28700, 656),
     (8192, 8192, 16), (300, 8200, 8208),
 ])
 def test_linear_variants(M, N, K, dtype):
@@ -539,7 +539,7 @@ def test_grouped_exact_and_equal_to_dense(counts):
     ([200, 100, 0, 130], 6000, 272),                      # 128 x 128
     ([200, 100, 0, 290], 4100, 8208),                     # 128 x 128 in splits
     ([300, 260, 0, 208], 14356, 400), ([257, 1, 600, 0, 300], 14356, 144),
-    ([2000, 988], 14356, 272), ([1, 730, 257], 14356, 528),                                 # 256 x 256
+    ([2000, 988], 14356, 784), ([1, 730, 257], 14356, 528),                                 # 256 x 256
 ])
 @pytest.mark.parametrize("gather", [True, False])
 def test_grouped_variants(counts, N, K, dtype, gather):
