@@ -524,7 +524,8 @@ class F8Experts(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
         """x[..., H] (the module's dtype); experts (integer) and weights, both [..., k]: each
-        token's experts and their routing weights."""
+        token's experts and their routing weights.  An expert outside 0..E-1 (a padded slot)
+        adds nothing."""
         xq, xscale = torch.ops.lowbit.quantize_act_f8(x.reshape(-1, self.hidden))
         return self.forward_codes(xq, xscale, experts, weights).reshape(x.shape)
 
@@ -534,7 +535,7 @@ class F8Experts(torch.nn.Module):
         T, k = xq.shape[0], experts.shape[-1]
         if experts.shape != weights.shape or experts.numel() != T * k:
             raise ValueError("experts and weights must both be [T, k]")
-        ids = experts.reshape(-1)
+        ids = experts.reshape(-1).long()
         order = torch.argsort(ids, stable=True)
         # rows of the experts below each bound: where every expert's rows begin and end
         bounds = torch.arange(self.num_experts + 1, device=ids.device, dtype=ids.dtype)
@@ -549,7 +550,9 @@ class F8Experts(torch.nn.Module):
         back = torch.empty_like(order)
         back[order] = torch.arange(order.numel(), device=order.device)
         out = slots[back].view(T, k, self.hidden).float() * weights.reshape(T, k, 1).float()
-        return out.sum(1).to(self.dtype)
+        # (rows of no expert are undefined)
+        used = ((ids >= 0) & (ids < self.num_experts)).view(T, k, 1)
+        return torch.where(used, out, 0.0).sum(1).to(self.dtype)
 
     def extra_repr(self) -> str:
         return (f"num_experts={self.num_experts}, hidden={self.hidden}, intermediate={self.intermediate}, "

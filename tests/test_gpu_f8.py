@@ -642,6 +642,25 @@ def test_block_norm_router_experts(T):
     assert torch.equal(m(y, ids, w), out)
 
 
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+def test_experts_leave_padded_slots_out(kind):
+    """Expert ids outside 0..E-1 add nothing, whatever memory their rows' buffers held before."""
+    torch.manual_seed(8)
+    E, H, I, T, k = 5, 144, 80, 33, 3
+    m = lnn.F8Experts(E, H, I, device=DEV).set_weight(torch.randn(E, 2 * I, H, device=DEV) * 0.06,
+                                                      torch.randn(E, H, I, device=DEV) * 0.08)
+    x = torch.randn(T, H, device=DEV).bfloat16()
+    ids, w = torch.randint(0, E, (T, k), device=DEV), torch.rand(T, k, device=DEV) + 0.1
+    out = torch.rand(T, k, device=DEV) < 0.4
+    out[0], out[1] = True, False
+    padded = torch.where(out, torch.where(torch.rand(T, k, device=DEV) < 0.5, -1, E), ids).to(kind)
+    want = m(x, ids, torch.where(out, 0.0, w))
+    for n in (T * k * 2 * I, T * k * H):
+        torch.full((n,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    got = m(x, padded, w)
+    assert torch.equal(got, want) and (got[0] == 0).all() and (got[1] != 0).any()
+
+
 def test_norm_feeds_both_linears():
     """int8 rows into lowbit_linear_a8, e4m3 blocks into lowbit_linear_f8."""
     torch.manual_seed(5)
