@@ -219,8 +219,19 @@ __device__ __attribute__((aligned(16))) const float kNanScales[4] = {
 
 // Block of WN x WM waves over BN columns (n) and BM rows (t) of y.  K steps of
 // 128 go through a ring of S LDS stages, loaded S - 1 steps ahead; a step has
-// one barrier, before which a wave waits for its own loads of that step.
+// one barrier, before which a wave waits for its own loads of that step; the
+// loads of later steps go out behind the step's LDS reads.
 // SPLIT: blockIdx.y takes a run of K blocks and writes fp32 partial sums.
+// Bound by the weights' bytes with few rows (8 rows, 14336 x 4096: 11.2 us, 5.2
+// TB/s), in between by a step's fixed costs: its 1 KiB loads (some 50 cycles of
+// the issuing wave each), LDS reads and barrier, 0.5 to 1.3 us against 0.1 to 0.4
+// of MFMAs (1024 rows, 4096 x 4096, 128 x 128: 27 us, 1.3 PFLOP/s).  Measured and
+// not kept: loads before the LDS reads (64 x 64, 512 rows, 4096 x 4096: 18.1
+// against 17.4), loads between the MFMAs (20.1 against 18.6), a ring of four
+// stages for 128 x 128, which leaves one block a CU (777 rows, 5000 x 4112: 46
+// against 32.5; 1024 rows, 4096 x 4096, one block a CU anyway: 25 against 27), of
+// two for 64 x 64 (64 rows, 14336 x 4096: 20 against 14), 128 x 64 tiles (512
+// rows, 4096 x 4096: 16.8 against 17.3 of 64 x 64; 1024 rows: 31 against 27).
 template <int BN, int BM, int WN, int WM, int S, bool SPLIT, int OUT>
 __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Params p) {
   constexpr bool EXACT = OUT == ACT_F32;
@@ -663,7 +674,8 @@ hipError_t launch_big(LinearF8Params p, hipStream_t s) {
 }
 
 // Sum of the K splits' planes, in their order, and the bias, for the rows of the
-// call (of the experts): four columns a thread.
+// call (of the experts): four columns a thread.  128 x 4096 in four splits: 3.9 us
+// with its launch, of 21.
 template <int OUT>
 __global__ __launch_bounds__(256) void linear_f8_reduce_kernel(LinearF8Params p, int splits) {
   int64_t lo = 0, hi = p.T;
@@ -699,6 +711,9 @@ __global__ __launch_bounds__(256) void linear_f8_reduce_kernel(LinearF8Params p,
 // waves each a run of K blocks; their sums meet in LDS in a fixed order.  The
 // weights go straight from memory to the MFMA operand (a step of a row is 128
 // consecutive bytes, two 16-byte loads of four lanes each), U steps ahead.
+// Bound by the weights' bytes: 64 tokens to 8 of 64 experts, 1408 x 2048, 38.7
+// us, 4.8 TB/s; one row, 8192 x 2048, 5.3 us (a launch that does nothing takes
+// about 2).
 template <int NT, int MT, int W, int U, int OUT>
 __global__ __launch_bounds__(64 * W) void linear_f8_rows_kernel(LinearF8Params p) {
   constexpr bool EXACT = OUT == ACT_F32;
