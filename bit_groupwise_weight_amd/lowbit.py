@@ -568,6 +568,20 @@ def _stream_of(device_index: int, stream) -> int:
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
+def _made_on(shape: Tuple[int, ...], dtype: torch.dtype, x: torch.Tensor, stream) -> torch.Tensor:
+    """An output that a call on `stream` makes, from that stream's memory: what the current stream
+    freed may still be read there by work that the call's stream does not wait for."""
+    if stream is None or not x.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream)
+                  else torch.cuda.default_stream(x.device))
+    if stream.device != x.device:
+        raise ValueError(f"stream is of {stream.device}, the tensors are on {x.device}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=x.device)
+
+
 def _f8_blocks(n: int) -> int:
     return -(-n // F8_BLOCK)
 
@@ -604,7 +618,7 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     if residual is not None:
         _expect_tensor(residual, "residual", (M, K), dt)
         if h is None:
-            h = torch.empty_like(x)
+            h = torch.empty_like(x) if stream is None else _made_on((M, K), dt, x, stream)
         else:
             _expect_tensor(h, "h", (M, K), dt)
     else:
@@ -614,17 +628,17 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
     else:
         code, spans = (torch.int8, (M,)) if fmt == Q8_I8 else (_F8, (M, _f8_blocks(K)))
         if q is None:
-            q = torch.empty_like(x, dtype=code)
+            q = torch.empty_like(x, dtype=code) if stream is None else _made_on((M, K), code, x, stream)
         else:
             _expect_tensor(q, "q", (M, K), code)
         if qscale is None:
-            qscale = torch.empty(spans, dtype=torch.float32, device=x.device)
+            qscale = _made_on(spans, torch.float32, x, stream)
         else:
             _expect_tensor(qscale, "qscale", spans, torch.float32)
     if y is not None:
         _expect_tensor(y, "y", (M, K), dt)
     elif want_y or fmt == Q8_NONE:
-        y = torch.empty_like(x)
+        y = torch.empty_like(x) if stream is None else _made_on((M, K), dt, x, stream)
     dev = _placed(x, weight, residual, q, qscale, h, y)
     st = _call_on(dev, "lowbit_add_rmsnorm_q8", _ptr(x), _ptr(residual), _ptr(weight), eps, _DTYPE_ENUM[dt], M,
                   K, fmt, _ptr(q), _ptr(qscale), _ptr(h), _ptr(y), _stream_of(dev, stream))
@@ -638,20 +652,13 @@ def lowbit_linear_f8_workspace_bytes(M: int, T: int, E: int, N: int, K: int, dty
     return load().lowbit_linear_f8_workspace_bytes(M, T, E, N, K, _DTYPE_ENUM[dtype])
 
 
-def _f8_workspace(dev: int, M: int, T: int, E: int, N: int, K: int, act: int,
+def _f8_workspace(xq: torch.Tensor, M: int, T: int, E: int, N: int, K: int, act: int,
                   stream) -> Optional[torch.Tensor]:
     """A workspace made for one call, on the call's stream: torch's allocator reuses it there only
     (and keeps it for a graph that captures the call), so no two calls or graphs share it."""
     address, fn = _entry("lowbit_linear_f8_workspace_bytes")
     need = fn(M, T, E, N, K, act) if address is None else fn(address, M, T, E, N, K, act)
-    if need == 0:
-        return None
-    if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+    return None if need == 0 else _made_on((need,), torch.uint8, xq, stream)
 
 
 def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
@@ -665,9 +672,9 @@ def lowbit_quantize_act_f8(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
         raise ValueError(f"x dtype {x.dtype} is not float32, float16 or bfloat16")
     M, K = x.shape
     if xq is None:
-        xq = torch.empty_like(x, dtype=_F8)
+        xq = torch.empty_like(x, dtype=_F8) if stream is None else _made_on((M, K), _F8, x, stream)
     if xscale is None:
-        xscale = torch.empty((M, _f8_blocks(K)), dtype=torch.float32, device=x.device)
+        xscale = _made_on((M, _f8_blocks(K)), torch.float32, x, stream)
     _expect_tensor(xq, "xq", (M, K), _F8)
     _expect_tensor(xscale, "xscale", (M, _f8_blocks(K)), torch.float32)
     dev = _placed(x, xq, xscale)
@@ -690,9 +697,9 @@ def lowbit_quantize_weight_f8(w: torch.Tensor, wq: Optional[torch.Tensor] = None
     shape = tuple(w.shape)
     spans = shape[:-2] + (_f8_blocks(N), _f8_blocks(K))
     if wq is None:
-        wq = torch.empty(shape, dtype=_F8, device=w.device)
+        wq = _made_on(shape, _F8, w, stream)
     if wscale is None:
-        wscale = torch.empty(spans, dtype=torch.float32, device=w.device)
+        wscale = _made_on(spans, torch.float32, w, stream)
     _expect_tensor(wq, "wq", shape, _F8)
     _expect_tensor(wscale, "wscale", spans, torch.float32)
     _require_cuda(w, wq, wscale)
@@ -724,7 +731,7 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
     if bias is not None:
         _expect_tensor(bias, "bias", (N,), dtype)
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=xq.device)
+        y = _made_on((M, N), dtype, xq, stream)
     else:
         _expect_tensor(y, "y", (M, N), dtype)
     if workspace is not None and workspace.dtype is not torch.uint8:
@@ -732,7 +739,7 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
     dev = _placed(xq, xscale, wq, wscale, bias, y, workspace)
     act = _DTYPE_ENUM[dtype]
     if workspace is None:
-        workspace = _f8_workspace(dev, M, M, 0, N, K, act, stream)
+        workspace = _f8_workspace(xq, M, M, 0, N, K, act, stream)
     st = _call_on(dev, "lowbit_linear_f8", _ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(y),
                   act, M, N, K, _ptr(workspace), 0 if workspace is None else workspace.numel(),
                   _stream_of(dev, stream))
@@ -772,7 +779,7 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
     if bias is not None:
         _expect_tensor(bias, "bias", (E, N), dtype)
     if y is None:
-        y = torch.empty((T, N), dtype=dtype, device=xq.device)
+        y = _made_on((T, N), dtype, xq, stream)
     else:
         _expect_tensor(y, "y", (T, N), dtype)
     if workspace is not None and workspace.dtype is not torch.uint8:
@@ -780,7 +787,7 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
     dev = _placed(xq, xscale, offsets, wq, wscale, bias, rows, y, workspace)
     act = _DTYPE_ENUM[dtype]
     if workspace is None:
-        workspace = _f8_workspace(dev, M, T, E, N, K, act, stream)
+        workspace = _f8_workspace(xq, M, T, E, N, K, act, stream)
     st = _call_on(dev, "lowbit_linear_f8_grouped", _ptr(xq), _ptr(xscale), _ptr(rows), _ptr(offsets), _ptr(wq),
                   _ptr(wscale), _ptr(bias), _ptr(y), act, M, T, E, N, K, _ptr(workspace),
                   0 if workspace is None else workspace.numel(), _stream_of(dev, stream))

@@ -474,6 +474,53 @@ def test_linear_weight_past_4_gib():
         assert (y == 0).all()
 
 
+@pytest.mark.parametrize("N, K, dtype, gather", [
+    (256, 65664, "bf16", False), (256, 65664, "f32", False), (256, 65664, "bf16", True),   # xq past 4 GiB
+    (40000, 528, "f16", False), (40000, 144, "f16", False)])                               # y past 4 GiB
+def test_linear_rows_past_4_gib(N, K, dtype, gather):
+    """All rows zero but a few, whose exact products appear in their places alone."""
+    M, kb = 66000, -(-K // 128)
+    at = np.array([0, 1, 40000, 65535, 65536, 65600, M - 1])
+    xs_, xsc, wq, ws = exact_inputs(N, len(at), N, K)
+    if K > 8192:                               # sums below 2^24 steps of 2^-6 all the same
+        xs_[:, 200:-200] = 0
+    cols = np.unique(np.concatenate([np.arange(40), np.arange(N - 300, N)])) if N > 256 else None
+    ref, A = o.linear_f8(xs_, xsc, wq, ws, None, *(() if cols is None else (cols,)))
+    assert A.max() < 2 ** 18
+    xq = torch.zeros(M, K, dtype=torch.uint8, device=DEV)
+    xs = torch.ones(M, kb, device=DEV)
+    rows = torch.from_numpy(at).to(DEV)
+    xq[rows] = torch.from_numpy(xs_).to(DEV)
+    xs[rows] = up(xsc)
+    if gather:
+        y = lb.lowbit_linear_f8_grouped(xq.view(F8), xs, up(np.array([0, M], np.int32)), up8(wq[None]), up(ws[None]),
+                                        None, DT[dtype], rows=torch.arange(M, dtype=torch.int32, device=DEV))
+    else:
+        y = lb.lowbit_linear_f8(xq.view(F8), xs, up8(wq), up(ws), None, DT[dtype])
+    got = y[rows] if cols is None else y[rows][:, torch.from_numpy(cols).to(DEV)]
+    assert np.array_equal(f64(got), f64(torch.from_numpy(ref).to(DT[dtype])))
+    y[rows] = 0
+    assert not y.any()
+
+
+def test_norm_and_quantizer_past_4_gib():
+    """Rows on both sides of 2^32 elements: a row's codes are those of the row alone."""
+    M, K = 66000, 65664
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, 32767, 65405, 65406, 65535, M - 1], device=DEV)
+    x[at] = torch.randn(len(at), K, device=DEV).bfloat16()
+    few = x[at]
+    q, s = lb.lowbit_quantize_act_f8(x)
+    q1, s1 = lb.lowbit_quantize_act_f8(few)
+    assert torch.equal(q[at].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[at], s1)
+    assert int((s != 0).any(1).sum()) == len(at)
+    del q, s
+    q, s, h, _ = lb.lowbit_add_rmsnorm_q8(x, None, 1e-5, lb.Q8_F8, residual=x)
+    q1, s1, h1, _ = lb.lowbit_add_rmsnorm_q8(few, None, 1e-5, lb.Q8_F8, residual=few)
+    assert torch.equal(q[at].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[at], s1)
+    assert torch.equal(h[at], h1) and int((s != 0).any(1).sum()) == len(at)
+
+
 # ---------------------------------------------------------------- grouped --
 
 def run_grouped(seed, counts, M, N, K, dtype, gather=True, bias=False, first=0, behind=0, rows=None):
@@ -760,6 +807,33 @@ def test_two_graphs_and_eager_calls_on_two_streams():
         for t in sets:
             for n in OUTS:
                 assert torch.equal(t[n].view(torch.uint8), t["want"][n].view(torch.uint8)), n
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_of_a_call_on_a_stream_spare_the_current_stream(handle):
+    """What the current stream freed while it still reads it is not given to a call on another."""
+    s = torch.cuda.Stream()
+    at = s.cuda_stream if handle else s
+    x = torch.randn(2048, 4096, device=DEV).bfloat16()
+    w = torch.randn(4096, 4096, device=DEV).bfloat16()
+    xq, xs = lb.lowbit_quantize_act_f8(x)
+    wq, ws = lb.lowbit_quantize_weight_f8(w)
+    off = torch.tensor([0, 2048], dtype=torch.int32, device=DEV)
+    calls = [lambda: lb.lowbit_linear_f8(xq, xs, wq, ws, None, torch.bfloat16, stream=at),
+             lambda: lb.lowbit_linear_f8_grouped(xq, xs, off, wq[None], ws[None], None, torch.bfloat16, stream=at),
+             lambda: lb.lowbit_add_rmsnorm_q8(x, None, 1e-5, lb.Q8_F8, residual=x, want_y=True, stream=at),
+             lambda: lb.lowbit_quantize_act_f8(x, stream=at), lambda: lb.lowbit_quantize_weight_f8(w, stream=at)]
+    big = torch.randn(8192, 8192, device=DEV)
+    for call in calls:
+        torch.cuda.synchronize()
+        held = [torch.full((2048, 4096), 2.0, dtype=t, device=DEV) for t in (torch.bfloat16, torch.int8) * 2]
+        slow = big @ big                      # the copies below wait for it
+        copies = [t + 0 * slow[0, 0].nan_to_num(0.0).to(t.dtype) for t in held]
+        del held
+        out = call()
+        torch.cuda.synchronize()
+        assert all((c == 2).all() for c in copies)
+        del out, copies
 
 
 def test_explicit_stream_argument():
