@@ -476,7 +476,7 @@ def test_linear_weight_past_4_gib():
 
 @pytest.mark.parametrize("N, K, dtype, gather", [
     (256, 65664, "bf16", False), (256, 65664, "f32", False), (256, 65664, "bf16", True),   # xq past 4 GiB
-    (40000, 528, "f16", False), (40000, 144, "f16", False)])                               # y past 4 GiB
+    (40000, 1040, "f16", False), (40000, 144, "f16", False)])                              # y past 4 GiB
 def test_linear_rows_past_4_gib(N, K, dtype, gather):
     """All rows zero but a few, whose exact products appear in their places alone."""
     M, kb = 66000, -(-K // 128)
