@@ -241,10 +241,12 @@ struct LinearF8Params {
 };
 // Variants: few rows (16 rows and 16, 32 or 64 columns a block, the weights
 // straight from memory); tiles of columns x rows through LDS, their K range
-// split over the grid where there are few (partial sums in the workspace);
-// and 256 x 256 tiles (16-bit outputs).
+// split between two groups of a block's waves (_K2) and over the grid where
+// there are few (partial sums in the workspace); and 256 x 256 tiles (16-bit
+// outputs).
 enum LinearF8Kind : int {
-  F8_ROWS_NT1, F8_ROWS_NT2, F8_ROWS_NT4, F8_TILE_64X32, F8_TILE_64X64, F8_TILE_128X128, F8_TILE_256X256
+  F8_ROWS_NT1, F8_ROWS_NT2, F8_ROWS_NT4, F8_TILE_64X32, F8_TILE_64X32_K2, F8_TILE_64X64, F8_TILE_64X64_K2,
+  F8_TILE_128X128, F8_TILE_256X256
 };
 struct LinearF8Plan {
   LinearF8Kind kind;

@@ -217,11 +217,16 @@ __device__ __attribute__((aligned(16))) const uint32_t kZeroCodes[4] = {0u, 0u, 
 __device__ __attribute__((aligned(16))) const float kNanScales[4] = {
     __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
 
-// Block of WN x WM waves over BN columns (n) and BM rows (t) of y.  K steps of
-// 128 go through a ring of S LDS stages, loaded S - 1 steps ahead; a step has
+// Block of KG groups of WN x WM waves over BN columns (n) and BM rows (t) of y:
+// each group takes a run of the block's K steps through a ring of its own, and
+// their sums meet in LDS.  K steps of 128 go through a ring of S LDS stages, loaded S - 1 steps ahead; a step has
 // one barrier, before which a wave waits for its own loads of that step; the
 // loads of later steps go out behind the step's LDS reads.
 // SPLIT: blockIdx.y takes a run of K blocks and writes fp32 partial sums.
+// Two groups: the waves of two blocks a CU for tiles of which each CU has one,
+// with no sums in memory to join (us, 64 x 32: 64 rows, 4096 x 4096 9.0 against
+// 10.3 in K splits; 128 rows 9.5 against 11.3; 64 x 64: 200 rows 11.5 against 12.9
+// of 64 x 32; four groups on rings of two stages 10.9 and 12.5).
 // Bound by the weights' bytes with few rows (8 rows, 14336 x 4096: 11.2 us, 5.2
 // TB/s), in between by a step's fixed costs: its 1 KiB loads (some 50 cycles of
 // the issuing wave each), LDS reads and barrier, 0.5 to 1.3 us against 0.1 to 0.4
@@ -232,8 +237,8 @@ __device__ __attribute__((aligned(16))) const float kNanScales[4] = {
 // against 32.5; 1024 rows, 4096 x 4096, one block a CU anyway: 25 against 27), of
 // two for 64 x 64 (64 rows, 14336 x 4096: 20 against 14), 128 x 64 tiles (512
 // rows, 4096 x 4096: 16.8 against 17.3 of 64 x 64; 1024 rows: 31 against 27).
-template <int BN, int BM, int WN, int WM, int S, bool SPLIT, int OUT>
-__global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Params p) {
+template <int BN, int BM, int WN, int WM, int S, int KG, bool SPLIT, int OUT>
+__global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(LinearF8Params p) {
   constexpr bool EXACT = OUT == ACT_F32;
   constexpr int NW = WN * WM;
   constexpr int NT = BN / WN / 16, MT = BM / WM / 16;   // 16-wide tiles of a wave
@@ -244,11 +249,15 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   static_assert((16 * NT) <= kF8Block && kF8Block % (16 * NT) == 0, "a wave's columns share a scale");
   constexpr int STAGE = ROWS * kF8Block;
   constexpr int OUT_BYTES = SPLIT ? 0 : NW * kOutBytes<OUT, NT, MT>;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[S * STAGE > OUT_BYTES ? S * STAGE : OUT_BYTES];
-  __shared__ __attribute__((aligned(1024))) float s_xs[2][64 * NW][4];
+  constexpr int RINGS = KG * S * STAGE;
+  static_assert(KG == 1 || OUT_BYTES + (KG - 1) * NW * NT * MT * 1024 <= RINGS, "room for the groups' sums");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[RINGS > OUT_BYTES ? RINGS : OUT_BYTES];
+  __shared__ __attribute__((aligned(1024))) float s_xs[KG][2][64 * NW][4];
 
   const int lane = threadIdx.x & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wv = wave % NW, kg = wave / NW;
+  uint8_t* const ring = s_mem + kg * (S * STAGE);
   int64_t tile_m;
   int tile_n;
   if (!tile_of_block<BM >= 128 ? 8 : 16>(count_row_tiles<BM>(p), p.tiles_n, &tile_m, &tile_n)) return;
@@ -262,8 +271,11 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   typedef const __attribute__((address_space(4))) float* scalar_floats;
   const scalar_floats ws = (scalar_floats)(p.ws + (static_cast<size_t>(rt.expert) * p.nb +
                             min((n0 + wn * NT * 16) / kF8Block, p.nb - 1)) * p.kb);
-  const int b_begin = SPLIT ? static_cast<int>(blockIdx.y) * p.kb_split : 0;
-  const int b_end = SPLIT ? min(b_begin + p.kb_split, p.kb) : p.kb;
+  const int b_first = SPLIT ? static_cast<int>(blockIdx.y) * p.kb_split : 0;
+  const int b_last = SPLIT ? min(b_first + p.kb_split, p.kb) : p.kb;
+  const int steps = (b_last - b_first + KG - 1) / KG;   // of the block: its barriers
+  const int b_begin = b_first + kg * steps;
+  const int b_end = min(b_begin + steps, b_last);       // (a last group may have none)
 
   // load i of this wave: rows 8 (wv LOADS + i) .. + 7 of the step's BN weight
   // rows and BM activation rows; lane l fills position l % 8 of row l / 8.
@@ -300,8 +312,8 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   const bool xs_ok = from[LOADS] >= 0 && from[LOADS] < p.M;
   const float* xs = p.xs + (xs_ok ? from[LOADS] : 0) * p.kb;
   const int tail = (p.K & (kF8Block - 1)) / 16;         // chunks of a last, partial block (0: none)
-  const uint32_t codes0 = lds_address(s_mem) + wv * LOADS * 8 * kF8Block;
-  const uint32_t xs0 = lds_address(&s_xs[0][0][0]) + wv * 64 * 16;
+  const uint32_t codes0 = lds_address(ring) + wv * LOADS * 8 * kF8Block;
+  const uint32_t xs0 = lds_address(&s_xs[kg][0][0][0]) + wv * 64 * 16;
   auto load_step = [&](int b, int stage) {
     const uint32_t dst = codes0 + stage * STAGE;
     const size_t at = static_cast<size_t>(b) * kF8Block;
@@ -337,8 +349,8 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   const int lo_at = c16 * kF8Block + 16 * (g ^ swizzle(c16));
   const int hi_at = c16 * kF8Block + 16 * ((g + 4) ^ swizzle(c16));
   auto compute = [&](int stage, const float* x_scale, float w_scale, auto&& meanwhile) {
-    const uint8_t* wrow = s_mem + stage * STAGE + wn * NT * 16 * kF8Block;
-    const uint8_t* xrow = s_mem + stage * STAGE + (BN + wm * MT * 16) * kF8Block;
+    const uint8_t* wrow = ring + stage * STAGE + wn * NT * 16 * kF8Block;
+    const uint8_t* xrow = ring + stage * STAGE + (BN + wm * MT * 16) * kF8Block;
     F8Fragment<EXACT> xf[MT];
     float s[MT];
 #pragma unroll
@@ -370,7 +382,7 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   if (p.kb >= 4) {
     load_scales(b_begin, 0);
   } else {                             // rows shorter than one 16-byte load
-    for (int q = 0; q < p.kb; ++q) s_xs[0][64 * wv + lane][q] = xs_ok ? xs[q] : kNanScales[q];
+    for (int q = 0; q < p.kb; ++q) s_xs[kg][0][64 * wv + lane][q] = xs_ok ? xs[q] : kNanScales[q];
   }
 #pragma unroll
   for (int n = 0; n < S - 1; ++n)
@@ -379,19 +391,20 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
   // scale slots are constants
   static_assert(4 % S == 0, "the ring's stages repeat every round");
   int half = 0;
-  for (int q = b_begin; q < b_end; q += 4, half ^= 1) {
-    const float* x_scale = &s_xs[half][0][q - xs_first(q)];
+  for (int q = b_begin; q < b_begin + steps; q += 4, half ^= 1) {
+    const float* x_scale = &s_xs[kg][half][0][q - xs_first(q)];
     float w_scale[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) w_scale[u] = ws[min(q + u, b_end - 1)];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int b = q + u;
-      if (b >= b_end) break;
+      if (b >= b_begin + steps) break;
       // step b has landed (the code loads of the S - 2 steps after it may be in
       // flight, while there are that many) and every wave has read step b - 1
       if (b + S - 1 <= b_end) wait_loads_then_barrier<(S - 2) * LOADS>();
       else wait_loads_then_barrier<0>();
+      if (KG > 1 && b >= b_end) continue;               // (the last group's: only the barrier)
       compute(u % S, x_scale + u, w_scale[u], [&]() {
         if (u == 0 && q + 4 < b_end) load_scales(q + 4, half ^ 1);
         if (b + S - 1 < b_end) load_step(b + S - 1, (u + S - 1) % S);
@@ -399,6 +412,24 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
     }
   }
 
+  if constexpr (KG > 1) {              // the groups' sums meet in the first, in their order
+    wait_loads_then_barrier<0>();      // every wave has read its last stage
+    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(s_mem + OUT_BYTES);
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sums[((((kg - 1) * NW + wv) * NT + i) * MT + j) * 64 + lane] = acc[i][j];
+    }
+    wait_loads_then_barrier<0>();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 1; k < KG; ++k)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] += sums[((((k - 1) * NW + wv) * NT + i) * MT + j) * 64 + lane];
+  }
   if constexpr (SPLIT) {
     // planes of T rows of n_pad (a multiple of 4) columns
 #pragma unroll
@@ -412,7 +443,7 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_f8_tile_kernel(LinearF8Pa
       }
     }
   } else {
-    wait_loads_then_barrier<0>();      // every wave has read the last stage
+    if constexpr (KG == 1) wait_loads_then_barrier<0>();    // every wave has read the last stage
     store_outputs<OUT>(p, acc, s_mem + wv * kOutBytes<OUT, NT, MT>, rt.expert, rt.begin + wm * MT * 16, rt.end,
                        n0 + wn * NT * 16);
   }
@@ -848,17 +879,17 @@ hipError_t launch_rows(LinearF8Params p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int BN, int BM, int WN, int WM, int S, int OUT>
+template <int BN, int BM, int WN, int WM, int S, int KG, int OUT>
 hipError_t launch_tile(LinearF8Params p, int splits, hipStream_t s) {
   p.tiles_n = (p.N + BN - 1) / BN;
   // row tiles: with experts, each adds less than one tile to T / BM
   int64_t tiles_m = (p.T + BM - 1) / BM;
   if (p.offsets) tiles_m = p.T / BM + (p.T < p.E ? p.T : p.E);
   const int64_t blocks = tiles_m * p.tiles_n;
-  if (blocks > 0x7fffffff / (64 * WN * WM)) return hipErrorInvalidConfiguration;
-  const dim3 block(64 * WN * WM);
+  if (blocks > 0x7fffffff / (64 * WN * WM * KG)) return hipErrorInvalidConfiguration;
+  const dim3 block(64 * WN * WM * KG);
   if (splits <= 1) {
-    linear_f8_tile_kernel<BN, BM, WN, WM, S, false, OUT>
+    linear_f8_tile_kernel<BN, BM, WN, WM, S, KG, false, OUT>
         <<<dim3(static_cast<unsigned>(blocks)), block, 0, s>>>(p);
     return hipGetLastError();
   }
@@ -867,7 +898,7 @@ hipError_t launch_tile(LinearF8Params p, int splits, hipStream_t s) {
   p.kb_split = (p.kb + splits - 1) / splits;
   splits = (p.kb + p.kb_split - 1) / p.kb_split;
   p.n_pad = (p.N + 3) / 4 * 4;
-  linear_f8_tile_kernel<BN, BM, WN, WM, S, true, OUT>
+  linear_f8_tile_kernel<BN, BM, WN, WM, S, KG, true, OUT>
       <<<dim3(static_cast<unsigned>(blocks), splits), block, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -882,9 +913,11 @@ hipError_t launch_out(const LinearF8Params& p, const LinearF8Plan& plan, hipStre
     case F8_ROWS_NT1: return launch_rows<1, 1, 8, 2, OUT>(p, s);
     case F8_ROWS_NT2: return launch_rows<2, 1, 8, 1, OUT>(p, s);
     case F8_ROWS_NT4: return launch_rows<4, 1, 4, 1, OUT>(p, s);
-    case F8_TILE_64X32: return launch_tile<64, 32, 4, 1, 4, OUT>(p, plan.splits, s);
-    case F8_TILE_64X64: return launch_tile<64, 64, 2, 2, 4, OUT>(p, plan.splits, s);
-    case F8_TILE_128X128: return launch_tile<128, 128, 2, 4, 2, OUT>(p, plan.splits, s);
+    case F8_TILE_64X32: return launch_tile<64, 32, 4, 1, 4, 1, OUT>(p, plan.splits, s);
+    case F8_TILE_64X32_K2: return launch_tile<64, 32, 4, 1, 4, 2, OUT>(p, plan.splits, s);
+    case F8_TILE_64X64: return launch_tile<64, 64, 2, 2, 4, 1, OUT>(p, plan.splits, s);
+    case F8_TILE_64X64_K2: return launch_tile<64, 64, 2, 2, 4, 2, OUT>(p, plan.splits, s);
+    case F8_TILE_128X128: return launch_tile<128, 128, 2, 4, 2, 1, OUT>(p, plan.splits, s);
     default:
       if constexpr (OUT == ACT_F32) return hipErrorInvalidValue;
       else return launch_big<OUT>(p, s);

@@ -575,33 +575,40 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 //   48 of 32 columns; 16, 28672, 4096: 27 against 30);
 // - 32 columns from 7/8 on (8, 8192, 2048: 5.7 against 6.3 of 16; 8, 4096, 4096,
 //   half a block: 8.1 against 6.7);
-// - 64 x 32 tiles, whose loads are further ahead, where they are 3/4 of a block
-//   to one a CU (8, 14336, 4096: 11.2 against 12.5; 8, 8192, 2048, half a block:
-//   6.8 against 5.7) and K is not long (8, 28672, 8192: 47 against 46);
+// - 64 x 32 tiles, whose loads are further ahead, where they are 2/3 of a block
+//   to one a CU (16, 14336, 4096: 11.5 against 13.3; 1 x 8 of 64, 1408, 2048: 8.0
+//   against 8.5; 8, 4096, 4096, 1/4 of a block: 8.8 against 6.7) and K is not
+//   long (8, 28672, 8192: 47 against 46);
 // - 16 columns read more activations than they can hide from 9 rows on where K
 //   is long (16, 4096, 14336: 18.4 against 14.4 of 64 x 32 tiles in splits).
 //
 // All other calls take the cheapest of the tiles by an estimate: a CU runs one
-// block's K step in `one`, the steps of two blocks in `two` (us, from 48 single
-// runs of each tile); splits of K of at least four steps add the write and the
-// read of their partial sums and a launch; weights come at 5 TB/s at best.  Over
-// 113 shapes (1 to 8192 rows, K of 1024 to 16384, dense and grouped) its choice
-// was 3 % (root mean square) slower than the fastest variant, 15 % at worst.
-// Where it changes over: 512, 4096, 4096: 17.4 of 64 x 64 against 25.6 of
-// 128 x 128; 1024, 4096, 4096: 33 against 27; 3000, 4096, 4096: 51 of 256 x 256
-// against 59; 2048, 4096, 4096: 50 against 37; 128, 4096, 14336 in 64 x 64
-// tiles: 20.6 in four splits against 51 in one.
+// block's K step in `one`, the steps of two blocks (or of two groups of waves of
+// one) in `two`; splits of K of at least four steps add the write and the read of
+// their partial sums and a launch; weights come at 5 TB/s at best.  The figures
+// (us) are fitted to forced runs of 94 shapes (1 to 8192 rows, K of 1024 to
+// 14336, dense and grouped), over which the choice is 3 % (root mean square)
+// slower than the fastest variant, 18 % at worst (17, 1024, 1024: 4.5 against
+// 3.8).  Where it changes over: 128, 4096, 4096: 9.5 of 64 x 32 in two groups
+// against 11.1 of 64 x 64; 256, 4096, 4096: 16.8 against 11.6; 384, 4096, 4096:
+// 20.6 of 64 x 64 in two groups against 16.3 in one; 512, 4096, 4096: 17.3 of 64 x
+// 64 against 25.6 of 128 x 128; 1024, 4096, 4096: 32 against 27; 3000, 4096, 4096:
+// 51 of 256 x 256 against 59; 2048, 4096, 4096: 50 against 37; 128, 4096, 14336 in
+// 64 x 64 tiles: 20.1 in four splits against 51 in one.
 struct F8TileRate {
   lowbit::LinearF8Kind kind;
-  int bn, bm;
+  int bn, bm, groups;
   double one, two;
 };
-constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 0.31, 0.38},
-                                   {lowbit::F8_TILE_64X64, 64, 64, 0.50, 0.54},
-                                   {lowbit::F8_TILE_128X128, 128, 128, 1.00, 1.34}};
-constexpr double kF8JoinUs = 3.2, kF8JoinUsPerByte = 0.48e-6, kF8BytesPerUs = 5e6;
+constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 1, 0.35, 0.45},
+                                   {lowbit::F8_TILE_64X64, 64, 64, 1, 0.46, 0.67},
+                                   {lowbit::F8_TILE_128X128, 128, 128, 1, 1.01, 1.31},
+                                   {lowbit::F8_TILE_64X32_K2, 64, 32, 2, 0.45, 0.45},
+                                   {lowbit::F8_TILE_64X64_K2, 64, 64, 2, 0.67, 0.67}};
+constexpr double kF8JoinUs = 3.9, kF8JoinUsPerByte = 0.55e-6, kF8BytesPerUs = 5e6;
+constexpr double kF8GroupsUs = 0.3;    // the sums of two groups
 // 256 x 256: one block a CU, a round's start and end, a step of few and of all CUs
-constexpr double kF8BigUs = 5.5, kF8BigStep = 1.35, kF8BigFullStep = 1.70;
+constexpr double kF8BigUs = 6.9, kF8BigStep = 1.47, kF8BigFullStep = 1.88;
 constexpr int kF8MaxSplits = 16, kF8MinSplitSteps = 4;
 lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64_t N, int64_t K,
                              lowbit_dtype dtype) {
@@ -612,7 +619,7 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   const int64_t per = (T + used - 1) / used;            // rows of one, on average
   if (per <= (grouped ? 10 : 16)) {
     const int64_t units = used * ((N + 15) / 16), wide = used * ((N + 63) / 64);
-    if (wide * 4 >= cus * 3 && wide <= cus && kb < 64) return {F8_TILE_64X32, 1};
+    if (wide * 3 >= cus * 2 && wide <= cus && kb < 64) return {F8_TILE_64X32_K2, 1};
     if (units >= 4 * (cus * 7 / 4)) return {F8_ROWS_NT4, 1};
     if (units >= 2 * (cus * 7 / 8)) return {F8_ROWS_NT2, 1};
     if (per <= 8 || kb < 64) return {F8_ROWS_NT1, 1};
@@ -631,10 +638,17 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
     for (int splits = 1; splits <= kF8MaxSplits; ++splits) {
       const int64_t steps = (kb + splits - 1) / splits;
       if (splits > 1 && (kb < int64_t{kF8MinSplitSteps} * splits || (kb + steps - 1) / steps != splits)) continue;
-      const double n = blocks * splits, rest = n - 2 * std::floor(n / 2);
-      double us = std::floor(n / 2) * t.two;
-      if (rest > 0) us += t.one + std::max(rest - 1, 0.0) * (t.two - t.one);
-      us *= static_cast<double>(steps);
+      const double n = blocks * splits;
+      double us;
+      if (t.groups == 1) {
+        const double rest = n - 2 * std::floor(n / 2);
+        us = std::floor(n / 2) * t.two;
+        if (rest > 0) us += t.one + std::max(rest - 1, 0.0) * (t.two - t.one);
+        us *= static_cast<double>(steps);
+      } else {                           // (eight steps or more)
+        if (kb < int64_t{8} * splits) continue;
+        us = std::ceil(n) * t.two * static_cast<double>((steps + 1) / 2) + kF8GroupsUs;
+      }
       if (splits > 1)
         us = std::max(us, codes / kF8BytesPerUs) + kF8JoinUs +
              kF8JoinUsPerByte * 4 * splits * static_cast<double>(T) * static_cast<double>(N);
