@@ -705,8 +705,9 @@ hipError_t launch_big(LinearF8Params p, hipStream_t s) {
 }
 
 // Sum of the K splits' planes, in their order, and the bias, for the rows of the
-// call (of the experts): four columns a thread.  128 x 4096 in four splits: 3.9 us
-// with its launch, of 21.
+// call (of the experts): four columns a thread.  128 x 4096 in two splits: 4.0 us
+// of 21, most of it a launch (four planes' loads in flight at once and 32-bit
+// indexes: 3.9).
 template <int OUT>
 __global__ __launch_bounds__(256) void linear_f8_reduce_kernel(LinearF8Params p, int splits) {
   int64_t lo = 0, hi = p.T;
