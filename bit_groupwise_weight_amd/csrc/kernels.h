@@ -246,7 +246,7 @@ struct LinearF8Params {
 // outputs).
 enum LinearF8Kind : int {
   F8_ROWS_NT1, F8_ROWS_NT2, F8_ROWS_NT4, F8_TILE_64X32, F8_TILE_64X32_K2, F8_TILE_64X64, F8_TILE_64X64_K2,
-  F8_TILE_128X128, F8_TILE_256X256
+  F8_TILE_128X128, F8_TILE_128X128_K2, F8_TILE_256X256
 };
 struct LinearF8Plan {
   LinearF8Kind kind;

@@ -226,11 +226,12 @@ __device__ __attribute__((aligned(16))) const float kNanScales[4] = {
 // Two groups: the waves of two blocks a CU for tiles of which each CU has one,
 // with no sums in memory to join (us, 64 x 32: 64 rows, 4096 x 4096 9.0 against
 // 10.3 in K splits; 128 rows 9.5 against 11.3; 64 x 64: 200 rows 11.5 against 12.9
-// of 64 x 32; four groups on rings of two stages 10.9 and 12.5).
+// of 64 x 32; four groups on rings of two stages 10.9 and 12.5; 128 x 128: 600
+// rows 21.8 against 25.7, 1024 rows 24.4 against 27.2).
 // Bound by the weights' bytes with few rows (8 rows, 14336 x 4096: 11.2 us, 5.2
 // TB/s), in between by a step's fixed costs: its 1 KiB loads (some 50 cycles of
 // the issuing wave each), LDS reads and barrier, 0.5 to 1.3 us against 0.1 to 0.4
-// of MFMAs (1024 rows, 4096 x 4096, 128 x 128: 27 us, 1.3 PFLOP/s).  Measured and
+// of MFMAs (1024 rows, 4096 x 4096, 128 x 128: 24 us, 1.4 PFLOP/s).  Measured and
 // not kept: loads before the LDS reads (64 x 64, 512 rows, 4096 x 4096: 18.1
 // against 17.4), loads between the MFMAs (20.1 against 18.6), a ring of four
 // stages for 128 x 128, which leaves one block a CU (777 rows, 5000 x 4112: 46
@@ -245,14 +246,14 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(Linea
   constexpr int ROWS = BN + BM;
   constexpr int LOADS = ROWS / 8 / NW;                  // 1 KiB loads of a wave per step
   static_assert(ROWS % (8 * NW) == 0 && BN % 8 == 0, "whole loads");
-  static_assert(BM <= 64 * NW, "one scale load a wave");
+  constexpr int XROWS = BM > 64 ? BM : 64;              // rows of scales: one load of a wave each 64
+  static_assert(XROWS % 64 == 0 && XROWS <= 64 * NW, "one scale load a wave");
   static_assert((16 * NT) <= kF8Block && kF8Block % (16 * NT) == 0, "a wave's columns share a scale");
   constexpr int STAGE = ROWS * kF8Block;
   constexpr int OUT_BYTES = SPLIT ? 0 : NW * kOutBytes<OUT, NT, MT>;
-  constexpr int RINGS = KG * S * STAGE;
-  static_assert(KG == 1 || OUT_BYTES + (KG - 1) * NW * NT * MT * 1024 <= RINGS, "room for the groups' sums");
-  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[RINGS > OUT_BYTES ? RINGS : OUT_BYTES];
-  __shared__ __attribute__((aligned(1024))) float s_xs[KG][2][64 * NW][4];
+  constexpr int RINGS = KG * S * STAGE, AFTER = OUT_BYTES + (KG - 1) * NW * NT * MT * 1024;   // (groups' sums)
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[RINGS > AFTER ? RINGS : AFTER];
+  __shared__ __attribute__((aligned(1024))) float s_xs[KG][2][XROWS][4];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -279,8 +280,8 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(Linea
 
   // load i of this wave: rows 8 (wv LOADS + i) .. + 7 of the step's BN weight
   // rows and BM activation rows; lane l fills position l % 8 of row l / 8.
-  // The scale load's lane takes row 64 wv + lane (rows past BM: padding of
-  // s_xs).  Rows past the tile's end are its last row again.
+  // The scale load's lane takes row 64 wv + lane, in the first waves (rows past
+  // BM: padding of s_xs).  Rows past the tile's end are its last row again.
   int64_t from[LOADS + 1];
   int chunk[LOADS];
 #pragma unroll
@@ -333,8 +334,9 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(Linea
   // every lane reads a line of its own): one 16-byte load a lane, shifted back
   // inside the row at its end.
   auto xs_first = [&](int q) { return max(min(q, p.kb - 4), 0); };
+  const bool has_xs = wv < XROWS / 64;
   auto load_scales = [&](int q, int half) {
-    dma16(xs_ok ? xs + xs_first(q) : kNanScales, xs0 + half * (64 * NW * 16));
+    if (has_xs) dma16(xs_ok ? xs + xs_first(q) : kNanScales, xs0 + half * (XROWS * 16));
   };
 
   const int c16 = lane & 15, g = lane >> 4;
@@ -381,7 +383,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(Linea
 
   if (p.kb >= 4) {
     load_scales(b_begin, 0);
-  } else {                             // rows shorter than one 16-byte load
+  } else if (has_xs) {                 // rows shorter than one 16-byte load
     for (int q = 0; q < p.kb; ++q) s_xs[kg][0][64 * wv + lane][q] = xs_ok ? xs[q] : kNanScales[q];
   }
 #pragma unroll
@@ -705,9 +707,8 @@ hipError_t launch_big(LinearF8Params p, hipStream_t s) {
 }
 
 // Sum of the K splits' planes, in their order, and the bias, for the rows of the
-// call (of the experts): four columns a thread.  128 x 4096 in two splits: 4.0 us
-// of 21, most of it a launch (four planes' loads in flight at once and 32-bit
-// indexes: 3.9).
+// call (of the experts): four columns a thread.  128 x 4096 in four splits: 3.9 us
+// of 21, most of it a launch (in two: 4.0).
 template <int OUT>
 __global__ __launch_bounds__(256) void linear_f8_reduce_kernel(LinearF8Params p, int splits) {
   int64_t lo = 0, hi = p.T;
@@ -919,8 +920,9 @@ hipError_t launch_out(const LinearF8Params& p, const LinearF8Plan& plan, hipStre
     case F8_TILE_64X64: return launch_tile<64, 64, 2, 2, 4, 1, OUT>(p, plan.splits, s);
     case F8_TILE_64X64_K2: return launch_tile<64, 64, 2, 2, 4, 2, OUT>(p, plan.splits, s);
     case F8_TILE_128X128: return launch_tile<128, 128, 2, 4, 2, 1, OUT>(p, plan.splits, s);
-    default:
+    default:                           // 16-bit outputs
       if constexpr (OUT == ACT_F32) return hipErrorInvalidValue;
+      else if (plan.kind == F8_TILE_128X128_K2) return launch_tile<128, 128, 2, 4, 2, 2, OUT>(p, plan.splits, s);
       else return launch_big<OUT>(p, s);
   }
 }

@@ -586,29 +586,31 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 // block's K step in `one`, the steps of two blocks (or of two groups of waves of
 // one) in `two`; splits of K of at least four steps add the write and the read of
 // their partial sums and a launch; weights come at 5 TB/s at best.  The figures
-// (us) are fitted to forced runs of 94 shapes (1 to 8192 rows, K of 1024 to
-// 14336, dense and grouped), over which the choice is 3 % (root mean square)
-// slower than the fastest variant, 18 % at worst (17, 1024, 1024: 4.5 against
-// 3.8).  Where it changes over: 128, 4096, 4096: 9.5 of 64 x 32 in two groups
-// against 11.1 of 64 x 64; 256, 4096, 4096: 16.8 against 11.6; 384, 4096, 4096:
-// 20.6 of 64 x 64 in two groups against 16.3 in one; 512, 4096, 4096: 17.3 of 64 x
-// 64 against 25.6 of 128 x 128; 1024, 4096, 4096: 32 against 27; 3000, 4096, 4096:
-// 51 of 256 x 256 against 59; 2048, 4096, 4096: 50 against 37; 128, 4096, 14336 in
-// 64 x 64 tiles: 20.1 in four splits against 51 in one.
+// (us) are fitted to forced runs of 100 shapes (1 to 8192 rows, K of 1024 to
+// 14336, dense and grouped), over which the choice is 2.4 % (root mean square)
+// slower than the fastest variant, 13 % at worst (17, 1024, 1024: 4.4 against
+// 3.9).  Where it changes over: 128, 4096, 4096: 9.4 of 64 x 32 in two groups
+// against 11.1 of 64 x 64; 256, 4096, 4096: 16.9 against 11.5; 384, 4096, 4096:
+// 20.6 of 64 x 64 in two groups against 16.3 in one; 512, 4096, 4096: 16.8 of 64 x
+// 64 against 21.9 of 128 x 128 in two groups; 600, 4096, 4096: 26.0 against 21.8;
+// 1500, 4096, 4096: 32 of 128 x 128 in one group against 49 of 256 x 256; 3000,
+// 4096, 4096: 59 against 51; 128, 4096, 14336 in 64 x 64 tiles of one group: 20.4
+// in four splits against 51 in one.
 struct F8TileRate {
   lowbit::LinearF8Kind kind;
   int bn, bm, groups;
   double one, two;
 };
-constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 1, 0.35, 0.45},
-                                   {lowbit::F8_TILE_64X64, 64, 64, 1, 0.46, 0.67},
-                                   {lowbit::F8_TILE_128X128, 128, 128, 1, 1.01, 1.31},
-                                   {lowbit::F8_TILE_64X32_K2, 64, 32, 2, 0.45, 0.45},
-                                   {lowbit::F8_TILE_64X64_K2, 64, 64, 2, 0.67, 0.67}};
-constexpr double kF8JoinUs = 3.9, kF8JoinUsPerByte = 0.55e-6, kF8BytesPerUs = 5e6;
-constexpr double kF8GroupsUs = 0.3;    // the sums of two groups
+constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 1, 0.36, 0.46},
+                                   {lowbit::F8_TILE_64X64, 64, 64, 1, 0.51, 0.57},
+                                   {lowbit::F8_TILE_128X128, 128, 128, 1, 1.04, 1.29},
+                                   {lowbit::F8_TILE_64X32_K2, 64, 32, 2, 0.51, 0.51},
+                                   {lowbit::F8_TILE_64X64_K2, 64, 64, 2, 0.72, 0.72},
+                                   {lowbit::F8_TILE_128X128_K2, 128, 128, 2, 1.64, 1.64}};
+constexpr double kF8JoinUs = 4.57, kF8JoinUsPerByte = 0.63e-6, kF8BytesPerUs = 5e6;
+constexpr double kF8GroupsUs = 0.27;   // the sums of two groups
 // 256 x 256: one block a CU, a round's start and end, a step of few and of all CUs
-constexpr double kF8BigUs = 6.9, kF8BigStep = 1.47, kF8BigFullStep = 1.88;
+constexpr double kF8BigUs = 6.85, kF8BigStep = 1.28, kF8BigFullStep = 1.65;
 constexpr int kF8MaxSplits = 16, kF8MinSplitSteps = 4;
 lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64_t N, int64_t K,
                              lowbit_dtype dtype) {
@@ -634,6 +636,8 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   LinearF8Plan plan{F8_TILE_64X32, 1};
   double best = std::numeric_limits<double>::infinity();
   for (const F8TileRate& t : kF8Tiles) {
+    // (16 waves have 128 registers each: too few for fp32's bf16 copies of the codes)
+    if (t.kind == F8_TILE_128X128_K2 && dtype == LOWBIT_F32) continue;
     const double blocks = load(t.bn, t.bm);
     for (int splits = 1; splits <= kF8MaxSplits; ++splits) {
       const int64_t steps = (kb + splits - 1) / splits;

@@ -104,12 +104,12 @@ def test_linear_f8_grouped_validation(lowbit_lib, kw, status):
 
 @pytest.mark.parametrize("M, T, E, N, K, dtype, splits", [
     (1, 1, 0, 14336, 4096, "bf16", 0),        # few rows: no workspace
-    (64, 64, 0, 4096, 14336, "bf16", 2),      # tiles of 64 columns
-    (128, 128, 0, 4096, 14336, "f32", 2),
+    (64, 64, 0, 4096, 14336, "bf16", 4),      # tiles of 64 columns
+    (128, 128, 0, 4096, 14336, "f32", 4),
     (20, 20, 0, 4096, 4096, "f16", 0),
     (8192, 8192, 0, 14336, 4096, "bf16", 0),  # 256 x 256: none
-    (64, 64, 0, 4098, 14336, "bf16", 3),      # planes padded to a multiple of 4 columns
-    (30, 60, 2, 1024, 8192, "bf16", 5),       # grouped: planes of T rows
+    (64, 64, 0, 4098, 14336, "bf16", 5),      # planes padded to a multiple of 4 columns
+    (30, 60, 2, 1024, 8192, "bf16", 6),       # grouped: planes of T rows
     (4, 0, 2, 64, 256, "bf16", 0), (4, 4, 0, 64, 40, "bf16", 0),
 ])
 def test_workspace_bytes(lowbit_lib, M, T, E, N, K, dtype, splits):

@@ -332,13 +332,14 @@ def test_linear_exact(M, N, K):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("M, N, K", [
-    (12, 300, 8336), (20, 300, 4096), (31, 2000, 8208), (70, 300, 8208), # K splits
+    (12, 300, 8336), (20, 300, 4096), (31, 2000, 8208), (70, 300, 8208),     # K splits
     (512, 2050, 14336), (300, 4608, 3600),                # 128 x 128 tiles, in splits and whole
     (300, 28700, 272), (257, 28673, 16), (300, 28700, 400), (259, 28700, 8336), (512, 14336, 528),  # 256 x 256
     (1100, 14340, 1168), (300, 28700, 528), (600, 14340, 1040), (600, 14340, 1168), (4100, 16400, 144), (700, 28700, 656),
     (8192, 8192, 16), (300, 8200, 8208),
     (4, 11000, 16), (8, 12000, 144), (15, 14001, 272), (9, 13000, 1168),      # two groups of waves, odd K blocks
-    (33, 4100, 1552), (130, 4000, 1296), (250, 4000, 1552), (128, 1030, 2064),
+    (33, 4100, 1552), (130, 4000, 1296), (250, 4000, 1552), (128, 1030, 2064), (250, 4000, 2064),
+    (600, 4000, 4112), (700, 4000, 3088),
 ])
 def test_linear_variants(M, N, K, dtype):
     """Every kernel variant at ragged edges: exact inputs, every column near a tile's edge and a
@@ -586,6 +587,7 @@ def test_grouped_exact_and_equal_to_dense(counts):
 @pytest.mark.parametrize("counts, N, K", [
     ([30, 0, 25], 200, 4112), ([60, 0, 70], 300, 2064),   # K splits, 64 x 32 and 64 x 64
     ([100, 0, 61, 70], 2056, 2064), ([30, 9, 0, 52], 2056, 1552),             # two groups of waves
+    ([400, 0, 500], 4000, 4112),
     ([200, 100, 0, 130], 6000, 272),                      # 128 x 128
     ([200, 100, 0, 290], 4100, 8208),                     # 128 x 128 in splits
     ([300, 260, 0, 208], 14356, 400), ([257, 1, 600, 0, 300], 14356, 144),
