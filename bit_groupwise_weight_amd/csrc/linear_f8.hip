@@ -458,7 +458,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(Linea
 // past the descriptor's end and read nothing.
 // A step has 2048 MFMA cycles a CU and as many of LDS traffic (192 KiB read, 64
 // KiB written, 128 bytes a cycle), and a scaling FMA a product in the MFMAs'
-// shadow.  8192 rows of K = 4096 into N = 14336: 421-435 us, 2.2-2.3 PFLOP/s
+// shadow.  8192 rows of K = 4096 into N = 14336: 421-429 us, 2.2-2.3 PFLOP/s
 // (a large unscaled e4m3 library product: 2.9-3.2); 352 us on codes of zero: the
 // rest is the clock that the card's power leaves (1.8 to 2.0 of 2.4 GHz).  What
 // each form measured (us, one box): one barrier a step and loads in pairs 452, a
