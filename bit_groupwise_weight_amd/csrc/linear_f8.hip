@@ -461,7 +461,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void linear_f8_tile_kernel(Linea
 // shadow.  8192 rows of K = 4096 into N = 14336: 421-429 us, 2.2-2.3 PFLOP/s
 // (a large unscaled e4m3 library product: 2.9-3.2); 352 us on codes of zero: the
 // rest is the clock that the card's power leaves (1.8 to 2.0 of 2.4 GHz).  What
-// each form measured (us, one box): one barrier a step and loads in pairs 452, a
+// each form measured (us, one card): one barrier a step and loads in pairs 452, a
 // load a tile 436; without loads 354.  MFMAs of 32 x 32 x 64 are no faster beside
 // the FMAs (registers only: 3.45 PFLOP/s against 3.80).
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));

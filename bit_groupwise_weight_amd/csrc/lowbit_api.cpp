@@ -564,7 +564,7 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 
 // Variant and K split of a block-scaled e4m3 product: T rows of y, E experts
 // (0: dense), rows of xq gathered from M.  Times: us on MI355X, bf16 outputs,
-// the variants forced in turn on one box (M, N, K; "64 x 8 of 64" is 64 tokens
+// the variants forced in turn on one card (M, N, K; "64 x 8 of 64" is 64 tokens
 // to 8 of 64 experts each).
 //
 // Up to 16 rows (10 an expert on average: grouped rows are uneven, and a second
