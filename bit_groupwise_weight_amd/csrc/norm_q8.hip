@@ -235,6 +235,8 @@ hipError_t launch_norm_rows(const NormQ8Params& p, hipStream_t s) {
 //   K = 512     64 x 1: 12.4 / 2.4     256 x 1: 19.9 / 2.5     (16384 rows)
 //   K = 1024    64 x 2: 25.9 / 3.2     256 x 1: 30.8 / 2.5     (16384 rows)
 //   K = 2048   256 x 1: 24.3 / 2.6     512 x 1: 30.7 / 2.6     (8192 rows)
+//   K = 2080   512 x 1: 32.9 / 2.6     256 x 2: 29.0 / 3.4     (8192 rows; few
+//              rows went first: the share of a short step is larger)
 //   K = 4096   512 x 1: 44.4 / 2.7     256 x 2: 46.9 / 3.5     (8192 rows)
 //   K = 8192  1024 x 1: 45.0 / 3.1     512 x 2: 46.9 / 3.6     (4096 rows)
 //   K = 14336 1024 x 2: 24.4 / 3.6     512 x 4: 22.0 / 4.0     (2048 rows, int8)
