@@ -713,6 +713,36 @@ def test_experts_leave_padded_slots_out(kind):
     assert torch.equal(got, want) and (got[0] == 0).all() and (got[1] != 0).any()
 
 
+@pytest.mark.parametrize("T", [1, 40, 700, 20000])
+def test_experts_in_a_graph(T):
+    """Replays with other tokens and routings, eager calls between them: each equal to the eager call."""
+    torch.manual_seed(T)
+    E, H, I, k = 16, 272, 144, 4
+    m = lnn.F8Experts(E, H, I, device=DEV).set_weight(torch.randn(E, 2 * I, H, device=DEV) * 0.06,
+                                                      torch.randn(E, H, I, device=DEV) * 0.08)
+
+    def inputs():
+        return (torch.randn(T, H, device=DEV).bfloat16(), torch.randint(-1, E, (T, k), device=DEV),
+                torch.rand(T, k, device=DEV))
+
+    x, ids, w = inputs()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        m(x, ids, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = m(x, ids, w)
+    for _ in range(6):
+        new = inputs()
+        for t, n in zip((x, ids, w), new):
+            t.copy_(n)
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, m(*new))
+
+
 def test_norm_feeds_both_linears():
     """int8 rows into lowbit_linear_a8, e4m3 blocks into lowbit_linear_f8."""
     torch.manual_seed(5)
