@@ -85,7 +85,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_q8_kernel(NormQ8Params
   __shared__ uint32_t s_max[2][T / 64];
   const int64_t m = T == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (T == 64 && m >= p.M) return;     // (no barrier in that form)
-  const int tid = threadIdx.x & (T - 1);
+  const int tid = T == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int chunks = p.K / 8;
   const int n = C ? C : (chunks + T - 1) / T;           // chunks of a thread, past the row's end included
   const size_t row_bytes = static_cast<size_t>(p.K) * Act<ACT>::bytes;
@@ -235,8 +235,9 @@ hipError_t launch_norm_rows(const NormQ8Params& p, hipStream_t s) {
 //   K = 512     64 x 1: 12.4 / 2.4     256 x 1: 19.9 / 2.5     (16384 rows)
 //   K = 1024    64 x 2: 25.9 / 3.2     256 x 1: 30.8 / 2.5     (16384 rows)
 //   K = 2048   256 x 1: 24.3 / 2.6     512 x 1: 30.7 / 2.6     (8192 rows)
-//   K = 2080   512 x 1: 32.9 / 2.6     256 x 2: 29.0 / 3.4     (8192 rows; few
-//              rows went first: the share of a short step is larger)
+//   K = 2080   320 x 1: 27.9 / 2.6     512 x 1: 32.1 / 2.6     (8192 rows)
+//   K = 2560   320 x 1: 30.5 / 2.6     512 x 1: 33.9 / 2.6     (8192 rows; 640 for
+//              K = 5120 gained 3 % over 1024 and was left out)
 //   K = 4096   512 x 1: 44.4 / 2.7     256 x 2: 46.9 / 3.5     (8192 rows)
 //   K = 8192  1024 x 1: 45.0 / 3.1     512 x 2: 46.9 / 3.6     (4096 rows)
 //   K = 14336 1024 x 2: 24.4 / 3.6     512 x 4: 22.0 / 4.0     (2048 rows, int8)
@@ -247,6 +248,7 @@ hipError_t launch_norm(const NormQ8Params& p, hipStream_t s) {
   if (p.K <= 512) return launch_norm_rows<ACT, FMT, 64, 1>(p, s);
   if (p.K <= 1024) return launch_norm_rows<ACT, FMT, 64, 2>(p, s);
   if (p.K <= 2048) return launch_norm_rows<ACT, FMT, 256, 1>(p, s);
+  if (p.K <= 2560) return launch_norm_rows<ACT, FMT, 320, 1>(p, s);
   if (p.K <= 4096) return launch_norm_rows<ACT, FMT, 512, 1>(p, s);
   if (p.K <= 8192) return launch_norm_rows<ACT, FMT, 1024, 1>(p, s);
   if (p.K <= 16384) return launch_norm_rows<ACT, FMT, 1024, 2>(p, s);

@@ -177,7 +177,7 @@ def check_norm(x, r, g, eps, fmt, q, s, h, y, dtype):
         assert np.all(np.abs(c).max(1) == top)       # the largest value takes the largest code
 
 
-NORM_K = [16, 32, 128, 160, 512, 544, 1024, 1040, 2048, 2080, 4096, 4112, 8192, 8224, 14336, 16384, 16416,
+NORM_K = [16, 32, 128, 160, 512, 544, 1024, 1040, 2048, 2080, 2560, 2576, 4096, 4112, 8192, 8224, 14336, 16384, 16416,
           32768, 32800, 40960]
 
 
@@ -200,7 +200,7 @@ def test_norm(dtype, fmt, K):
 
 
 @pytest.mark.parametrize("fmt", [lb.Q8_I8, lb.Q8_F8])
-@pytest.mark.parametrize("K", [96, 1056, 4096, 20512, 33024])
+@pytest.mark.parametrize("K", [96, 1056, 2528, 4096, 20512, 33024])
 def test_norm_many_rows_equal_single_rows(fmt, K):
     """A row's result does not depend on the rows beside it or on its place."""
     g = torch.Generator(device="cuda").manual_seed(K)
@@ -220,7 +220,7 @@ def test_norm_many_rows_equal_single_rows(fmt, K):
 
 @pytest.mark.parametrize("fmt", [lb.Q8_I8, lb.Q8_F8])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("K", [160, 4128, 33024])
+@pytest.mark.parametrize("K", [160, 2528, 4128, 33024])
 def test_norm_extreme_rows(dtype, fmt, K):
     """Rows of zeros, a NaN, infinities, squares beyond fp32, tiny values; gains beyond the range."""
     rng = np.random.default_rng(K)
