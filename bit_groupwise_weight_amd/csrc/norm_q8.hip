@@ -11,7 +11,9 @@
 //
 // A row holding a NaN or an infinity: y is NaN throughout, its scales are NaN
 // and its codes 0.  A finite row whose squares overflow fp32 is summed again
-// from h * 2^-96 (exact), so that it is normalized as any other.
+// from h * 2^-96 (exact), so that it is normalized as any other; it is divided
+// in two steps, h * 2^-32 and the rest, as 1 / rms alone may be subnormal (what
+// the first step loses of y is below fp32's smallest number).
 #include "f8_common.h"
 
 namespace lowbit {
@@ -133,6 +135,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_q8_kernel(NormQ8Params
   };
   ss = row_sum<T>(ss, s_sum[0]);
   float inv = 1.0f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
+  float down = 1.0f;                   // (of a row read again: kept ones are scaled in place)
   if (!(ss < __builtin_inff())) {      // the same for every thread of the row
     if (row_max<T>(top, s_max[0]) >= 0x7f800000u) {
       inv = __builtin_nanf("");
@@ -143,16 +146,20 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_q8_kernel(NormQ8Params
         float v[8];
         h_of(k, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s2 = fmaf(v[i] * 0x1p-96f, v[i] * 0x1p-96f, s2);
+        for (int i = 0; i < 8; ++i) {
+          s2 = fmaf(v[i] * 0x1p-96f, v[i] * 0x1p-96f, s2);
+          if constexpr (C != 0) kept[k][i] *= 0x1p-32f;
+        }
       }
-      inv = 0x1p-96f / sqrtf(row_sum<T>(s2, s_sum[1]) / static_cast<float>(p.K));
+      down = 0x1p-32f;
+      inv = 0x1p-64f / sqrtf(row_sum<T>(s2, s_sum[1]) / static_cast<float>(p.K));
     }
   }
 
   auto normed = [&](int k, float (&v)[8]) {
     h_of(k, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    for (int i = 0; i < 8; ++i) v[i] = (C != 0 ? v[i] : v[i] * down) * inv;
     const int c = tid + k * T;
     if (p.weight && c < chunks) {
       float g[8];
