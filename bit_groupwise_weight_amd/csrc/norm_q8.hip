@@ -82,7 +82,7 @@ __device__ __forceinline__ u32v2_t codes8(const float (&v)[8], const SpanScale& 
 // for the sum.  bf16 with residual to e4m3, MI355X: 8192 x 4096 43.5 us, 5.4 TB/s
 // (a copy of 1 GiB: 5.1); 1 x 4096 2.7 us.  int8, 128 x 14336: 4.1 us.
 template <int ACT, int FMT, int T, int C>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_q8_kernel(NormQ8Params p) {
+__global__ __launch_bounds__(T == 64 ? 256 : T) void norm_q8_kernel(NormQ8Params p) {
   __shared__ float s_sum[2][T / 64];
   __shared__ uint32_t s_max[2][T / 64];
   const int64_t m = T == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
@@ -232,35 +232,56 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_q8_kernel(NormQ8Params
 template <int ACT, int FMT, int T, int C>
 hipError_t launch_norm_rows(const NormQ8Params& p, hipStream_t s) {
   const int64_t blocks = T == 64 ? (p.M + 3) / 4 : p.M;
-  norm_q8_kernel<ACT, FMT, T, C><<<dim3(static_cast<unsigned>(blocks)), dim3(T < 256 ? 256 : T), 0, s>>>(p);
+  norm_q8_kernel<ACT, FMT, T, C><<<dim3(static_cast<unsigned>(blocks)), dim3(T == 64 ? 256 : T), 0, s>>>(p);
   return hipGetLastError();
 }
 
 // The threads of a row by its length alone, so that a row's result does not
-// depend on how many there are: one chunk a thread, or the fewest, with waves
-// enough.  us for many rows / one row, bf16 with residual to e4m3 (T x C):
+// depend on how many there are.  Up to 1024 values one wave a row, up to 8192 one
+// chunk a thread: the row's chunks rounded up to whole waves, past 512 threads to
+// pairs of them; beyond, 1024 threads with two or four chunks each.  us for many
+// rows / one row, bf16 with residual to e4m3 (T x C), at each width's upper end
+// and a little over it:
 //   K = 512     64 x 1: 12.4 / 2.4     256 x 1: 19.9 / 2.5     (16384 rows)
 //   K = 1024    64 x 2: 25.9 / 3.2     256 x 1: 30.8 / 2.5     (16384 rows)
+//   K = 1056   192 x 1: 29.3 / 2.5     256 x 1: 33.1 / 2.6     (16384 rows)
+//   K = 1536   192 x 1: 34.1           256 x 1: 36.8           (16384 rows)
 //   K = 2048   256 x 1: 24.3 / 2.6     512 x 1: 30.7 / 2.6     (8192 rows)
-//   K = 2080   320 x 1: 27.9 / 2.6     512 x 1: 32.1 / 2.6     (8192 rows)
-//   K = 2560   320 x 1: 30.5 / 2.6     512 x 1: 33.9 / 2.6     (8192 rows; 640 for
-//              K = 5120 gained 3 % over 1024 and was left out)
+//   K = 2080   320 x 1: 51.9 / 2.6     384 x 1: 55.9   512 x 1: 60.4 / 2.6   (16131 rows)
+//   K = 2560   320 x 1: 46.1           384 x 1: 48.6   512 x 1: 52.1         (13107 rows)
+//   K = 2576   384 x 1: 51.1           448 x 1: 53.3   512 x 1: 53.7         (13025 rows)
+//   K = 3328   448 x 1: 45.9 / 2.6     512 x 1: 46.2 / 2.7     (10082 rows)
 //   K = 4096   512 x 1: 44.4 / 2.7     256 x 2: 46.9 / 3.5     (8192 rows)
+//   K = 4128   640 x 1: 53.0 / 2.8     768 x 1: 58.5   1024 x 1: 61.2 / 2.8  (8128 rows)
+//   K = 5120   640 x 1: 50.6 / 2.8     768 x 1: 51.1   1024 x 1: 52.5 / 2.8  (6553 rows)
+//   K = 6144   768 x 1: 46.1 / 2.9     896 x 1: 46.8   1024 x 1: 47.4 / 2.9  (5461 rows)
+//   K = 7168   896 x 1: 45.4           1024 x 1: 45.6          (4681 rows)
 //   K = 8192  1024 x 1: 45.0 / 3.1     512 x 2: 46.9 / 3.6     (4096 rows)
+//   K = 8224  1024 x 2: 51.7 / 3.5     640 x 2: 52.3 / 3.6     (4080 rows; fewer threads gain nothing)
+//   K = 10240 1024 x 2: 49.6 / 3.5     640 x 2: 49.6 / 3.9     (3276 rows)
 //   K = 14336 1024 x 2: 24.4 / 3.6     512 x 4: 22.0 / 4.0     (2048 rows, int8)
+//   K = 16416 1024 x 4: 52.0 / 4.9     768 x 4: 51.6 / 5.0     (2044 rows)
 //   K = 32768 1024 x 4: 50.5 / 6.6     re-read: 56.7 / 7.6     (1024 rows)
 //   K = 65536  re-read: 60.7 / 13.0 of 1024, 92.3 / 35.2 of 256 (512 rows)
 template <int ACT, int FMT>
 hipError_t launch_norm(const NormQ8Params& p, hipStream_t s) {
-  if (p.K <= 512) return launch_norm_rows<ACT, FMT, 64, 1>(p, s);
-  if (p.K <= 1024) return launch_norm_rows<ACT, FMT, 64, 2>(p, s);
-  if (p.K <= 2048) return launch_norm_rows<ACT, FMT, 256, 1>(p, s);
-  if (p.K <= 2560) return launch_norm_rows<ACT, FMT, 320, 1>(p, s);
-  if (p.K <= 4096) return launch_norm_rows<ACT, FMT, 512, 1>(p, s);
-  if (p.K <= 8192) return launch_norm_rows<ACT, FMT, 1024, 1>(p, s);
-  if (p.K <= 16384) return launch_norm_rows<ACT, FMT, 1024, 2>(p, s);
-  if (p.K <= 32768) return launch_norm_rows<ACT, FMT, 1024, 4>(p, s);
-  return launch_norm_rows<ACT, FMT, 1024, 0>(p, s);
+  if (p.K > 32768) return launch_norm_rows<ACT, FMT, 1024, 0>(p, s);
+  if (p.K > 16384) return launch_norm_rows<ACT, FMT, 1024, 4>(p, s);
+  if (p.K > 8192) return launch_norm_rows<ACT, FMT, 1024, 2>(p, s);
+  switch ((p.K + 511) / 512) {         // waves of one chunk a thread
+    case 1: return launch_norm_rows<ACT, FMT, 64, 1>(p, s);
+    case 2: return launch_norm_rows<ACT, FMT, 64, 2>(p, s);
+    case 3: return launch_norm_rows<ACT, FMT, 192, 1>(p, s);
+    case 4: return launch_norm_rows<ACT, FMT, 256, 1>(p, s);
+    case 5: return launch_norm_rows<ACT, FMT, 320, 1>(p, s);
+    case 6: return launch_norm_rows<ACT, FMT, 384, 1>(p, s);
+    case 7: return launch_norm_rows<ACT, FMT, 448, 1>(p, s);
+    case 8: return launch_norm_rows<ACT, FMT, 512, 1>(p, s);
+    case 9: case 10: return launch_norm_rows<ACT, FMT, 640, 1>(p, s);
+    case 11: case 12: return launch_norm_rows<ACT, FMT, 768, 1>(p, s);
+    case 13: case 14: return launch_norm_rows<ACT, FMT, 896, 1>(p, s);
+    default: return launch_norm_rows<ACT, FMT, 1024, 1>(p, s);
+  }
 }
 
 template <int ACT>

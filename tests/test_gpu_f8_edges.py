@@ -33,6 +33,36 @@ def up8(a):
 
 # ------------------------------------------------------------------- norm --
 
+@pytest.mark.parametrize("fmt", [lb.Q8_NONE, lb.Q8_I8, lb.Q8_F8])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("waves", range(1, 18))
+def test_norm_at_each_width(waves, dtype, fmt):
+    """Every number of threads a row can take, at both ends of its widths and between: y within the
+    oracle's bound (at most K / 64 + 32 additions in a row, halved by the root, and 8 roundings),
+    whole rows and rows of a batch alike."""
+    for K in (512 * (waves - 1) + 32, 512 * waves - 256, 512 * waves - 32):
+        rng = np.random.default_rng(K)
+        x = torch.from_numpy(rng.standard_normal((9, K)).astype(np.float32)).to(DT[dtype])
+        g = torch.from_numpy(rng.standard_normal(K).astype(np.float32)).to(DT[dtype])
+        q, s, h, y = lb.lowbit_add_rmsnorm_q8(x.to(DEV), g.to(DEV), 1e-5, fmt, want_y=True)
+        ref = o.rmsnorm(f64(x), f64(g), float(np.float32(1e-5)))
+        d = (K / 128 + 24) * U
+        fi = torch.finfo(DT[dtype])
+        half = np.maximum(np.abs(ref) * (1 + d) * fi.eps / 2, fi.smallest_normal * fi.eps / 2)
+        assert np.all(np.abs(f64(y) - ref) <= d * np.abs(ref) + half)
+        one = lb.lowbit_add_rmsnorm_q8(x[7:8].to(DEV), g.to(DEV), 1e-5, fmt, want_y=True)
+        assert torch.equal(one[3][0], y[7])
+        if fmt != lb.Q8_NONE:
+            assert torch.equal(one[0][0].view(torch.uint8), q[7].view(torch.uint8)) and torch.equal(one[1][0], s[7])
+            span = K if fmt == lb.Q8_I8 else 128
+            codes = f64(q) if fmt == lb.Q8_I8 else o.E4M3[patterns(q)]
+            top = 127.0 if fmt == lb.Q8_I8 else 448.0
+            full = np.repeat(f64(s).reshape(9, -1), span, 1)[:, :K]
+            step = 0.5 * full if fmt == lb.Q8_I8 else np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * full)
+            assert np.all(np.abs(codes * full - ref) <= step * (1 + 2 * d) + 2 * d * np.abs(ref))
+            assert all((np.abs(codes[:, b:b + span]).max(1) == top).all() for b in range(0, K, span))
+
+
 @pytest.mark.parametrize("K", [16, 1024, 2048, 4096, 16384, 32768, 65536])
 def test_norm_rows_near_the_largest_number(K):
     """Rows of one value r above 2^126, whose reciprocal is subnormal: y = r / r.  r has five
