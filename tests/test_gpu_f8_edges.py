@@ -63,6 +63,21 @@ def test_norm_at_each_width(waves, dtype, fmt):
             assert all((np.abs(codes[:, b:b + span]).max(1) == top).all() for b in range(0, K, span))
 
 
+def test_norm_codes_are_those_of_its_own_y():
+    """With fp32 the unrounded y is the one returned: codes and scales are the oracle's rule on it,
+    bit for bit."""
+    for M, K in ((5, 160), (3, 1056), (2, 4128), (3, 8256), (2, 33024)):
+        x, g = torch.randn(M, K, device=DEV) * 3, torch.randn(K, device=DEV)
+        q, s, _, y = lb.lowbit_add_rmsnorm_q8(x, g, 1e-5, lb.Q8_F8, want_y=True)
+        rq, rs = o.quantize_f8_rows(y.cpu().numpy())
+        assert np.array_equal(patterns(q), rq) and np.array_equal(s.cpu().numpy(), rs)
+        q, s, _, y = lb.lowbit_add_rmsnorm_q8(x, g, 1e-5, lb.Q8_I8, want_y=True)
+        v = y.cpu().numpy()
+        rs, f = o.span_scale(v, 127.0)
+        assert np.array_equal(s.cpu().numpy(), rs)
+        assert np.array_equal(q.cpu().numpy(), np.rint((v * f[:, None]).astype(np.float32)).astype(np.int8))
+
+
 @pytest.mark.parametrize("K", [16, 1024, 2048, 4096, 16384, 32768, 65536])
 def test_norm_rows_near_the_largest_number(K):
     """Rows of one value r above 2^126, whose reciprocal is subnormal: y = r / r.  r has five
