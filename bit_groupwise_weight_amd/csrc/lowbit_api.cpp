@@ -577,8 +577,13 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 //   half a block: 8.1 against 6.7);
 // - 64 x 32 tiles, whose loads are further ahead, where they are 2/3 of a block
 //   to one a CU (16, 14336, 4096: 11.5 against 13.3; 1 x 8 of 64, 1408, 2048: 8.0
-//   against 8.5; 8, 4096, 4096, 1/4 of a block: 8.8 against 6.7) and K is not
-//   long (8, 28672, 8192: 47 against 46);
+//   against 8.5; 8, 4096, 4096, 1/4 of a block: 8.8 against 6.7; 8, 14336, 12288:
+//   34.9 against 37.9 of 64 columns), but not where the rows they read side by
+//   side lie a multiple of 8 KiB apart: there 64 columns, whose waves read
+//   different parts of K (8, 14336: K = 8064 23.3 against 24.6, K = 8192 29.5
+//   against 24.4, K = 8320 24.0 against 25.6; 16, 16384, 8192: 34.6 against 26.5;
+//   8, 11264, 8192: 23.4 against 23.3; 8, 14336, 16384: 55.0 against 57.2; 1 x 8 of
+//   64, 2048, 8192: 28.8 against 26.8, with 1536 columns 24.4 against 26.7);
 // - 16 columns read more activations than they can hide from 9 rows on where K
 //   is long (16, 4096, 14336: 18.4 against 14.4 of 64 x 32 tiles in splits).
 //
@@ -621,7 +626,7 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   const int64_t per = (T + used - 1) / used;            // rows of one, on average
   if (per <= (grouped ? 10 : 16)) {
     const int64_t units = used * ((N + 15) / 16), wide = used * ((N + 63) / 64);
-    if (wide * 3 >= cus * 2 && wide <= cus && kb < 64) return {F8_TILE_64X32_K2, 1};
+    if (wide * 3 >= cus * 2 && wide <= cus) return {K % 8192 != 0 ? F8_TILE_64X32_K2 : F8_ROWS_NT4, 1};
     if (units >= 4 * (cus * 7 / 4)) return {F8_ROWS_NT4, 1};
     if (units >= 2 * (cus * 7 / 8)) return {F8_ROWS_NT2, 1};
     if (per <= 8 || kb < 64) return {F8_ROWS_NT1, 1};

@@ -94,3 +94,30 @@ def test_norm_rows_near_the_largest_number(K):
         assert np.abs(f64(y) - want).max() <= 2 * U
         assert np.abs(f64(s) * 448 - 1).max() <= 4 * U
         assert np.array_equal(o.E4M3[patterns(q)], 448 * want)
+
+
+# ----------------------------------------------------------------- linear --
+
+def exact_inputs(seed, M, N, K, E=None):
+    """Small integers and powers of two: every sum is exact in fp32, in any order."""
+    rng = np.random.default_rng(seed)
+    kb, nb = -(-K // 128), -(-N // 128)
+    lead = () if E is None else (E,)
+    ints = np.array([0x00, 0x38, 0x40, 0xb8, 0xc0, 0x30], np.uint8)     # 0, 1, 2, -1, -2, 0.5
+    xq, wq = rng.choice(ints, (M, K)), rng.choice(ints, (*lead, N, K))
+    xs = (2.0 ** rng.integers(-2, 2, (M, kb))).astype(np.float32)
+    ws = (2.0 ** rng.integers(-2, 2, (*lead, nb, kb))).astype(np.float32)
+    return xq, xs, wq, ws
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M, N, K", [(1, 11100, 8192), (16, 16300, 8192), (8, 12000, 8208), (3, 11000, 8064)])
+def test_linear_few_rows_of_long_k(M, N, K, dtype):
+    """Both sides of the rule for rows that lie a multiple of 8 KiB apart."""
+    xq, xs, wq, ws = exact_inputs(M + K, M, N, K)
+    cols = np.unique(np.concatenate([np.arange(70), np.arange(N - 300, N), np.random.default_rng(N).integers(0, N, 200)]))
+    ref, A = o.linear_f8(xq, xs, wq, ws, None, cols)
+    assert A.max() < 2 ** 18                   # steps of 2^-6: below 2^24 of them, exact in fp32
+    y = lb.lowbit_linear_f8(up8(xq), up(xs), up8(wq), up(ws), None, DT[dtype])
+    want = ref if dtype == "f32" else f64(torch.from_numpy(ref).to(DT[dtype]))
+    assert np.array_equal(f64(y[:, torch.from_numpy(cols).to(DEV)]), want)
