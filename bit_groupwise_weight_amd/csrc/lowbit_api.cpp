@@ -552,6 +552,7 @@ void a8_tiles(int64_t M, int64_t N, int* mtt_out, int* nt_out) {
 // fit 32 bits, and launches of fewer than 2^32 threads (checked per call).
 constexpr int64_t kQ8MaxK = int64_t(1) << 23;
 constexpr int64_t kNormMaxM = (int64_t(1) << 22) - 1;
+constexpr int64_t kActF8MaxBlocks = (int64_t(1) << 28) - 16;   // of 16 threads each
 constexpr int64_t kF8MaxExperts = int64_t(1) << 16;
 int64_t f8_blocks(int64_t n) { return (n + 127) / 128; }
 
@@ -1018,8 +1019,8 @@ lowbit_status lowbit_quantize_act_f8(const void* x, lowbit_dtype dtype, int64_t 
   if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
   const lowbit_status st = check_q8_row(K, 16);
   if (st != LOWBIT_OK) return st;
-  if (M < 0 || M > kMaxDim || M * f8_blocks(K) >= (int64_t(1) << 28))
-    return fail(LOWBIT_ERR_INVALID_ARG, "M=%lld: M * ceil(K / 128) must be below 2^28", (long long)M);
+  if (M < 0 || M > kMaxDim || M * f8_blocks(K) > kActF8MaxBlocks)
+    return fail(LOWBIT_ERR_INVALID_ARG, "M=%lld: M * ceil(K / 128) must be at most 2^28 - 16", (long long)M);
   if (M == 0) return LOWBIT_OK;
   if (!x || !xq || !xscale) return fail(LOWBIT_ERR_INVALID_ARG, "NULL x, xq or xscale");
   if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(xscale, 4))

@@ -336,7 +336,7 @@ lowbit_status lowbit_add_rmsnorm_q8(const void* x, const void* residual, const v
  *
  *   x        device, M x K row-major, dtype, 16-byte aligned.
  *   M >= 0 (0 is a no-op), K > 0 and a multiple of 16, K <= 2^23,
- *            M * ceil(K / 128) < 2^28.
+ *            M * ceil(K / 128) at most 2^28 - 16.
  *   xq       device, M x K e4m3 codes, 16-byte aligned.  Written.
  *   xscale   device, M x ceil(K / 128) fp32, 4-byte aligned.  Written.
  * Asynchronous. */

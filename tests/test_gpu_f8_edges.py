@@ -96,6 +96,21 @@ def test_norm_rows_near_the_largest_number(K):
         assert np.array_equal(o.E4M3[patterns(q)], 448 * want)
 
 
+# -------------------------------------------------------------- quantizer --
+
+def test_quantize_act_f8_of_the_most_blocks():
+    """2^28 - 16 rows of one block each: the largest launch; every row as in a small call."""
+    M, K, n = (1 << 28) - 16, 16, 1 << 12
+    base = torch.randn(n, K, device=DEV).bfloat16()
+    want, wants = lb.lowbit_quantize_act_f8(base)
+    q, s = lb.lowbit_quantize_act_f8(base.repeat((1 << 28) // n, 1)[:M])
+    whole = M // n * n
+    q = q.view(torch.uint8)
+    assert (q[:whole].view(-1, n, K) == want.view(torch.uint8)).all()
+    assert (s[:whole].view(-1, n) == wants.view(-1)).all()
+    assert torch.equal(q[whole:], want.view(torch.uint8)[:M - whole]) and torch.equal(s[whole:], wants[:M - whole])
+
+
 # ----------------------------------------------------------------- linear --
 
 def exact_inputs(seed, M, N, K, E=None):
