@@ -248,6 +248,7 @@ enum LinearF8Kind : int {
   F8_ROWS_NT1, F8_ROWS_NT2, F8_ROWS_NT4, F8_TILE_64X32, F8_TILE_64X32_K2, F8_TILE_64X64, F8_TILE_64X64_K2,
   F8_TILE_128X128, F8_TILE_128X128_K2, F8_TILE_256X256
 };
+constexpr int64_t kF8MaxThreads = 0xffffffff;   // of a launch (HIP counts them in 32 bits)
 struct LinearF8Plan {
   LinearF8Kind kind;
   int splits;             // K splits (tiles below 256 x 256; 1: no partial sums)

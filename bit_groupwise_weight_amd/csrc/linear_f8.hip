@@ -701,7 +701,7 @@ hipError_t launch_big(LinearF8Params p, hipStream_t s) {
   int64_t tiles_m = (p.T + 255) / 256;
   if (p.offsets) tiles_m = p.T / 256 + (p.T < p.E ? p.T : p.E);
   const int64_t blocks = tiles_m * p.tiles_n;
-  if (blocks > 0x7fffffff / 512) return hipErrorInvalidConfiguration;
+  if (blocks > kF8MaxThreads / 512) return hipErrorInvalidConfiguration;
   linear_f8_big_kernel<OUT><<<dim3(static_cast<unsigned>(blocks)), dim3(512), 0, s>>>(p);
   return hipGetLastError();
 }
@@ -876,7 +876,7 @@ hipError_t launch_rows(LinearF8Params p, hipStream_t s) {
   int64_t tiles_m = (p.T + 16 * MT - 1) / (16 * MT);
   if (p.offsets) tiles_m = p.T / (16 * MT) + (p.T < p.E ? p.T : p.E);
   const int64_t blocks = tiles_m * p.tiles_n;
-  if (blocks > 0x7fffffff / (64 * W)) return hipErrorInvalidConfiguration;
+  if (blocks > kF8MaxThreads / (64 * W)) return hipErrorInvalidConfiguration;
   linear_f8_rows_kernel<NT, MT, W, U, OUT><<<dim3(static_cast<unsigned>(blocks)), dim3(64 * W), 0, s>>>(p);
   return hipGetLastError();
 }
@@ -888,7 +888,7 @@ hipError_t launch_tile(LinearF8Params p, int splits, hipStream_t s) {
   int64_t tiles_m = (p.T + BM - 1) / BM;
   if (p.offsets) tiles_m = p.T / BM + (p.T < p.E ? p.T : p.E);
   const int64_t blocks = tiles_m * p.tiles_n;
-  if (blocks > 0x7fffffff / (64 * WN * WM * KG)) return hipErrorInvalidConfiguration;
+  if (blocks > kF8MaxThreads / (64 * WN * WM * KG)) return hipErrorInvalidConfiguration;
   const dim3 block(64 * WN * WM * KG);
   if (splits <= 1) {
     linear_f8_tile_kernel<BN, BM, WN, WM, S, KG, false, OUT>

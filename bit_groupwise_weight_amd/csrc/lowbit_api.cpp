@@ -604,15 +604,15 @@ lowbit_status check_q8_row(int64_t K, int unit) {
 // in four splits against 51 in one.
 struct F8TileRate {
   lowbit::LinearF8Kind kind;
-  int bn, bm, groups;
+  int bn, bm, groups, threads;
   double one, two;
 };
-constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 1, 0.36, 0.46},
-                                   {lowbit::F8_TILE_64X64, 64, 64, 1, 0.51, 0.57},
-                                   {lowbit::F8_TILE_128X128, 128, 128, 1, 1.04, 1.29},
-                                   {lowbit::F8_TILE_64X32_K2, 64, 32, 2, 0.51, 0.51},
-                                   {lowbit::F8_TILE_64X64_K2, 64, 64, 2, 0.72, 0.72},
-                                   {lowbit::F8_TILE_128X128_K2, 128, 128, 2, 1.64, 1.64}};
+constexpr F8TileRate kF8Tiles[] = {{lowbit::F8_TILE_64X32, 64, 32, 1, 256, 0.36, 0.46},
+                                   {lowbit::F8_TILE_64X64, 64, 64, 1, 256, 0.51, 0.57},
+                                   {lowbit::F8_TILE_128X128, 128, 128, 1, 512, 1.04, 1.29},
+                                   {lowbit::F8_TILE_64X32_K2, 64, 32, 2, 512, 0.51, 0.51},
+                                   {lowbit::F8_TILE_64X64_K2, 64, 64, 2, 512, 0.72, 0.72},
+                                   {lowbit::F8_TILE_128X128_K2, 128, 128, 2, 1024, 1.64, 1.64}};
 constexpr double kF8JoinUs = 4.57, kF8JoinUsPerByte = 0.63e-6, kF8BytesPerUs = 5e6;
 constexpr double kF8GroupsUs = 0.27;   // the sums of two groups
 // 256 x 256: one block a CU, a round's start and end, a step of few and of all CUs
@@ -625,7 +625,13 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   const bool grouped = E > 0;
   const int64_t used = grouped ? std::min(E, T) : 1;    // experts with rows, at most
   const int64_t per = (T + used - 1) / used;            // rows of one, on average
-  if (per <= (grouped ? 10 : 16)) {
+  // a variant's row tiles (with experts, each adds less than one to T / bm), and
+  // whether a launch can hold its threads
+  auto fits = [&](int64_t bn, int64_t bm, int64_t threads) {
+    const int64_t tm = grouped ? T / bm + used : (T + bm - 1) / bm;
+    return tm * ((N + bn - 1) / bn) <= kF8MaxThreads / threads;
+  };
+  if (per <= (grouped ? 10 : 16) && fits(64, 16, 256)) {
     const int64_t units = used * ((N + 15) / 16), wide = used * ((N + 63) / 64);
     if (wide * 3 >= cus * 2 && wide <= cus) return {K % 8192 != 0 ? F8_TILE_64X32_K2 : F8_ROWS_NT4, 1};
     if (units >= 4 * (cus * 7 / 4)) return {F8_ROWS_NT4, 1};
@@ -639,11 +645,12 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   };
   const double codes = (static_cast<double>(used) * static_cast<double>(N) + static_cast<double>(T)) *
                        static_cast<double>(kb) * 128.0;
-  LinearF8Plan plan{F8_TILE_64X32, 1};
+  LinearF8Plan plan{F8_TILE_128X128, 1};                // the fewest threads (16-bit outputs have fewer still)
   double best = std::numeric_limits<double>::infinity();
   for (const F8TileRate& t : kF8Tiles) {
     // (16 waves have 128 registers each: too few for fp32's bf16 copies of the codes)
     if (t.kind == F8_TILE_128X128_K2 && dtype == LOWBIT_F32) continue;
+    if (!fits(t.bn, t.bm, t.threads)) continue;
     const double blocks = load(t.bn, t.bm);
     for (int splits = 1; splits <= kF8MaxSplits; ++splits) {
       const int64_t steps = (kb + splits - 1) / splits;
@@ -670,7 +677,7 @@ lowbit::LinearF8Plan f8_plan(int64_t M, int64_t T, int64_t E, bool gather, int64
   }
   // 256 x 256 tiles: their sums are those of the fp8 MFMA, their offsets into a
   // gathered xq 32 bits, and they load four blocks' scales at once
-  if (dtype != LOWBIT_F32 && kb >= 4 && !(gather && M * K > int64_t{0xffffffff})) {
+  if (dtype != LOWBIT_F32 && kb >= 4 && !(gather && M * K > int64_t{0xffffffff}) && fits(256, 256, 512)) {
     const double n = load(256, 256), whole = std::floor(n);
     double us = whole * (kF8BigUs + static_cast<double>(kb) * kF8BigFullStep);
     if (n > whole) us += kF8BigUs + static_cast<double>(kb) * kF8BigStep;
@@ -733,7 +740,8 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
   p.partials = static_cast<float*>(workspace);
   const hipError_t he = lowbit::launch_linear_f8(p, plan, act_kind(dtype), static_cast<hipStream_t>(stream));
   if (he == hipErrorInvalidConfiguration)
-    return fail(LOWBIT_ERR_INVALID_ARG, "problem too large: T=%lld N=%lld", (long long)T, (long long)N);
+    return fail(LOWBIT_ERR_INVALID_ARG, "T=%lld N=%lld: the outputs have 2^23 tiles of 128 x 128 or more",
+                (long long)T, (long long)N);
   if (he != hipSuccess) return hip_fail(he, "linear_f8 launch");
   return LOWBIT_OK;
 }

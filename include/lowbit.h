@@ -347,7 +347,7 @@ lowbit_status lowbit_quantize_act_f8(const void* x, lowbit_dtype dtype, int64_t 
  *
  *   w        device, E x N x K row-major ([expert,] out, in), dtype, 16-byte
  *            aligned.
- *   E, N, K > 0, K a multiple of 16, K <= 2^23, N <= 2^30,
+ *   E, N, K > 0, E <= 2^16, K a multiple of 16, K <= 2^23, N <= 2^30,
  *            E * ceil(N / 128) * ceil(K / 128) < 2^24.
  *   wq       device, E x N x K e4m3 codes, 16-byte aligned.  Written.
  *   wscale   device, E x ceil(N / 128) x ceil(K / 128) fp32.  Written.
@@ -367,7 +367,10 @@ lowbit_status lowbit_quantize_weight_f8(const void* w, lowbit_dtype dtype, int64
  *   y        device, M x N row-major, dtype, aligned to its element size.
  *            Overwritten; must not alias an input.
  *   dtype    type of bias and y (fp32, fp16, bf16).
- *   M >= 0 (0 is a no-op; at most 2^30), N > 0 (at most 2^30), K as above.
+ *   M >= 0 (0 is a no-op; at most 2^30), N > 0 (at most 2^30), K as above,
+ *            fewer than 2^23 tiles of 128 x 128 outputs, ceil(M / 128) *
+ *            ceil(N / 128) (a launch's 2^32 threads; a call with more may be
+ *            refused with LOWBIT_ERR_INVALID_ARG).
  *   xq and wq 16-byte aligned, the scales 4-byte aligned.
  *
  *   workspace/workspace_bytes: device scratch or NULL/0, at least
@@ -411,7 +414,8 @@ size_t lowbit_linear_f8_workspace_bytes(int64_t M, int64_t T, int64_t E, int64_t
  *   wq, wscale   E matrices as written by lowbit_quantize_weight_f8.
  *   bias     device, E x N elements of dtype, or NULL.
  *   y        device, T x N row-major, dtype.
- *   T >= 0 (0 is a no-op; at most 2^30), M >= 1 where T > 0, 1 <= E <= 2^16;
+ *   T >= 0 (0 is a no-op; at most 2^30), M >= 1 where T > 0, 1 <= E <= 2^16,
+ *            (floor(T / 128) + min(T, E)) * ceil(N / 128) < 2^23;
  *   N, K, alignment, workspace, accumulation and order as for lowbit_linear_f8.
  *
  * Asynchronous; nothing waits for the offsets on the host. */

@@ -136,3 +136,35 @@ def test_linear_few_rows_of_long_k(M, N, K, dtype):
     y = lb.lowbit_linear_f8(up8(xq), up(xs), up8(wq), up(ws), None, DT[dtype])
     want = ref if dtype == "f32" else f64(torch.from_numpy(ref).to(DT[dtype]))
     assert np.array_equal(f64(y[:, torch.from_numpy(cols).to(DEV)]), want)
+
+
+def grids_of_codes(rows, cols):
+    """e4m3 codes 0 or 1 and a scale of 1, 2 or 4 a span, made in place (the arrays are large)."""
+    q = torch.empty(rows, cols, dtype=torch.uint8, device=DEV).random_(0, 2).mul_(0x38)
+    return q.view(F8)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_one_row_into_more_than_2_to_the_29_columns(dtype):
+    """More blocks than 2^31 threads make; sums of at most 16 codes times scales up to 4, exact."""
+    N, K = (1 << 29) + (1 << 20) + 37, 16
+    wq, ws = grids_of_codes(N, K), (2.0 ** (torch.arange(-(-N // 128), device=DEV) % 3)).float()[:, None]
+    xq = torch.tensor([[0x38, 0] * 8], dtype=torch.uint8, device=DEV).view(F8)
+    y = lb.lowbit_linear_f8(xq, torch.ones(1, 1, device=DEV), wq, ws, None, DT[dtype])[0]
+    for at in range(0, N, 1 << 24):
+        n = min(1 << 24, N - at)
+        want = wq[at:at + n].float()[:, ::2].sum(1) * ws[at // 128:, 0].repeat_interleave(128)[:n]
+        assert torch.equal(y[at:at + n].float(), want), at
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_2_to_the_29_rows(dtype):
+    """The other way round: rows past 2^29 into 16 columns."""
+    M, K, N = (1 << 29) + 300, 16, 16
+    xq, xs = grids_of_codes(M, K), (2.0 ** (torch.arange(M, dtype=torch.int32, device=DEV) % 3)).float()[:, None]
+    wq = grids_of_codes(N, K)
+    y = lb.lowbit_linear_f8(xq, xs, wq, torch.ones(1, 1, device=DEV), None, DT[dtype])
+    w = wq.float().t().contiguous()
+    for at in range(0, M, 1 << 24):
+        n = min(1 << 24, M - at)
+        assert torch.equal(y[at:at + n].float(), (xq[at:at + n].float() @ w) * xs[at:at + n]), at
