@@ -1064,7 +1064,9 @@ size_t lowbit_linear_f8_workspace_bytes(int64_t M, int64_t T, int64_t E, int64_t
   if (K <= 0 || K > kQ8MaxK || K % 16 != 0 || N <= 0 || N > kMaxDim || T <= 0 || T > kMaxDim || M <= 0 ||
       M > kMaxDim || E < 0 || E > kF8MaxExperts || !valid_dtype(dtype))
     return 0;
-  return f8_partial_bytes(f8_plan(M, T, E, false, N, K, dtype), T, N);
+  // (whether the rows are gathered is not said here, and decides the schedule of a large xq)
+  const size_t plain = f8_partial_bytes(f8_plan(M, T, E, false, N, K, dtype), T, N);
+  return E == 0 ? plain : std::max(plain, f8_partial_bytes(f8_plan(M, T, E, true, N, K, dtype), T, N));
 }
 
 lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uint8_t* wq,

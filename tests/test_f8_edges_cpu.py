@@ -18,3 +18,14 @@ def test_quantize_act_f8_takes_no_more_than_a_launch_can_hold(lowbit_lib, M, K, 
     assert lowbit_lib.lowbit_quantize_act_f8(None, BF16, M, K, None, None, None) == INVALID
     assert ("NULL" in lb.lowbit_last_error()) == within
     assert ("2^28 - 16" in lb.lowbit_last_error()) != within
+
+
+@pytest.mark.parametrize("M, T, E, N, K, splits", [
+    (226200, 3841, 2, 2441, 19072, 2),       # a gathered xq past 4 GiB has no 256 x 256 tiles: K splits
+    (99400, 803, 2, 10552, 43648, 4),
+    (225000, 3841, 2, 2441, 19072, 0),       # just below: 256 x 256
+])
+def test_workspace_covers_the_schedule_of_gathered_rows(lowbit_lib, M, T, E, N, K, splits):
+    """The schedule on a 256-CU device, seen through its fp32 planes of T x N."""
+    need = lb.lowbit_linear_f8_workspace_bytes(M, T, E, N, K, torch.bfloat16)
+    assert need == splits * T * -(-N // 4) * 4 * 4

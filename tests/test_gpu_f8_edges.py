@@ -168,3 +168,32 @@ def test_linear_2_to_the_29_rows(dtype):
     for at in range(0, M, 1 << 24):
         n = min(1 << 24, M - at)
         assert torch.equal(y[at:at + n].float(), (xq[at:at + n].float() @ w) * xs[at:at + n]), at
+
+
+def test_grouped_gather_past_4_gib_in_splits():
+    """Rows gathered from more than 4 GiB of codes run in K splits through the workspace that the
+    query asks for; without one the same sums (exact ones) come from one pass over K."""
+    M, T, N, K = 226200, 3841, 2441, 19072
+    rng = np.random.default_rng(4)
+    few, xsc, wq, ws = exact_inputs(4, 48, N, K, E=2)
+    few[rng.random((48, K)) < 0.9] = 0         # sums below 2^24 steps of 2^-6
+    at = np.unique(np.concatenate([[0, M - 1], rng.integers(0, M, 60)]))[:48]
+    at[-1] = M - 1
+    xq = torch.zeros(M, K, dtype=torch.uint8, device=DEV)
+    xs = torch.ones(M, K // 128, device=DEV)
+    xq[up(at)], xs[up(at)] = up(few), up(xsc)
+    pick = rng.integers(0, 48, T)
+    off = np.array([0, 1700, T], np.int32)
+    need = lb.lowbit_linear_f8_workspace_bytes(M, T, 2, N, K, torch.float16)
+    assert need == 2 * T * 2444 * 4
+    a = [xq.view(F8), xs, up(off), up8(wq), up(ws), None, torch.float16]
+    rows = up(at[pick].astype(np.int32))
+    y = lb.lowbit_linear_f8_grouped(*a, rows=rows)
+    cols = np.unique(np.concatenate([np.arange(20), np.arange(N - 140, N), rng.integers(0, N, 60)]))
+    for e in range(2):
+        ref, A = o.linear_f8(few, xsc, wq[e], ws[e], None, cols)
+        assert A.max() < 2 ** 18
+        want = f64(torch.from_numpy(ref).to(torch.float16))[pick[off[e]:off[e + 1]]]
+        assert np.array_equal(f64(y[off[e]:off[e + 1]][:, up(cols)]), want)
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)
+    assert torch.equal(lb.lowbit_linear_f8_grouped(*a, rows=rows, workspace=small), y)
