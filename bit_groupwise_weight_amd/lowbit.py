@@ -648,16 +648,17 @@ def lowbit_add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: 
 
 
 def lowbit_linear_f8_workspace_bytes(M: int, T: int, E: int, N: int, K: int, dtype: torch.dtype) -> int:
-    """Bytes lowbit_linear_f8 (T = M, E = 0) or lowbit_linear_f8_grouped can use as workspace."""
+    """Bytes lowbit_linear_f8 (T = M, E = 0) or lowbit_linear_f8_grouped can use as workspace, on the
+    current device."""
     return load().lowbit_linear_f8_workspace_bytes(M, T, E, N, K, _DTYPE_ENUM[dtype])
 
 
-def _f8_workspace(xq: torch.Tensor, M: int, T: int, E: int, N: int, K: int, act: int,
+def _f8_workspace(dev: int, xq: torch.Tensor, M: int, T: int, E: int, N: int, K: int, act: int,
                   stream) -> Optional[torch.Tensor]:
     """A workspace made for one call, on the call's stream: torch's allocator reuses it there only
-    (and keeps it for a graph that captures the call), so no two calls or graphs share it."""
-    address, fn = _entry("lowbit_linear_f8_workspace_bytes")
-    need = fn(M, T, E, N, K, act) if address is None else fn(address, M, T, E, N, K, act)
+    (and keeps it for a graph that captures the call), so no two calls or graphs share it.  Its size
+    is that of the tensors' device, as the call's schedule is."""
+    need = _call_on(dev, "lowbit_linear_f8_workspace_bytes", M, T, E, N, K, act)
     return None if need == 0 else _made_on((need,), torch.uint8, xq, stream)
 
 
@@ -739,7 +740,7 @@ def lowbit_linear_f8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, w
     dev = _placed(xq, xscale, wq, wscale, bias, y, workspace)
     act = _DTYPE_ENUM[dtype]
     if workspace is None:
-        workspace = _f8_workspace(xq, M, M, 0, N, K, act, stream)
+        workspace = _f8_workspace(dev, xq, M, M, 0, N, K, act, stream)
     st = _call_on(dev, "lowbit_linear_f8", _ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(y),
                   act, M, N, K, _ptr(workspace), 0 if workspace is None else workspace.numel(),
                   _stream_of(dev, stream))
@@ -787,7 +788,7 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
     dev = _placed(xq, xscale, offsets, wq, wscale, bias, rows, y, workspace)
     act = _DTYPE_ENUM[dtype]
     if workspace is None:
-        workspace = _f8_workspace(xq, M, T, E, N, K, act, stream)
+        workspace = _f8_workspace(dev, xq, M, T, E, N, K, act, stream)
     st = _call_on(dev, "lowbit_linear_f8_grouped", _ptr(xq), _ptr(xscale), _ptr(rows), _ptr(offsets), _ptr(wq),
                   _ptr(wscale), _ptr(bias), _ptr(y), act, M, T, E, N, K, _ptr(workspace),
                   0 if workspace is None else workspace.numel(), _stream_of(dev, stream))

@@ -392,7 +392,8 @@ lowbit_status lowbit_linear_f8(const uint8_t* xq, const float* xscale, const uin
                                void* stream);
 
 /* Bytes of workspace that lowbit_linear_f8 (T = M, E = 0) or
- * lowbit_linear_f8_grouped can use (0 when the shape's schedule needs none).
+ * lowbit_linear_f8_grouped can use on the current device (0 when the shape's
+ * schedule needs none).
  * With less, the call runs without a K split. */
 size_t lowbit_linear_f8_workspace_bytes(int64_t M, int64_t T, int64_t E, int64_t N, int64_t K,
                                         lowbit_dtype dtype);

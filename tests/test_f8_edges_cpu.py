@@ -29,3 +29,35 @@ def test_workspace_covers_the_schedule_of_gathered_rows(lowbit_lib, M, T, E, N, 
     """The schedule on a 256-CU device, seen through its fp32 planes of T x N."""
     need = lb.lowbit_linear_f8_workspace_bytes(M, T, E, N, K, torch.bfloat16)
     assert need == splits * T * -(-N // 4) * 4 * 4
+
+
+def test_calls_and_workspace_queries_run_with_the_tensors_device_current(lowbit_lib, monkeypatch):
+    """Tensors on GPU 1 while GPU 0 is current: schedules are the device's own, so the query that
+    sizes the workspace and the call must both see GPU 1."""
+    current, seen = [0], []
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    def entry(name):
+        return None, lambda *args: (seen.append((name, current[0])), 0)[1]
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(lb, "_entry", entry)
+    monkeypatch.setattr(lb, "_placed", lambda *tensors: 1)
+    monkeypatch.setattr(lb, "_stream_of", lambda index, stream: 0)
+    f8 = torch.float8_e4m3fn
+    xq, xs = torch.zeros(3, 256, dtype=f8), torch.zeros(3, 2)
+    wq, ws = torch.zeros(2, 40, 256, dtype=f8), torch.zeros(2, 1, 2)
+    lb.lowbit_linear_f8(xq, xs, wq[0], ws[0], None, torch.bfloat16)
+    lb.lowbit_linear_f8_grouped(xq, xs, torch.zeros(3, dtype=torch.int32), wq, ws, None, torch.bfloat16)
+    assert seen == [("lowbit_linear_f8_workspace_bytes", 1), ("lowbit_linear_f8", 1),
+                    ("lowbit_linear_f8_workspace_bytes", 1), ("lowbit_linear_f8_grouped", 1)]
