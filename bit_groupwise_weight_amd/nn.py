@@ -411,7 +411,32 @@ def _swap(parent, name, child, qual, bits, group_size, dtype, filter_fn, act_bit
         _swap(child, n, c, f"{qual}.{n}", bits, group_size, dtype, filter_fn, act_bits)
 
 
-class F8Linear(torch.nn.Module):
+class _F8Module(torch.nn.Module):
+    """Base of the e4m3 modules.  Their codes and scales (every buffer but ``bias``) are a format, not
+    numbers to be cast: ``.half()``, ``.to(dtype)`` and the like leave their types alone and set the
+    type of the outputs and the bias."""
+
+    def _apply(self, fn, recurse=True):
+        def example(t, dtype):
+            return fn(torch.empty(1, dtype=dtype, device=t.device))
+
+        held = {id(b) for name, b in self._buffers.items() if name != "bias"}
+        dtype = example(next(b for b in self._buffers.values() if b is not None), self.dtype).dtype
+        if dtype not in _SZ_DTYPES:
+            raise ValueError(f"{type(self).__name__} computes in one of {_SZ_DTYPES}, not {dtype}")
+
+        def keep(t):
+            if id(t) not in held:
+                return fn(t)
+            like = example(t, t.dtype)
+            return fn(t) if like.dtype == t.dtype else t.to(like.device)
+
+        super()._apply(keep, recurse)
+        self.dtype = dtype
+        return self
+
+
+class F8Linear(_F8Module):
     """``nn.Linear`` with e4m3 weights and activations, an fp32 scale for each block of 128 x 128
     weights and of 128 activations of a row.
 
@@ -485,7 +510,7 @@ def quantize_linears_f8(model: torch.nn.Module, dtype: Optional[torch.dtype] = N
     return model
 
 
-class F8Experts(torch.nn.Module):
+class F8Experts(_F8Module):
     """The experts of a mixture-of-experts block in the e4m3 format: for a token x and each of its
     experts e with routing weight r,
 

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from bit_groupwise_weight_amd import lowbit as lb
+from bit_groupwise_weight_amd import nn as lnn
 
 OK, INVALID = 0, 1
 BF16 = 2
@@ -61,3 +62,56 @@ def test_calls_and_workspace_queries_run_with_the_tensors_device_current(lowbit_
     lb.lowbit_linear_f8_grouped(xq, xs, torch.zeros(3, dtype=torch.int32), wq, ws, None, torch.bfloat16)
     assert seen == [("lowbit_linear_f8_workspace_bytes", 1), ("lowbit_linear_f8", 1),
                     ("lowbit_linear_f8_workspace_bytes", 1), ("lowbit_linear_f8_grouped", 1)]
+
+
+# ---------------------------------------------------------------- modules --
+
+def f8_modules():
+    lin = lnn.F8Linear(272, 200, dtype=torch.bfloat16)
+    lin.wq.view(torch.uint8).random_(0, 120)
+    lin.wscale.uniform_(1e-6, 1.0)
+    exp = lnn.F8Experts(3, 64, 96)
+    exp.down.view(torch.uint8).random_(0, 120)
+    exp.down_scale.uniform_(1e-6, 1.0)
+    return [lin, exp]
+
+
+CASTS = [("half", lambda m: m.half(), torch.float16), ("to f16", lambda m: m.to(torch.float16), torch.float16),
+         ("float", lambda m: m.float(), torch.float32), ("to cpu f32", lambda m: m.to("cpu", torch.float32), torch.float32),
+         ("bfloat16", lambda m: m.bfloat16(), torch.bfloat16), ("type", lambda m: m.type(torch.float16), torch.float16),
+         ("like", lambda m: m.to(torch.zeros(1, dtype=torch.float16)), torch.float16), ("cpu", lambda m: m.cpu(), torch.bfloat16)]
+
+
+@pytest.mark.parametrize("name, cast, dtype", CASTS, ids=[c[0] for c in CASTS])
+def test_a_cast_leaves_codes_and_scales(name, cast, dtype):
+    """Codes and scales stay bit for bit; outputs and bias take the type."""
+    for m in f8_modules():
+        before = {n: b.clone() for n, b in m.named_buffers()}
+        assert cast(torch.nn.Sequential(m))[0] is m and m.dtype == dtype
+        for n, b in m.named_buffers():
+            if n == "bias":
+                assert b.dtype == dtype
+            else:
+                assert b.dtype == before[n].dtype
+                assert torch.equal(b.view(torch.uint8), before[n].view(torch.uint8))
+
+
+def test_a_cast_module_runs_on_meta():
+    m = lnn.F8Linear(272, 200, dtype=torch.bfloat16).half().to("meta")
+    assert m.wq.is_meta and m.wscale.is_meta and m.bias.is_meta
+    y = m(torch.empty((3, 272), dtype=torch.float16, device="meta"))
+    assert y.shape == (3, 200) and y.dtype == torch.float16
+    m = lnn.F8Linear(272, 200, bias=False, device="meta").to("meta", torch.float32)
+    assert m.wq.dtype == torch.float8_e4m3fn and m.wscale.dtype == torch.float32 and m.dtype == torch.float32
+    assert m.to_empty(device="cpu").wq.device.type == "cpu"
+
+
+@pytest.mark.parametrize("dtype", [torch.float64, torch.float8_e4m3fn])
+def test_a_cast_to_a_type_without_outputs_is_refused(dtype):
+    for m in f8_modules():
+        before = {n: b.clone() for n, b in m.named_buffers()}
+        with pytest.raises(ValueError, match="computes in one of"):
+            m.to(dtype)
+        assert m.dtype == torch.bfloat16
+        for n, b in m.named_buffers():
+            assert b.dtype == before[n].dtype and torch.equal(b.view(torch.uint8), before[n].view(torch.uint8))

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from bit_groupwise_weight_amd import lowbit as lb
+from bit_groupwise_weight_amd import nn as lnn
 from oracle import f8_oracle as o
 
 pytestmark = pytest.mark.gpu
@@ -197,3 +198,25 @@ def test_grouped_gather_past_4_gib_in_splits():
         assert np.array_equal(f64(y[off[e]:off[e + 1]][:, up(cols)]), want)
     small = torch.empty(256, dtype=torch.uint8, device=DEV)
     assert torch.equal(lb.lowbit_linear_f8_grouped(*a, rows=rows, workspace=small), y)
+
+
+# ---------------------------------------------------------------- modules --
+
+def test_cast_modules_compute_in_the_new_type():
+    """A cast module equals the one made in that type: the same codes, scales and bias."""
+    torch.manual_seed(3)
+    lin = torch.nn.Linear(272, 200).to(DEV)
+    lin.bias.data = lin.bias.data.bfloat16().float()
+    x = torch.randn(7, 272, device=DEV).half()
+    m = lnn.F8Linear.from_linear(lin, torch.bfloat16)
+    want = lnn.F8Linear.from_linear(lin, torch.float16)(x)
+    got = m.half()(x)
+    assert got.dtype == torch.float16 and torch.equal(got, want)
+    e = lnn.F8Experts(3, 144, 80, device=DEV).set_weight(torch.randn(3, 160, 144, device=DEV) * 0.06,
+                                                         torch.randn(3, 144, 80, device=DEV) * 0.08)
+    x = torch.randn(9, 144, device=DEV).half()
+    ids, w = torch.randint(0, 3, (9, 2), device=DEV), torch.rand(9, 2, device=DEV)
+    f = lnn.F8Experts(3, 144, 80, dtype=torch.float16, device=DEV)
+    f.load_state_dict(e.state_dict())
+    y = e.cpu().half().to(DEV)(x, ids, w)
+    assert y.dtype == torch.float16 and torch.equal(y, f(x, ids, w))
