@@ -502,11 +502,17 @@ def quantize_linears_f8(model: torch.nn.Module, dtype: Optional[torch.dtype] = N
                         ) -> torch.nn.Module:
     """Replace every ``nn.Linear`` of ``model`` (in place) by an F8Linear; layers whose in_features
     is not a multiple of 16, and those that ``filter_fn(module, qualified_name)`` excludes, are left
-    as they are."""
-    for qual, child in [(n, c) for n, c in model.named_modules() if isinstance(c, torch.nn.Linear) and n]:
+    as they are.  A layer that stands at several places is quantized once and shared by those that
+    the filter admits."""
+    made = {}
+    linears = [(n, c) for n, c in model.named_modules(remove_duplicate=False)
+               if isinstance(c, torch.nn.Linear) and n]
+    for qual, child in linears:
         if child.in_features % 16 == 0 and (filter_fn is None or filter_fn(child, qual)):
+            if id(child) not in made:
+                made[id(child)] = F8Linear.from_linear(child, dtype)
             parent, _, name = qual.rpartition(".")
-            setattr(model.get_submodule(parent), name, F8Linear.from_linear(child, dtype))
+            setattr(model.get_submodule(parent), name, made[id(child)])
     return model
 
 

@@ -115,3 +115,26 @@ def test_a_cast_to_a_type_without_outputs_is_refused(dtype):
         assert m.dtype == torch.bfloat16
         for n, b in m.named_buffers():
             assert b.dtype == before[n].dtype and torch.equal(b.view(torch.uint8), before[n].view(torch.uint8))
+
+
+def shared_model(device):
+    lin, block = torch.nn.Linear(64, 64, device=device), torch.nn.Sequential(torch.nn.Linear(64, 32, device=device))
+    return torch.nn.ModuleDict({"a": lin, "b": torch.nn.Sequential(lin, lin), "c": block, "d": block})
+
+
+def test_a_shared_linear_stays_shared():
+    """A layer at several places, and a block at two, become one quantized layer each."""
+    net = lnn.quantize_linears_f8(shared_model("meta"))
+    assert type(net["a"]) is lnn.F8Linear and net["b"][0] is net["a"] and net["b"][1] is net["a"]
+    assert net["c"] is net["d"] and type(net["c"][0]) is lnn.F8Linear
+    assert not any(isinstance(m, torch.nn.Linear) for m in net.modules())
+
+
+def test_a_shared_linear_with_a_filter():
+    """The filter sees every place; the layer stays where it excludes it."""
+    names = []
+    net = shared_model("meta")
+    lin = net["a"]
+    lnn.quantize_linears_f8(net, filter_fn=lambda m, name: names.append(name) or name != "b.1")
+    assert names == ["a", "b.0", "b.1", "c.0", "d.0"]
+    assert net["b"][0] is net["a"] is not lin and net["b"][1] is lin
