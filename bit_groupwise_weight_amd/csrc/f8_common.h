@@ -26,8 +26,15 @@ constexpr float kI8Max = 127.0f;
 // the largest of them and cuts off what lies below 2^-13 of that one (observed:
 // beside a product of 2^16, 2^3 survives and 2^2 does not; from one eight to
 // the next 24 bits survive), so a sum is off by at most 7 * 2^-13 of its
-// magnitudes and by about 2^-16 for random ones: far below the rounding of a
-// 16-bit output, the only ones it is used for.
+// magnitudes' sum A.  It is used for 16-bit outputs, at twice the rate.  Measured
+// on normal activations, plain and with one in a hundred twenty times as large,
+// K of 1024 to 14336: the cuts come to 2^-18.5 to 2^-22.4 of A (rms, falling with
+// the root of K).  To bf16 that is nothing (rms error 1.0002 times that of the
+// rounding alone, 1 to 2 % of the outputs not the nearest number).  In fp16 it
+// shows: 1.2 % more rms error, 6 to 12 % of the outputs not the nearest, and
+// outputs that cancel (|y| far below A) are off by many half steps of their own
+// (one in a thousand by 38 at K = 4096 with outliers, the rms of A being 22
+// times that of y).
 // EXACT == true, for fp32 outputs: the codes as bf16 (exact) and four bf16
 // MFMAs, whose sums keep 24 bits, at half the fp8 rate.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));

@@ -200,6 +200,43 @@ def test_grouped_gather_past_4_gib_in_splits():
     assert torch.equal(lb.lowbit_linear_f8_grouped(*a, rows=rows, workspace=small), y)
 
 
+def cut_of_eights(x, w):
+    """Mean square, per output, of what the fp8 instruction cuts off: each eight products lose at
+    most seven parts below 2^-13 of their largest, of either sign, evenly spread at worst: a mean
+    square of 7 / 3 (2^-13 max)^2, independent from one eight to the next."""
+    top = (x[:, None, :] * w[None, :, :]).abs_().view(x.shape[0], w.shape[0], -1, 8).amax(3).double()
+    return (7 / 3) * (2.0 ** -13 * top).square().sum(2)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M, N, K", [(3, 2000, 4096), (16, 8192, 2048), (64, 4096, 4096), (200, 2500, 2064),
+                                     (600, 4000, 4112), (600, 14340, 1040)])
+def test_16_bit_outputs_lose_no_more_than_the_cuts(M, N, K, dtype):
+    """Every kernel family on random codes: the mean square error of the outputs is at most that of
+    their rounding plus that of the instruction's cuts (a quarter more for the sample's spread).
+    A lost product would break it from one output in 500 on (fp16) or in 50 (bf16, whose rounding's
+    mean square, (1.66e-3 y)^2, is 1 / 88 of a product's y^2 / K at K = 4096)."""
+    gen = torch.Generator(device=DEV).manual_seed(M + N)
+    x = torch.randn(M, K, generator=gen, device=DEV)
+    x[torch.rand(M, K, generator=gen, device=DEV) < 0.01] *= 20
+    xq, xs = lb.lowbit_quantize_act_f8(x)
+    wq, ws = lb.lowbit_quantize_weight_f8(torch.randn(N, K, generator=gen, device=DEV) * 0.02)
+    y = lb.lowbit_linear_f8(xq, xs, wq, ws, None, DT[dtype])
+    at = torch.unique(torch.randint(0, M, (24,), generator=gen, device=DEV))
+    cols = torch.unique(torch.cat([torch.randint(0, N, (300,), generator=gen, device=DEV),
+                                   torch.arange(N - 100, N, device=DEV)]))
+    deq = xq[at].double() * xs[at].double().repeat_interleave(128, 1)[:, :K]
+    wd = wq.view(torch.uint8)[cols].view(F8).double() * ws.double()[cols // 128].repeat_interleave(128, 1)[:, :K]
+    ref = deq @ wd.t()
+    rounding = (ref.to(DT[dtype]).double() - ref).square().mean()
+    cuts = torch.cat([cut_of_eights(deq[i:i + 4].float(), wd.float()) for i in range(0, len(at), 4)]).mean()
+    bound = 1.25 * (rounding + cuts)
+    got = y[at][:, cols].double()
+    assert (got - ref).square().mean() <= bound
+    one = (deq.square() @ wd.square().t() / K).mean()                      # one product's mean square
+    assert one / (500 if dtype == "f16" else 50) > bound
+
+
 # ---------------------------------------------------------------- modules --
 
 def test_cast_modules_compute_in_the_new_type():
