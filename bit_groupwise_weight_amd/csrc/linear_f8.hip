@@ -6,7 +6,11 @@
 //
 // MFMAs over the block's 128 K positions give P_b of an output tile (fp32, from
 // a zero accumulator); the two scales are multiplied once per column of the
-// tile and applied by one fused multiply-add per output.  The weights are the MFMA's A
+// tile and applied by one fused multiply-add per output.  (Their product may
+// leave fp32's normal range before the result does: below 2^-126 a term is off
+// by up to 2^-150 |P_b| < 2^-125, past 2^128 it is infinite.  Applying them one
+// after the other would move that border and cost a multiplication an output,
+// which the 256 x 256 tiles have no room for beside their MFMAs.)  The weights are the MFMA's A
 // operand, so that a lane holds four consecutive n of one output row: the row's
 // scale is one value a lane, and the outputs leave in 8- or 16-byte pieces.
 //

@@ -386,6 +386,9 @@ lowbit_status lowbit_quantize_weight_f8(const void* w, lowbit_dtype dtype, int64
  * fp16 outputs are not the nearest number, and one whose products cancel (|y|
  * far below A) can be off by many steps of its own.  Where that matters, take
  * fp32 outputs (the matrix cores run them at half the rate) and round.  The
+ * two scales are multiplied in fp32 first: where their product lies below
+ * 2^-126 the block's term is off by less than 2^-125, where it passes fp32's
+ * largest number the term is infinite, NaN with a block sum of zero.  The
  * blocks accumulate in fp32; the bias is added in fp32 and the result rounded
  * once to dtype, nearest even.  Asynchronous and deterministic: no atomics,
  * and every output is summed in an order fixed by the shape and by whether the

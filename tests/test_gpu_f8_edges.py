@@ -237,6 +237,33 @@ def test_16_bit_outputs_lose_no_more_than_the_cuts(M, N, K, dtype):
     assert one / (500 if dtype == "f16" else 50) > bound
 
 
+VARIANTS = [(3, 300, 400), (64, 640, 2048), (200, 2500, 1040), (600, 14340, 528)]
+
+
+@pytest.mark.parametrize("M, N, K", VARIANTS)
+def test_scales_whose_product_is_at_the_ends_of_fp32(M, N, K):
+    """Exact sums times 2^e, e the exponent of xscale * wscale: exact inside the normal range, off
+    by less than 2^-125 a block below it, infinite or NaN past it."""
+    xq, xs, wq, ws = exact_inputs(M, M, N, K)
+    cols = np.unique(np.concatenate([np.arange(20), np.arange(N - 260, N)]))
+    ref, A = o.linear_f8(xq, xs, wq, ws, None, cols)       # scale products of 2^-4 .. 2^2
+    assert A.max() < 2 ** 18
+    xq, wq, pick = up8(xq), up8(wq), up(cols)
+    for dtype in (torch.float32, torch.bfloat16):
+        # exponents of xscale and wscale: e = -117 keeps every product and sum normal, above 0 all finite
+        for ex, ew in ((-100, -17), (-17, -100), (70, 37), (107, 0), (-120, 115)):
+            y = lb.lowbit_linear_f8(xq, up(xs * np.float32(2.0 ** ex)), wq, up(ws * np.float32(2.0 ** ew)), None, dtype)
+            want = torch.from_numpy(ref * 2.0 ** (ex + ew)).to(dtype)
+            assert np.array_equal(f64(y[:, pick]), f64(want)), (ex, ew)
+        for ex, ew in ((-70, -70), (-90, -50), (-119, -119)):
+            y = lb.lowbit_linear_f8(xq, up(xs * np.float32(2.0 ** ex)), wq, up(ws * np.float32(2.0 ** ew)), None, dtype)
+            err = np.abs(f64(y[:, pick]) - ref * 2.0 ** (ex + ew))
+            half = np.maximum(np.abs(ref) * 2.0 ** (ex + ew) * torch.finfo(dtype).eps / 2, 2.0 ** -134)
+            assert np.all(err <= xs.shape[1] * 2.0 ** -125 + half), (ex, ew)
+        y = lb.lowbit_linear_f8(xq, up(xs * np.float32(2.0 ** 70)), wq, up(ws * np.float32(2.0 ** 70)), None, dtype)
+        assert not torch.isfinite(y).any()
+
+
 # ---------------------------------------------------------------- modules --
 
 def test_cast_modules_compute_in_the_new_type():
