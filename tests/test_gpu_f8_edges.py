@@ -264,6 +264,44 @@ def test_scales_whose_product_is_at_the_ends_of_fp32(M, N, K):
         assert not torch.isfinite(y).any()
 
 
+@pytest.mark.parametrize("M, dtype", [(1, "f32"), (3, "f16"), (16, "bf16"), (40, "f32"), (300, "f32"), (300, "f16"),
+                                     (600, "bf16")])
+def test_linear_of_a_weight_past_4_gib(M, dtype):
+    """Weight rows on both sides of 2^32 bytes through few-row, tile and 256 x 256 kernels: exact
+    sums of random codes all along K where rows are marked, zeros everywhere else."""
+    N, K = 1 << 16, (1 << 16) + 128
+    rng = np.random.default_rng(M)
+    at = np.unique(np.concatenate([[0, 1, 127, 128, 32640, 65407, 65408, N - 1], rng.integers(0, N, 40)]))
+    xq, xs, few, _ = exact_inputs(M, M, len(at), K)
+    ws = (2.0 ** rng.integers(-2, 2, (N // 128, K // 128))).astype(np.float32)
+    few[rng.random(few.shape) < 0.97] = 0      # sums below 2^24 steps of 2^-6
+    wq = torch.zeros(N, K, dtype=torch.uint8, device=DEV)
+    wq[up(at)] = up(few)
+    y = lb.lowbit_linear_f8(up8(xq), up(xs), wq.view(F8), up(ws), None, DT[dtype])
+    x, w, ref, A = o.E4M3[xq], o.E4M3[few], 0.0, 0.0
+    for b in range(K // 128):                  # (each marked row with its own block's scales)
+        k, s = np.s_[:, 128 * b:128 * b + 128], xs[:, b:b + 1] * ws[at // 128, b]
+        ref, A = ref + s * (x[k] @ w[k].T), A + s * (np.abs(x[k]) @ np.abs(w[k]).T)
+    assert A.max() < 2 ** 18
+    want = f64(torch.from_numpy(ref).to(DT[dtype]))
+    assert np.array_equal(f64(y[:, up(at)]), want)
+    y[:, up(at)] = 0
+    assert not y.any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M, N, K", [(13, 4096, 4096), (100, 1024, 4096), (128, 4096, 14336), (300, 1000, 2064),
+                                     (700, 4000, 1040), (1100, 14340, 1168)])
+def test_linear_equal_rows_give_equal_rows(M, N, K, dtype):
+    """The same row everywhere: every row of y has the same bits, whatever tile it lies in."""
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    xq, xs = lb.lowbit_quantize_act_f8(torch.randn(1, K, generator=gen, device=DEV))
+    wq, ws = lb.lowbit_quantize_weight_f8(torch.randn(N, K, generator=gen, device=DEV))
+    xq = xq.view(torch.uint8).expand(M, -1).contiguous().view(F8)
+    y = lb.lowbit_linear_f8(xq, xs.expand(M, -1).contiguous(), wq, ws, None, DT[dtype])
+    assert torch.equal(y, y[:1].expand_as(y)) and torch.isfinite(y).all() and (y != 0).any()
+
+
 # ---------------------------------------------------------------- modules --
 
 def test_cast_modules_compute_in_the_new_type():
