@@ -4,7 +4,8 @@ Every step of the computation runs in the HIP library liblowbit.so; this module
 only turns torch tensors into device pointers and sizes, allocates outputs with
 torch when the caller does not pass them, and raises LowbitError on a non-OK
 status.  There is no fallback: if the library is missing or fails to load,
-every call raises.
+every call raises.  Only pointers are handed over, so results carry no gradient,
+also where an input requires one (the torch ops raise in the backward pass).
 """
 from __future__ import annotations
 

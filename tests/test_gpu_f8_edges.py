@@ -237,7 +237,7 @@ def test_16_bit_outputs_lose_no_more_than_the_cuts(M, N, K, dtype):
     assert one / (500 if dtype == "f16" else 50) > bound
 
 
-VARIANTS = [(3, 300, 400), (64, 640, 2048), (200, 2500, 1040), (600, 14340, 528)]
+VARIANTS = [(3, 300, 400), (64, 640, 2048), (200, 2500, 1040), (600, 14340, 528), (600, 14340, 1040)]
 
 
 @pytest.mark.parametrize("M, N, K", VARIANTS)
@@ -291,7 +291,7 @@ def test_linear_of_a_weight_past_4_gib(M, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M, N, K", [(13, 4096, 4096), (100, 1024, 4096), (128, 4096, 14336), (300, 1000, 2064),
-                                     (700, 4000, 1040), (1100, 14340, 1168)])
+                                     (700, 4000, 1040), (600, 14340, 1040)])
 def test_linear_equal_rows_give_equal_rows(M, N, K, dtype):
     """The same row everywhere: every row of y has the same bits, whatever tile it lies in."""
     gen = torch.Generator(device=DEV).manual_seed(K)
