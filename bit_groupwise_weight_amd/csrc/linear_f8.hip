@@ -233,9 +233,13 @@ __device__ __attribute__((aligned(16))) const float kNanScales[4] = {
 // of 64 x 32; four groups on rings of two stages 10.9 and 12.5; 128 x 128: 600
 // rows 21.8 against 25.7, 1024 rows 24.4 against 27.2).
 // Bound by the weights' bytes with few rows (8 rows, 14336 x 4096: 11.2 us, 5.2
-// TB/s), in between by a step's fixed costs: its 1 KiB loads (some 50 cycles of
-// the issuing wave each), LDS reads and barrier, 0.5 to 1.3 us against 0.1 to 0.4
-// of MFMAs (1024 rows, 4096 x 4096, 128 x 128: 24 us, 1.4 PFLOP/s).  Measured and
+// TB/s), in between by LDS: a step of 128 x 128 in waves of 64 x 32 reads 96 KiB
+// and writes 32, 1024 cycles at 128 bytes each, for 512 cycles of MFMAs (64 x 64:
+// 384 for 128; 64 x 32: 288 for 64).  Two blocks' steps take 1.29 us (0.57,
+// 0.46), of which that is 0.85 (0.32, 0.24) at 2.4 GHz and more at the clock that
+// the power leaves; the rest are the 1 KiB loads (some 50 cycles of the issuing
+// wave each) and the barrier.  1024 rows, 4096 x 4096, 128 x 128: 24 us, 1.4
+// PFLOP/s.  What follows moves no fewer bytes through LDS; measured and
 // not kept: loads before the LDS reads (64 x 64, 512 rows, 4096 x 4096: 18.1
 // against 17.4), loads between the MFMAs (20.1 against 18.6), a ring of four
 // stages for 128 x 128, which leaves one block a CU (777 rows, 5000 x 4112: 46

@@ -80,7 +80,7 @@ __device__ __forceinline__ u32v2_t codes8(const float (&v)[8], const SpanScale& 
 // Bound by memory with many rows, by one round of latencies (load, row sum, row
 // maximum, store) with few: a row is read once and its values wait in registers
 // for the sum.  bf16 with residual to e4m3, MI355X: 8192 x 4096 43.5 us, 5.4 TB/s
-// (a copy of 1 GiB: 5.1); 1 x 4096 2.7 us.  int8, 128 x 14336: 4.1 us.
+// (a copy of 1 GiB: 5.1; a plain read of 4 GiB: 6.8); 1 x 4096 2.7 us.  int8, 128 x 14336: 4.1 us.
 template <int ACT, int FMT, int T, int C>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_q8_kernel(NormQ8Params p) {
   __shared__ float s_sum[2][T / 64];
