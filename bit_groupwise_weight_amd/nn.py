@@ -226,8 +226,16 @@ def _quantize_act_f8_fake(x):
     return _norm_out(x, _lb.Q8_F8)
 
 
+def _check_weight(w: torch.Tensor) -> None:
+    if w.dim() not in (2, 3) or w.numel() == 0:
+        raise ValueError("w must be [N, K] or [E, N, K], not empty")
+    if w.shape[-1] % 16:
+        raise ValueError(f"K={w.shape[-1]} must be a multiple of 16")
+
+
 @torch.library.custom_op("lowbit::quantize_weight_f8", mutates_args=())
 def quantize_weight_f8(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    _check_weight(w)
     if w.dtype not in _SZ_DTYPES:
         w = w.float()
     return _lb.lowbit_quantize_weight_f8(w.contiguous())
@@ -235,15 +243,18 @@ def quantize_weight_f8(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
 
 @quantize_weight_f8.register_fake
 def _quantize_weight_f8_fake(w):
-    if w.dim() not in (2, 3):
-        raise ValueError("w must be [N, K] or [E, N, K]")
+    _check_weight(w)
     N, K = w.shape[-2:]
     spans = (*w.shape[:-2], _lb._f8_blocks(N), _lb._f8_blocks(K))
     return w.new_empty(w.shape, dtype=torch.float8_e4m3fn), w.new_empty(spans, dtype=torch.float32)
 
 
-def _check_f8(xq, xscale, wq, wscale, bias, dtype) -> None:
+def _check_f8(xq, xscale, wq, wscale, bias, dtype, wdims=2) -> None:
+    if xq.dim() < 1 or wq.dim() != wdims:
+        raise ValueError(f"xq must be [..., K] and wq {'[N, K]' if wdims == 2 else '[E, N, K]'}")
     K = xq.shape[-1]
+    if K == 0 or K % 16:
+        raise ValueError(f"K={K} must be a positive multiple of 16")
     if wq.shape[-1] != K:
         raise ValueError(f"xq has K={K}, wq has K={wq.shape[-1]}")
     if xq.dtype != torch.float8_e4m3fn or wq.dtype != torch.float8_e4m3fn:
@@ -276,11 +287,21 @@ def _linear_f8_fake(xq, xscale, wq, wscale, bias, dtype):
     return xq.new_empty((*xq.shape[:-1], wq.shape[0]), dtype=dtype)
 
 
+def _check_grouped(xq, xscale, rows, offsets, wq, wscale, bias, dtype) -> None:
+    _check_f8(xq, xscale, wq, wscale, bias, dtype, wdims=3)
+    if xq.dim() != 2:
+        raise ValueError("xq must be [M, K]")
+    if offsets.shape != (wq.shape[0] + 1,) or offsets.dtype != torch.int32:
+        raise ValueError("offsets must be int32 [E + 1]")
+    if rows is not None and (rows.dim() != 1 or rows.dtype != torch.int32):
+        raise ValueError("rows must be int32 [T]")
+
+
 @torch.library.custom_op("lowbit::linear_f8_grouped", mutates_args=())
 def linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, rows: Optional[torch.Tensor],
                       offsets: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor,
                       bias: Optional[torch.Tensor], dtype: torch.dtype) -> torch.Tensor:
-    _check_f8(xq, xscale, wq, wscale, bias, dtype)
+    _check_grouped(xq, xscale, rows, offsets, wq, wscale, bias, dtype)
     return _lb.lowbit_linear_f8_grouped(xq.contiguous(), xscale.contiguous(), offsets, wq.contiguous(),
                                         wscale.contiguous(), None if bias is None else bias.contiguous(),
                                         dtype, rows=rows)
@@ -288,7 +309,7 @@ def linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, rows: Optional[tor
 
 @linear_f8_grouped.register_fake
 def _linear_f8_grouped_fake(xq, xscale, rows, offsets, wq, wscale, bias, dtype):
-    _check_f8(xq, xscale, wq, wscale, bias, dtype)
+    _check_grouped(xq, xscale, rows, offsets, wq, wscale, bias, dtype)
     T = xq.shape[0] if rows is None else rows.shape[0]
     return xq.new_empty((T, wq.shape[1]), dtype=dtype)
 

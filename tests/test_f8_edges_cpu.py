@@ -138,3 +138,44 @@ def test_a_shared_linear_with_a_filter():
     lnn.quantize_linears_f8(net, filter_fn=lambda m, name: names.append(name) or name != "b.1")
     assert names == ["a", "b.0", "b.1", "c.0", "d.0"]
     assert net["b"][0] is net["a"] is not lin and net["b"][1] is lin
+
+
+# -------------------------------------------------------- shape functions --
+
+F8, META = torch.float8_e4m3fn, "meta"
+
+
+def empty(*shape, dtype=torch.float32):
+    return torch.empty(shape, dtype=dtype, device=META)
+
+
+@pytest.mark.parametrize("call", [
+    lambda op: op.quantize_weight_f8(empty(8, 24)), lambda op: op.quantize_weight_f8(empty(8)),
+    lambda op: op.quantize_weight_f8(empty(2, 2, 8, 16)), lambda op: op.quantize_weight_f8(empty(0, 16)),
+    # a weight of one expert is no dense weight, nor the other way round
+    lambda op: op.linear_f8(empty(3, 256, dtype=F8), empty(3, 2), empty(1, 40, 256, dtype=F8), empty(1, 1, 2), None,
+                            torch.float16),
+    lambda op: op.linear_f8(empty(3, 24, dtype=F8), empty(3, 1), empty(40, 24, dtype=F8), empty(1, 1), None,
+                            torch.float16),
+    lambda op: grouped(op, wq=empty(40, 256, dtype=F8), ws=empty(1, 2)),
+    lambda op: grouped(op, xq=empty(2, 3, 256, dtype=F8), xs=empty(2, 3, 2)),
+    lambda op: grouped(op, off=empty(4, dtype=torch.int32)), lambda op: grouped(op, off=empty(5, dtype=torch.int64)),
+    lambda op: grouped(op, rows=empty(6, 1, dtype=torch.int32)), lambda op: grouped(op, rows=empty(6, dtype=torch.int64)),
+])
+def test_shape_functions_refuse_what_the_calls_refuse(call):
+    """On meta tensors (as under a compiler) these gave shapes for calls that raise on the GPU."""
+    with pytest.raises(ValueError):
+        call(torch.ops.lowbit)
+
+
+def grouped(op, **kw):
+    a = dict(xq=empty(3, 256, dtype=F8), xs=empty(3, 2), rows=empty(6, dtype=torch.int32), off=empty(5, dtype=torch.int32),
+             wq=empty(4, 40, 256, dtype=F8), ws=empty(4, 1, 2))
+    a.update(kw)
+    return op.linear_f8_grouped(a["xq"], a["xs"], a["rows"], a["off"], a["wq"], a["ws"], None, torch.bfloat16)
+
+
+def test_shape_functions_take_what_the_calls_take():
+    assert grouped(torch.ops.lowbit).shape == (6, 40) and grouped(torch.ops.lowbit, rows=None).shape == (3, 40)
+    q, s = torch.ops.lowbit.quantize_weight_f8(empty(2, 130, 272, dtype=torch.float64))
+    assert q.shape == (2, 130, 272) and s.shape == (2, 2, 3)
