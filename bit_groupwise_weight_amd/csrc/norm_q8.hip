@@ -238,10 +238,10 @@ hipError_t launch_norm_rows(const NormQ8Params& p, hipStream_t s) {
 
 // The threads of a row by its length alone, so that a row's result does not
 // depend on how many there are.  Up to 1024 values one wave a row, up to 8192 one
-// chunk a thread: the row's chunks rounded up to whole waves, past 512 threads to
-// pairs of them; beyond, 1024 threads with two or four chunks each.  us for many
-// rows / one row, bf16 with residual to e4m3 (T x C), at each width's upper end
-// and a little over it:
+// chunk a thread: the smallest power of two that holds them, or 3/4 or 5/8 of it
+// (in whole waves); beyond, 1024 threads with two or four chunks each.  us for
+// many rows / one row, bf16 with residual to e4m3 (T x C), at each width's upper
+// end and a little over it:
 //   K = 512     64 x 1: 12.4 / 2.4     256 x 1: 19.9 / 2.5     (16384 rows)
 //   K = 1024    64 x 2: 25.9 / 3.2     256 x 1: 30.8 / 2.5     (16384 rows)
 //   K = 1056   192 x 1: 29.3 / 2.5     256 x 1: 33.1 / 2.6     (16384 rows)
@@ -250,12 +250,12 @@ hipError_t launch_norm_rows(const NormQ8Params& p, hipStream_t s) {
 //   K = 2080   320 x 1: 51.9 / 2.6     384 x 1: 55.9   512 x 1: 60.4 / 2.6   (16131 rows)
 //   K = 2560   320 x 1: 46.1           384 x 1: 48.6   512 x 1: 52.1         (13107 rows)
 //   K = 2576   384 x 1: 51.1           448 x 1: 53.3   512 x 1: 53.7         (13025 rows)
-//   K = 3328   448 x 1: 45.9 / 2.6     512 x 1: 46.2 / 2.7     (10082 rows)
+//   K = 3328   512 x 1: 46.2 / 2.7     448 x 1: 45.9 / 2.6     (10082 rows; int8 3360: 33.0 and 33.1)
 //   K = 4096   512 x 1: 44.4 / 2.7     256 x 2: 46.9 / 3.5     (8192 rows)
-//   K = 4128   640 x 1: 53.0 / 2.8     768 x 1: 58.5   1024 x 1: 61.2 / 2.8  (8128 rows)
+//   K = 4128   640 x 1: 53.0 / 2.8     768 x 1: 58.5   1024 x 1: 61.2 / 2.8  (8128 rows; int8: 47.5, 48.4, 48.6)
 //   K = 5120   640 x 1: 50.6 / 2.8     768 x 1: 51.1   1024 x 1: 52.5 / 2.8  (6553 rows)
 //   K = 6144   768 x 1: 46.1 / 2.9     896 x 1: 46.8   1024 x 1: 47.4 / 2.9  (5461 rows)
-//   K = 7168   896 x 1: 45.4           1024 x 1: 45.6          (4681 rows)
+//   K = 7168  1024 x 1: 45.6           896 x 1: 45.4           (4681 rows; int8: 35.7 and 36.5)
 //   K = 8192  1024 x 1: 45.0 / 3.1     512 x 2: 46.9 / 3.6     (4096 rows)
 //   K = 8224  1024 x 2: 51.7 / 3.5     640 x 2: 52.3 / 3.6     (4080 rows; fewer threads gain nothing)
 //   K = 10240 1024 x 2: 49.6 / 3.5     640 x 2: 49.6 / 3.9     (3276 rows)
@@ -275,11 +275,9 @@ hipError_t launch_norm(const NormQ8Params& p, hipStream_t s) {
     case 4: return launch_norm_rows<ACT, FMT, 256, 1>(p, s);
     case 5: return launch_norm_rows<ACT, FMT, 320, 1>(p, s);
     case 6: return launch_norm_rows<ACT, FMT, 384, 1>(p, s);
-    case 7: return launch_norm_rows<ACT, FMT, 448, 1>(p, s);
-    case 8: return launch_norm_rows<ACT, FMT, 512, 1>(p, s);
+    case 7: case 8: return launch_norm_rows<ACT, FMT, 512, 1>(p, s);
     case 9: case 10: return launch_norm_rows<ACT, FMT, 640, 1>(p, s);
     case 11: case 12: return launch_norm_rows<ACT, FMT, 768, 1>(p, s);
-    case 13: case 14: return launch_norm_rows<ACT, FMT, 896, 1>(p, s);
     default: return launch_norm_rows<ACT, FMT, 1024, 1>(p, s);
   }
 }
