@@ -7,8 +7,9 @@
  *   call(capsule, x, y, M, workspace, workspace_bytes, stream) -> status
  *       calls fn with them and the per-call arguments (device pointers and
  *       the stream handle as Python ints, 0 for NULL).
- * and one for each entry point of the 8-bit path, named as it, which takes the
- * entry point's address in the loaded library and then its arguments.
+ * and one for each entry point of the 8-bit path, around the experts and of
+ * the adapters, named as it, which takes the entry point's address in the
+ * loaded library and then its arguments.
  * It does no arithmetic of the layer and holds no state beyond the capsule:
  * every argument is passed on unchanged and the library validates them.
  * (ctypes builds and converts fifteen argument objects per call; this takes
@@ -146,11 +147,43 @@ ENTRY(lowbit_linear_f8_workspace_bytes, 6, int64_t a1 = I64(1); int64_t a2 = I64
       int64_t a4 = I64(4); int64_t a5 = I64(5); lowbit_dtype a6 = (lowbit_dtype)INT(6);)
 #undef CALL
 
+#define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15)
+ENTRY(lowbit_moe_route, 15, const void* a1 = PTR(1); lowbit_dtype a2 = (lowbit_dtype)INT(2);
+      const float* a3 = (const float*)PTR(3); int64_t a4 = I64(4); int64_t a5 = I64(5); int64_t a6 = I64(6);
+      lowbit_route_score a7 = (lowbit_route_score)INT(7); int64_t a8 = I64(8); int64_t a9 = I64(9);
+      int a10 = INT(10); int a11 = INT(11); float a12 = (float)PyFloat_AsDouble(args[12]);
+      int32_t* a13 = (int32_t*)PTR(13); float* a14 = (float*)PTR(14); void* a15 = PTR(15);)
+#undef CALL
+#define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9)
+ENTRY(lowbit_group_rows, 9, const void* a1 = PTR(1); int a2 = INT(2); int64_t a3 = I64(3); int64_t a4 = I64(4);
+      int64_t a5 = I64(5); int32_t* a6 = (int32_t*)PTR(6); int32_t* a7 = (int32_t*)PTR(7);
+      int32_t* a8 = (int32_t*)PTR(8); void* a9 = PTR(9);)
+#undef CALL
+#define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11)
+ENTRY(lowbit_moe_combine, 11, const void* a1 = PTR(1); const int32_t* a2 = (const int32_t*)PTR(2);
+      const float* a3 = (const float*)PTR(3); const void* a4 = PTR(4); void* a5 = PTR(5);
+      lowbit_dtype a6 = (lowbit_dtype)INT(6); int64_t a7 = I64(7); int64_t a8 = I64(8); int64_t a9 = I64(9);
+      int64_t a10 = I64(10); void* a11 = PTR(11);)
+#undef CALL
+#define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15, a16, a17, a18)
+ENTRY(lowbit_lora, 18, const void* a1 = PTR(1); const void* a2 = PTR(2); const void* a3 = PTR(3);
+      const float* a4 = (const float*)PTR(4); const int32_t* a5 = (const int32_t*)PTR(5);
+      const int32_t* a6 = (const int32_t*)PTR(6); const void* a7 = PTR(7); void* a8 = PTR(8);
+      lowbit_dtype a9 = (lowbit_dtype)INT(9); int64_t a10 = I64(10); int64_t a11 = I64(11); int64_t a12 = I64(12);
+      int64_t a13 = I64(13); int64_t a14 = I64(14); int64_t a15 = I64(15); void* a16 = PTR(16);
+      size_t a17 = (size_t)I64(17); void* a18 = PTR(18);)
+#undef CALL
+#define CALL fn(a1, a2, a3, a4, a5, a6)
+ENTRY(lowbit_lora_workspace_bytes, 6, int64_t a1 = I64(1); int64_t a2 = I64(2); int64_t a3 = I64(3);
+      int64_t a4 = I64(4); int64_t a5 = I64(5); lowbit_dtype a6 = (lowbit_dtype)INT(6);)
+#undef CALL
+
 #define METHOD(name) \
   {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, "call " #name " at the address given first"}
 static PyMethodDef kMethods[] = {
     METHOD(lowbit_add_rmsnorm_q8), METHOD(lowbit_quantize_act_f8), METHOD(lowbit_linear_f8),
-    METHOD(lowbit_linear_f8_grouped), METHOD(lowbit_linear_f8_workspace_bytes),
+    METHOD(lowbit_linear_f8_grouped), METHOD(lowbit_linear_f8_workspace_bytes), METHOD(lowbit_moe_route),
+    METHOD(lowbit_group_rows), METHOD(lowbit_moe_combine), METHOD(lowbit_lora), METHOD(lowbit_lora_workspace_bytes),
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind one layer's fixed arguments"},
     {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call lowbit_linear for a bound layer"},
     {NULL, NULL, 0, NULL}};

@@ -45,6 +45,9 @@ def _units():
              ("device_scratch.hip", "device_scratch.o", []),
              ("act_quant.hip", "act_quant.o", ["-ffp-contract=off"]),
              ("norm_q8.hip", "norm_q8.o", ["-ffp-contract=off"]),
+             ("moe_route.hip", "moe_route.o", []),
+             ("moe_rows.hip", "moe_rows.o", ["-ffp-contract=off"]),
+             ("lora.hip", "lora.o", ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]),
              ("linear_f8.hip", "linear_f8.o", ["-mllvm", "-amdgpu-mfma-vgpr-form=1"])]
     for b in range(1, 8):
         units.append(("qmm_a8.hip", f"qmm_a8_b{b}.o",

@@ -255,6 +255,69 @@ struct LinearF8Plan {
 };
 hipError_t launch_linear_f8(const LinearF8Params&, const LinearF8Plan&, int out, hipStream_t);
 
+// ------------------------------------------- around the experts, adapters --
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopk = 64;
+constexpr int kRouteMaxGroups = 64;
+struct RouteParams {
+  const void* logits;     // T x E, act
+  const float* bias;      // E, or nullptr
+  int32_t* experts;       // T x topk
+  float* weights;         // T x topk
+  int64_t T;
+  int E, topk;
+  int sigmoid;            // 0: softmax
+  int groups;             // divides E
+  int groups_shift;       // log2(groups), rounded up
+  int topk_groups, group_best;
+  int renormalize;
+  float scale;
+};
+hipError_t launch_moe_route(const RouteParams&, int act, hipStream_t);
+
+struct GroupRowsParams {
+  const void* ids;        // S = T x topk, int32 or int64
+  int32_t* rows;          // S
+  int32_t* offsets;       // E + 1
+  int32_t* position;      // S, or nullptr
+  int64_t S;
+  int topk, E;
+};
+hipError_t launch_group_rows(const GroupRowsParams&, int id_bytes, hipStream_t);
+
+struct CombineParams {
+  const void* y;            // R x N, act
+  const int32_t* position;  // T x topk rows of y
+  const float* weights;     // T x topk
+  const void* residual;     // T x N, act, or nullptr
+  void* out;                // T x N, act (may be residual)
+  int64_t R, T;
+  int N, topk;
+};
+hipError_t launch_moe_combine(const CombineParams&, int act, hipStream_t);
+
+constexpr int kLoraMaxRank = 256;
+struct LoraParams {
+  const void* x;            // M x K, act, 16-byte aligned
+  const void* a;            // L x rank x K, act, 16-byte aligned
+  const void* b;            // L x N x rank, act, 16-byte aligned
+  const float* scales;      // L, or nullptr (ones)
+  const int32_t* rows;      // T, or nullptr (T == M, position t is row t)
+  const int32_t* offsets;   // L + 1
+  const void* base;         // M x N, act, or nullptr (zeros)
+  void* y;                  // M x N, act (may be base)
+  float* t;                 // workspace: splits x T x rank_pad
+  int64_t M, T;
+  int L, N, K;              // K % 16 == 0
+  int rank, rank_pad;       // rank % 8 == 0; rounded up to 16
+  int splits, k_split;      // K ranges of the first product, multiples of 32
+  int wide;                 // rows of base and y are whole 16-byte pieces
+};
+struct LoraPlan {
+  int shrink_mt, expand_mt; // row tiles of 16 in a block: 1 or 4
+};
+hipError_t launch_lora(const LoraParams&, const LoraPlan&, int act, hipStream_t);
+
 // ------------------------------------------------- library-owned scratch --
 // Size of the device array behind lowbit_linear_noalloc (per device).  The
 // largest K-split schedule of the MFMA path writes one fp32 partial per

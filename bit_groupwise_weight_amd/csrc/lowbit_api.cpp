@@ -746,6 +746,40 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
   return LOWBIT_OK;
 }
 
+// ------------------------------------------- around the experts, adapters --
+
+constexpr int64_t kLoraMaxN = int64_t(1) << 23;
+constexpr int64_t kLaunchBlocks = lowbit::kF8MaxThreads / 256;   // of 256 threads
+
+// Schedule of the adapters' two products: 64-row tiles where adapters have
+// rows for them, and enough K ranges of the first product to fill the device.
+struct LoraSchedule {
+  lowbit::LoraPlan plan;
+  int rank_pad, splits, k_split;
+  size_t bytes;
+};
+LoraSchedule lora_schedule(int64_t T, int64_t L, int64_t rank, int64_t K) {
+  LoraSchedule s{};
+  const int64_t each = T / std::min(T, L);
+  const int mt = each >= 32 && rank <= 128 ? 4 : 1;
+  s.plan = {mt, mt};
+  s.rank_pad = static_cast<int>((rank + 15) / 16 * 16);
+  const int64_t tiles = std::max<int64_t>((T + 16 * mt - 1) / (16 * mt), 1) * ((rank + 63) / 64);
+  const int64_t want = std::max<int64_t>(2 * device_cus() / tiles, 1);
+  const int64_t most = std::max<int64_t>((K + 255) / 256, 1);
+  int64_t splits = std::min<int64_t>({want, most, 64});
+  s.k_split = static_cast<int>(((K + splits - 1) / splits + 127) / 128 * 128);
+  s.splits = static_cast<int>((K + s.k_split - 1) / s.k_split);
+  s.bytes = static_cast<size_t>(s.splits) * T * s.rank_pad * sizeof(float);
+  return s;
+}
+
+bool lora_sizes_ok(int64_t T, int64_t L, int64_t rank, int64_t N, int64_t K) {
+  return T >= 0 && T <= kMaxDim && L >= 1 && L <= kF8MaxExperts && rank >= 8 && rank % 8 == 0 &&
+         rank <= lowbit::kLoraMaxRank && N >= 1 && N <= kLoraMaxN && K >= 16 && K % 16 == 0 && K <= kQ8MaxK &&
+         (T / 16 + std::min(T, L + 2)) * ((N + 255) / 256) < kLaunchBlocks;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1090,6 +1124,150 @@ lowbit_status lowbit_linear_f8_grouped(const uint8_t* xq, const float* xscale, c
     return fail(LOWBIT_ERR_INVALID_ARG, "without rows, xq's M=%lld must be y's T=%lld", (long long)M, (long long)T);
   return run_linear_f8(xq, xscale, rows, offsets, wq, wscale, bias, y, dtype, M, T, E, N, K, workspace,
                        workspace_bytes, stream);
+}
+
+lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const float* bias, int64_t T,
+                               int64_t E, int64_t topk, lowbit_route_score score, int64_t groups,
+                               int64_t topk_groups, int group_best, int renormalize, float scale,
+                               int32_t* experts, float* weights, void* stream) {
+  g_last_error.clear();
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  if (score != LOWBIT_ROUTE_SOFTMAX && score != LOWBIT_ROUTE_SIGMOID)
+    return fail(LOWBIT_ERR_UNSUPPORTED, "score=%d", (int)score);
+  if (T < 0 || T > kMaxDim) return fail(LOWBIT_ERR_INVALID_ARG, "T=%lld not in 0..2^30", (long long)T);
+  if (E < 1 || E > lowbit::kRouteMaxExperts)
+    return fail(LOWBIT_ERR_INVALID_ARG, "E=%lld not in 1..%d", (long long)E, lowbit::kRouteMaxExperts);
+  if (topk < 1 || topk > E || topk > lowbit::kRouteMaxTopk)
+    return fail(LOWBIT_ERR_INVALID_ARG, "topk=%lld not in 1..min(E, %d)", (long long)topk, lowbit::kRouteMaxTopk);
+  if (groups < 1 || groups > lowbit::kRouteMaxGroups || E % groups != 0)
+    return fail(LOWBIT_ERR_INVALID_ARG, "groups=%lld must be a divisor of E=%lld, at most %d", (long long)groups,
+                (long long)E, lowbit::kRouteMaxGroups);
+  if (topk_groups < 1 || topk_groups > groups)
+    return fail(LOWBIT_ERR_INVALID_ARG, "topk_groups=%lld not in 1..groups", (long long)topk_groups);
+  if (group_best != 1 && group_best != 2) return fail(LOWBIT_ERR_INVALID_ARG, "group_best=%d not 1 or 2", group_best);
+  if (!std::isfinite(scale)) return fail(LOWBIT_ERR_INVALID_ARG, "scale=%g is not finite", scale);
+  if (T == 0) return LOWBIT_OK;
+  if (!logits || !experts || !weights) return fail(LOWBIT_ERR_INVALID_ARG, "NULL logits, experts or weights");
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(bias, 4) || !aligned(experts, 4) || !aligned(weights, 4))
+    return fail(LOWBIT_ERR_MISALIGNED, "arrays must be aligned to their element size");
+  lowbit::RouteParams p{};
+  p.logits = logits;
+  p.bias = bias;
+  p.experts = experts;
+  p.weights = weights;
+  p.T = T;
+  p.E = static_cast<int>(E);
+  p.topk = static_cast<int>(topk);
+  p.sigmoid = score == LOWBIT_ROUTE_SIGMOID;
+  p.groups = static_cast<int>(groups);
+  while ((int64_t{1} << p.groups_shift) < groups) ++p.groups_shift;
+  p.topk_groups = static_cast<int>(topk_groups);
+  p.group_best = group_best;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  const hipError_t e = lowbit::launch_moe_route(p, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "moe_route launch");
+  return LOWBIT_OK;
+}
+
+lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_t topk, int64_t E,
+                                int32_t* rows, int32_t* offsets, int32_t* position, void* stream) {
+  g_last_error.clear();
+  if (id_bytes != 4 && id_bytes != 8) return fail(LOWBIT_ERR_UNSUPPORTED, "id_bytes=%d not 4 or 8", id_bytes);
+  if (T < 0 || T > kMaxDim || topk < 1 || topk > kMaxDim || T * topk > kMaxDim)
+    return fail(LOWBIT_ERR_INVALID_ARG, "T=%lld topk=%lld: T * topk must be in 0..2^30, topk at least 1",
+                (long long)T, (long long)topk);
+  if (E < 1 || E > kF8MaxExperts) return fail(LOWBIT_ERR_INVALID_ARG, "E=%lld not in 1..2^16", (long long)E);
+  if (!offsets || (T > 0 && (!ids || !rows))) return fail(LOWBIT_ERR_INVALID_ARG, "NULL ids, rows or offsets");
+  if (!aligned(ids, id_bytes) || !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(position, 4))
+    return fail(LOWBIT_ERR_MISALIGNED, "arrays must be aligned to their element size");
+  const lowbit::GroupRowsParams p{ids, rows, offsets, position, T * topk, static_cast<int>(topk),
+                                  static_cast<int>(E)};
+  const hipError_t e = lowbit::launch_group_rows(p, id_bytes, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "group_rows launch");
+  return LOWBIT_OK;
+}
+
+lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const float* weights,
+                                 const void* residual, void* out, lowbit_dtype dtype, int64_t R, int64_t T,
+                                 int64_t topk, int64_t N, void* stream) {
+  g_last_error.clear();
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  if (T < 0 || T > kMaxDim || R < 0 || R > kMaxDim)
+    return fail(LOWBIT_ERR_INVALID_ARG, "rows T=%lld, R=%lld must be in 0..2^30", (long long)T, (long long)R);
+  if (topk < 1 || topk > (int64_t(1) << 16)) return fail(LOWBIT_ERR_INVALID_ARG, "topk=%lld not in 1..2^16", (long long)topk);
+  if (N < 1 || N > kMaxDim || T * ((N + 255) / 256) >= kLaunchBlocks)
+    return fail(LOWBIT_ERR_INVALID_ARG, "N=%lld T=%lld: N must be in 1..2^30, T * ceil(N / 256) below 2^24",
+                (long long)N, (long long)T);
+  if (T == 0) return LOWBIT_OK;
+  if (!position || !weights || !out || (R > 0 && !y))
+    return fail(LOWBIT_ERR_INVALID_ARG, "NULL y, position, weights or out");
+  const size_t e = dtype_bytes(dtype);
+  if (!aligned(y, e) || !aligned(residual, e) || !aligned(out, e) || !aligned(position, 4) || !aligned(weights, 4))
+    return fail(LOWBIT_ERR_MISALIGNED, "arrays must be aligned to their element size");
+  const lowbit::CombineParams p{y, position, weights, residual, out, R, T, static_cast<int>(N),
+                                static_cast<int>(topk)};
+  const hipError_t he = lowbit::launch_moe_combine(p, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (he != hipSuccess) return hip_fail(he, "moe_combine launch");
+  return LOWBIT_OK;
+}
+
+size_t lowbit_lora_workspace_bytes(int64_t T, int64_t L, int64_t rank, int64_t N, int64_t K,
+                                   lowbit_dtype dtype) {
+  if (!lora_sizes_ok(T, L, rank, N, K) || T == 0 || !valid_dtype(dtype)) return 0;
+  return lora_schedule(T, L, rank, K).bytes;
+}
+
+lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const float* scales,
+                          const int32_t* rows, const int32_t* offsets, const void* base, void* y,
+                          lowbit_dtype dtype, int64_t M, int64_t T, int64_t L, int64_t rank, int64_t N,
+                          int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
+  if (M < 0 || M > kMaxDim || !lora_sizes_ok(T, L, rank, N, K))
+    return fail(LOWBIT_ERR_INVALID_ARG,
+                "M=%lld T=%lld L=%lld rank=%lld N=%lld K=%lld: rows in 0..2^30, L in 1..2^16, rank a multiple of 8 "
+                "up to 256, K a multiple of 16 up to 2^23, N in 1..2^23, fewer than 2^24 tiles of 16 x 256",
+                (long long)M, (long long)T, (long long)L, (long long)rank, (long long)N, (long long)K);
+  if (!rows && M != T) return fail(LOWBIT_ERR_INVALID_ARG, "without rows, M=%lld must be T=%lld", (long long)M, (long long)T);
+  if (!a || !b || !offsets) return fail(LOWBIT_ERR_INVALID_ARG, "NULL a, b or offsets");
+  if (workspace == nullptr && workspace_bytes != 0)
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace_bytes > 0 with a NULL workspace");
+  if (workspace != nullptr && !aligned(workspace, 256))
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (T == 0 || M == 0) return LOWBIT_OK;
+  if (!x || !y) return fail(LOWBIT_ERR_INVALID_ARG, "NULL x or y");
+  const size_t e = dtype_bytes(dtype);
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16))
+    return fail(LOWBIT_ERR_MISALIGNED, "x, a and b must be 16-byte aligned");
+  if (!aligned(scales, 4) || !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(base, e) || !aligned(y, e))
+    return fail(LOWBIT_ERR_MISALIGNED, "scales, rows, offsets, base and y must be aligned to their element size");
+  const LoraSchedule s = lora_schedule(T, L, rank, K);
+  if (workspace_bytes < s.bytes)
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, s.bytes);
+  lowbit::LoraParams p{};
+  p.x = x;
+  p.a = a;
+  p.b = b;
+  p.scales = scales;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.base = base;
+  p.y = y;
+  p.t = static_cast<float*>(workspace);
+  p.M = M;
+  p.T = T;
+  p.L = static_cast<int>(L);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.rank = static_cast<int>(rank);
+  p.rank_pad = s.rank_pad;
+  p.splits = s.splits;
+  p.k_split = s.k_split;
+  p.wide = N % 8 == 0 && aligned(base, 16) && aligned(y, 16);
+  const hipError_t he = lowbit::launch_lora(p, s.plan, act_kind(dtype), static_cast<hipStream_t>(stream));
+  if (he != hipSuccess) return hip_fail(he, "lora launch");
+  return LOWBIT_OK;
 }
 
 }  // extern "C"

@@ -27,6 +27,9 @@ STATUS_NAMES = {
 LOWBIT_F32, LOWBIT_F16, LOWBIT_BF16 = 0, 1, 2
 PATH_AUTO, PATH_QMV, PATH_QMM = 0, 1, 2
 Q8_NONE, Q8_I8, Q8_F8 = 0, 1, 2      # lowbit_q8_format
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1  # lowbit_route_score
+ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, ROUTE_MAX_GROUPS = 1024, 64, 64   # LOWBIT_ROUTE_MAX_*
+LORA_MAX_RANK = 256
 F8_BLOCK = 128                       # K elements (and weight rows) sharing an e4m3 scale
 _DTYPE_ENUM = {torch.float32: LOWBIT_F32, torch.float16: LOWBIT_F16, torch.bfloat16: LOWBIT_BF16}
 _ENUM_DTYPE = {v: k for k, v in _DTYPE_ENUM.items()}
@@ -37,7 +40,8 @@ EXPORTED_SYMBOLS = (
     "lowbit_status_string", "lowbit_last_error", "lowbit_linear_noalloc", "lowbit_set_tuning",
     "lowbit_quantize_act_i8", "lowbit_linear_a8", "lowbit_add_rmsnorm_q8", "lowbit_quantize_act_f8",
     "lowbit_quantize_weight_f8", "lowbit_linear_f8", "lowbit_linear_f8_grouped",
-    "lowbit_linear_f8_workspace_bytes",
+    "lowbit_linear_f8_workspace_bytes", "lowbit_moe_route", "lowbit_group_rows", "lowbit_moe_combine",
+    "lowbit_lora", "lowbit_lora_workspace_bytes",
 )
 ABI_VERSION = 3
 # schedule overrides (include/lowbit_tuning.h)
@@ -127,6 +131,17 @@ def load() -> ctypes.CDLL:
                                              c_i64, c_i64, vp, c_sz, vp]
     lib.lowbit_linear_f8_workspace_bytes.restype = c_sz
     lib.lowbit_linear_f8_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64, c_i64, ci]
+    lib.lowbit_moe_route.restype = ci
+    lib.lowbit_moe_route.argtypes = [vp, ci, vp, c_i64, c_i64, c_i64, ci, c_i64, c_i64, ci, ci, cf, vp, vp, vp]
+    lib.lowbit_group_rows.restype = ci
+    lib.lowbit_group_rows.argtypes = [vp, ci, c_i64, c_i64, c_i64, vp, vp, vp, vp]
+    lib.lowbit_moe_combine.restype = ci
+    lib.lowbit_moe_combine.argtypes = [vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64, c_i64, vp]
+    lib.lowbit_lora.restype = ci
+    lib.lowbit_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                vp, c_sz, vp]
+    lib.lowbit_lora_workspace_bytes.restype = c_sz
+    lib.lowbit_lora_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64, c_i64, ci]
     if lib.lowbit_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{path} has ABI version {lib.lowbit_abi_version()}, this binding "
                            f"expects {ABI_VERSION}: rebuild it with __graft_entry__.build()")
@@ -798,6 +813,171 @@ def lowbit_linear_f8_grouped(xq: torch.Tensor, xscale: torch.Tensor, offsets: to
                   0 if workspace is None else workspace.numel(), _stream_of(dev, stream))
     if st != LOWBIT_OK:
         _check(st, "lowbit_linear_f8_grouped")
+    return y
+
+
+def lowbit_moe_route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None,
+                     score: int = ROUTE_SOFTMAX, groups: int = 1, topk_groups: int = 1, group_best: int = 1,
+                     renormalize: bool = True, scale: float = 1.0, experts: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Each token's `topk` experts and their weights from logits[T, E].
+
+    Scores s are the softmax over the experts (ROUTE_SOFTMAX) or each logit's sigmoid
+    (ROUTE_SIGMOID); experts are chosen by s + bias (bias: float32 [E], not in the weights), of the
+    `topk_groups` best of `groups` groups of neighbouring experts, a group's value being its
+    largest choice (group_best 1) or the sum of its two largest (2).  Weights are s, divided by the
+    row's sum if `renormalize`, times `scale`.  Equal choices: the lowest index first.  A logit of
+    -inf masks its expert; slots that no expert is left for get -1 and weight 0; a row with a NaN
+    gets NaN weights.  Returns (experts int32 [T, topk], weights float32 [T, topk])."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [T, E]")
+    if logits.dtype not in _DTYPE_ENUM:
+        raise ValueError(f"logits dtype {logits.dtype} is not float32, float16 or bfloat16")
+    T, E = logits.shape
+    if not 1 <= topk <= E:
+        raise ValueError(f"topk={topk} not in 1..E={E}")
+    if bias is not None:
+        _expect_tensor(bias, "bias", (E,), torch.float32)
+    if experts is None:
+        experts = _made_on((T, topk), torch.int32, logits, stream)
+    else:
+        _expect_tensor(experts, "experts", (T, topk), torch.int32)
+    if weights is None:
+        weights = _made_on((T, topk), torch.float32, logits, stream)
+    else:
+        _expect_tensor(weights, "weights", (T, topk), torch.float32)
+    dev = _placed(logits, bias, experts, weights)
+    st = _call_on(dev, "lowbit_moe_route", _ptr(logits), _DTYPE_ENUM[logits.dtype], _ptr(bias), T, E, topk, score,
+                  groups, topk_groups, group_best, int(renormalize), scale, _ptr(experts), _ptr(weights),
+                  _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_moe_route")
+    return experts, weights
+
+
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def lowbit_group_rows(ids: torch.Tensor, E: int, rows: Optional[torch.Tensor] = None,
+                      offsets: Optional[torch.Tensor] = None, position: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The slots of ids[T, k] (int32 or int64, on the GPU) in the order of their expert, 0..E-1.
+
+    Returns (rows int32 [T * k], offsets int32 [E + 1], position int32 [T, k]): rows[p] is the token
+    of the p-th slot, offsets where each expert's begin (`rows` and `offsets` of
+    lowbit_linear_f8_grouped and lowbit_lora), position where each slot went (of
+    lowbit_moe_combine).  Slots whose id is no expert come last, with position -1."""
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError("ids must be 2-D [T, k]")
+    if ids.dtype not in _ID_BYTES:
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    if not 1 <= E <= 1 << 16:
+        raise ValueError(f"E={E} not in 1..2^16")
+    T, k = ids.shape
+    if rows is None:
+        rows = _made_on((T * k,), torch.int32, ids, stream)
+    else:
+        _expect_tensor(rows, "rows", (T * k,), torch.int32)
+    if offsets is None:
+        offsets = _made_on((E + 1,), torch.int32, ids, stream)
+    else:
+        _expect_tensor(offsets, "offsets", (E + 1,), torch.int32)
+    if position is None:
+        position = _made_on((T, k), torch.int32, ids, stream)
+    else:
+        _expect_tensor(position, "position", (T, k), torch.int32)
+    dev = _placed(ids, rows, offsets, position)
+    st = _call_on(dev, "lowbit_group_rows", _ptr(ids), _ID_BYTES[ids.dtype], T, k, E, _ptr(rows), _ptr(offsets),
+                  _ptr(position), _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_group_rows")
+    return rows, offsets, position
+
+
+def lowbit_moe_combine(y: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
+                       residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[position[t, j]] (+ residual[t]), summed in fp32.
+
+    y[R, N]: the experts' rows; position int32 [T, k] and weights float32 [T, k].  A negative
+    position adds nothing, one of R or more makes its row NaN.  `out` may be the residual itself."""
+    if y.dim() != 2 or position.dim() != 2:
+        raise ValueError("y must be [R, N] and position [T, k]")
+    dt = y.dtype
+    if dt not in _DTYPE_ENUM:
+        raise ValueError(f"y dtype {dt} is not float32, float16 or bfloat16")
+    R, N = y.shape
+    T, k = position.shape
+    _expect_tensor(position, "position", (T, k), torch.int32)
+    _expect_tensor(weights, "weights", (T, k), torch.float32)
+    if residual is not None:
+        _expect_tensor(residual, "residual", (T, N), dt)
+    if out is None:
+        out = _made_on((T, N), dt, y, stream)
+    else:
+        _expect_tensor(out, "out", (T, N), dt)
+    dev = _placed(y, position, weights, residual, out)
+    st = _call_on(dev, "lowbit_moe_combine", _ptr(y), _ptr(position), _ptr(weights), _ptr(residual), _ptr(out),
+                  _DTYPE_ENUM[dt], R, T, k, N, _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_moe_combine")
+    return out
+
+
+def lowbit_lora_workspace_bytes(T: int, L: int, rank: int, N: int, K: int, dtype: torch.dtype) -> int:
+    """Bytes lowbit_lora needs as workspace, on the current device."""
+    return load().lowbit_lora_workspace_bytes(T, L, rank, N, K, _DTYPE_ENUM[dtype])
+
+
+def lowbit_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: Optional[torch.Tensor],
+                rows: Optional[torch.Tensor], offsets: torch.Tensor, base: Optional[torch.Tensor],
+                y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """y = base + scales[l] * (x . a[l]^T) . b[l]^T, l the adapter of each row; rows without one
+    keep base (0 where base is None).
+
+    x[M, K], a[L, rank, K], b[L, N, rank], base[M, N] of one dtype, scales float32 [L] or None (1).
+    rows int32 [T] names the rows in the order of their adapter (None: T = M, as they stand),
+    offsets int32 [L + 1] where each adapter's begin: lowbit_group_rows(ids[:, None], L) makes both
+    for a batch, once for all its projections.  `y` may be base itself, which is then updated in
+    place.  (Rows that `rows` does not name are left as they are in y.)"""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [M, K], a [L, rank, K] and b [L, N, rank]")
+    dt = x.dtype
+    if dt not in _DTYPE_ENUM:
+        raise ValueError(f"x dtype {dt} is not float32, float16 or bfloat16")
+    M, K = x.shape
+    L, rank = a.shape[:2]
+    N = b.shape[1]
+    _expect_tensor(a, "a", (L, rank, K), dt)
+    _expect_tensor(b, "b", (L, N, rank), dt)
+    _expect_tensor(offsets, "offsets", (L + 1,), torch.int32)
+    if scales is not None:
+        _expect_tensor(scales, "scales", (L,), torch.float32)
+    T = M
+    if rows is not None:
+        if rows.dim() != 1:
+            raise ValueError("rows must be 1-D [T]")
+        T = rows.shape[0]
+        _expect_tensor(rows, "rows", (T,), torch.int32)
+    if base is not None:
+        _expect_tensor(base, "base", (M, N), dt)
+    if y is None:
+        y = _made_on((M, N), dt, x, stream)
+    else:
+        _expect_tensor(y, "y", (M, N), dt)
+    if workspace is not None and workspace.dtype is not torch.uint8:
+        raise ValueError("workspace must be uint8")
+    dev = _placed(x, a, b, scales, rows, offsets, base, y, workspace)
+    act = _DTYPE_ENUM[dt]
+    if workspace is None:
+        need = _call_on(dev, "lowbit_lora_workspace_bytes", T, L, rank, N, K, act)
+        workspace = None if need == 0 else _made_on((need,), torch.uint8, x, stream)
+    st = _call_on(dev, "lowbit_lora", _ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(rows), _ptr(offsets), _ptr(base),
+                  _ptr(y), act, M, T, L, rank, N, K, _ptr(workspace),
+                  0 if workspace is None else workspace.numel(), _stream_of(dev, stream))
+    if st != LOWBIT_OK:
+        _check(st, "lowbit_lora")
     return y
 
 

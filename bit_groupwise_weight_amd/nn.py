@@ -38,7 +38,18 @@ Ops (namespace ``lowbit``):
   the fp8 matrix cores;
 * ``lowbit::linear_f8_grouped(Tensor xq, Tensor xscale, Tensor? rows, Tensor
   offsets, Tensor wq, Tensor wscale, Tensor? bias, ScalarType dtype) ->
-  Tensor`` -- the same for rows grouped by expert.
+  Tensor`` -- the same for rows grouped by expert;
+* ``lowbit::moe_route(Tensor logits, Tensor? bias, int topk, int score, int
+  groups, int topk_groups, int group_best, bool renormalize, float scale) ->
+  (Tensor experts, Tensor weights)`` -- each token's experts and their weights;
+* ``lowbit::group_rows(Tensor ids, int num_experts) -> (Tensor rows, Tensor
+  offsets, Tensor position)`` -- the slots of ``ids[T, k]`` in the order of their
+  expert (or adapter);
+* ``lowbit::moe_combine(Tensor y, Tensor position, Tensor weights, Tensor?
+  residual) -> Tensor`` -- each token's weighted sum of its experts' rows;
+* ``lowbit::lora(Tensor x, Tensor a, Tensor b, Tensor? scales, Tensor? rows,
+  Tensor offsets, Tensor? base) -> Tensor`` -- ``base`` plus the low-rank adapter
+  of each row.
 
 All run in liblowbit.so through :mod:`bit_groupwise_weight_amd.lowbit`;
 nothing here computes on the CPU.
@@ -314,6 +325,133 @@ def _linear_f8_grouped_fake(xq, xscale, rows, offsets, wq, wscale, bias, dtype):
     return xq.new_empty((T, wq.shape[1]), dtype=dtype)
 
 
+# ------------------------------------------ ops, around the experts, adapters --
+
+def _check_route(logits, bias, topk, score, groups, topk_groups, group_best) -> int:
+    if logits.dim() < 1 or logits.dtype not in _SZ_DTYPES:
+        raise ValueError(f"logits must be [..., E] in one of {_SZ_DTYPES}")
+    E = logits.shape[-1]
+    if not 1 <= E <= _lb.ROUTE_MAX_EXPERTS:
+        raise ValueError(f"E={E} not in 1..{_lb.ROUTE_MAX_EXPERTS}")
+    if not 1 <= topk <= min(E, _lb.ROUTE_MAX_TOPK):
+        raise ValueError(f"topk={topk} not in 1..min(E, {_lb.ROUTE_MAX_TOPK})")
+    if score not in (_lb.ROUTE_SOFTMAX, _lb.ROUTE_SIGMOID):
+        raise ValueError(f"score must be ROUTE_SOFTMAX or ROUTE_SIGMOID, got {score}")
+    if not 1 <= groups <= _lb.ROUTE_MAX_GROUPS or E % groups:
+        raise ValueError(f"groups={groups} must be a divisor of E={E}, at most {_lb.ROUTE_MAX_GROUPS}")
+    if not 1 <= topk_groups <= groups or group_best not in (1, 2):
+        raise ValueError("topk_groups must be in 1..groups, group_best 1 or 2")
+    if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32):
+        raise ValueError("bias must be float32 [E]")
+    return E
+
+
+@torch.library.custom_op("lowbit::moe_route", mutates_args=())
+def moe_route(logits: torch.Tensor, bias: Optional[torch.Tensor], topk: int, score: int, groups: int,
+              topk_groups: int, group_best: int, renormalize: bool,
+              scale: float) -> Tuple[torch.Tensor, torch.Tensor]:
+    E = _check_route(logits, bias, topk, score, groups, topk_groups, group_best)
+    experts, weights = _lb.lowbit_moe_route(logits.reshape(-1, E).contiguous(), topk,
+                                            None if bias is None else bias.contiguous(), score, groups,
+                                            topk_groups, group_best, renormalize, scale)
+    shape = (*logits.shape[:-1], topk)
+    return experts.view(shape), weights.view(shape)
+
+
+@moe_route.register_fake
+def _moe_route_fake(logits, bias, topk, score, groups, topk_groups, group_best, renormalize, scale):
+    _check_route(logits, bias, topk, score, groups, topk_groups, group_best)
+    shape = (*logits.shape[:-1], topk)
+    return logits.new_empty(shape, dtype=torch.int32), logits.new_empty(shape, dtype=torch.float32)
+
+
+def _check_group_rows(ids: torch.Tensor, num_experts: int) -> None:
+    if ids.dim() != 2 or ids.shape[1] < 1 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be [T, k], int32 or int64")
+    if not 1 <= num_experts <= 1 << 16:
+        raise ValueError(f"num_experts={num_experts} not in 1..2^16")
+
+
+@torch.library.custom_op("lowbit::group_rows", mutates_args=())
+def group_rows(ids: torch.Tensor, num_experts: int) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    _check_group_rows(ids, num_experts)
+    return _lb.lowbit_group_rows(ids.contiguous(), num_experts)
+
+
+@group_rows.register_fake
+def _group_rows_fake(ids, num_experts):
+    _check_group_rows(ids, num_experts)
+    T, k = ids.shape
+    return (ids.new_empty((T * k,), dtype=torch.int32), ids.new_empty((num_experts + 1,), dtype=torch.int32),
+            ids.new_empty((T, k), dtype=torch.int32))
+
+
+def _check_combine(y, position, weights, residual) -> None:
+    if y.dim() != 2 or y.shape[1] < 1 or y.dtype not in _SZ_DTYPES:
+        raise ValueError(f"y must be [R, N] in one of {_SZ_DTYPES}")
+    if position.dim() != 2 or position.shape[1] < 1 or position.dtype != torch.int32:
+        raise ValueError("position must be int32 [T, k]")
+    if weights.shape != position.shape or weights.dtype != torch.float32:
+        raise ValueError("weights must be float32 [T, k]")
+    if residual is not None and (residual.shape != (position.shape[0], y.shape[1]) or residual.dtype != y.dtype):
+        raise ValueError("residual must be [T, N] in y's dtype")
+
+
+@torch.library.custom_op("lowbit::moe_combine", mutates_args=())
+def moe_combine(y: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
+                residual: Optional[torch.Tensor]) -> torch.Tensor:
+    _check_combine(y, position, weights, residual)
+    return _lb.lowbit_moe_combine(y.contiguous(), position.contiguous(), weights.contiguous(),
+                                  None if residual is None else residual.contiguous())
+
+
+@moe_combine.register_fake
+def _moe_combine_fake(y, position, weights, residual):
+    _check_combine(y, position, weights, residual)
+    return y.new_empty((position.shape[0], y.shape[1]))
+
+
+def _check_lora(x, a, b, scales, rows, offsets, base) -> Tuple[int, int]:
+    if x.dim() < 1 or x.dtype not in _SZ_DTYPES:
+        raise ValueError(f"x must be [..., K] in one of {_SZ_DTYPES}")
+    if a.dim() != 3 or b.dim() != 3 or a.dtype != x.dtype or b.dtype != x.dtype:
+        raise ValueError("a must be [L, rank, K] and b [L, N, rank] in x's dtype")
+    L, rank, K = a.shape
+    N = b.shape[1]
+    if x.shape[-1] != K or b.shape[0] != L or b.shape[2] != rank:
+        raise ValueError(f"x has K={x.shape[-1]}; a {list(a.shape)} and b {list(b.shape)} do not fit it and each other")
+    if L < 1 or N < 1 or K == 0 or K % 16 or rank == 0 or rank % 8 or rank > _lb.LORA_MAX_RANK:
+        raise ValueError(f"L and N must be positive, K a positive multiple of 16, rank one of 8 up to {_lb.LORA_MAX_RANK}")
+    if offsets.shape != (L + 1,) or offsets.dtype != torch.int32:
+        raise ValueError("offsets must be int32 [L + 1]")
+    if scales is not None and (scales.shape != (L,) or scales.dtype != torch.float32):
+        raise ValueError("scales must be float32 [L]")
+    if rows is not None and (rows.dim() != 1 or rows.dtype != torch.int32):
+        raise ValueError("rows must be int32 [T]")
+    if base is not None and (base.shape != (*x.shape[:-1], N) or base.dtype != x.dtype):
+        raise ValueError("base must be [..., N] in x's dtype")
+    return N, K
+
+
+@torch.library.custom_op("lowbit::lora", mutates_args=())
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: Optional[torch.Tensor],
+         rows: Optional[torch.Tensor], offsets: torch.Tensor, base: Optional[torch.Tensor]) -> torch.Tensor:
+    N, K = _check_lora(x, a, b, scales, rows, offsets, base)
+    x2 = x.reshape(-1, K).contiguous()
+    base2 = None if base is None else base.reshape(-1, N).contiguous()
+    y = None
+    if rows is not None and rows.shape[0] < x2.shape[0]:      # rows that are not named keep base, too
+        y = x2.new_zeros((x2.shape[0], N)) if base2 is None else base2.clone()
+    y = _lb.lowbit_lora(x2, a.contiguous(), b.contiguous(), scales, rows, offsets, base2, y=y)
+    return y.reshape(*x.shape[:-1], N)
+
+
+@lora.register_fake
+def _lora_fake(x, a, b, scales, rows, offsets, base):
+    N, _ = _check_lora(x, a, b, scales, rows, offsets, base)
+    return x.new_empty((*x.shape[:-1], N))
+
+
 # --------------------------------------------------------------- module --
 
 class LowbitLinear(torch.nn.Module):
@@ -587,25 +725,146 @@ class F8Experts(_F8Module):
         T, k = xq.shape[0], experts.shape[-1]
         if experts.shape != weights.shape or experts.numel() != T * k:
             raise ValueError("experts and weights must both be [T, k]")
-        ids = experts.reshape(-1).long()
-        order = torch.argsort(ids, stable=True)
-        # rows of the experts below each bound: where every expert's rows begin and end
-        bounds = torch.arange(self.num_experts + 1, device=ids.device, dtype=ids.dtype)
-        offsets = torch.searchsorted(ids[order], bounds).to(torch.int32)
-        rows = torch.div(order, k, rounding_mode="floor").to(torch.int32)
+        ids = experts.reshape(T, k)
+        if ids.dtype not in (torch.int32, torch.int64):
+            ids = ids.long()
+        rows, offsets, position = torch.ops.lowbit.group_rows(ids, self.num_experts)
         gu = torch.ops.lowbit.linear_f8_grouped(xq, xscale, rows, offsets, self.gate_up, self.gate_up_scale,
                                                 None, self.dtype)
         gate, up = gu.split(self.intermediate, dim=-1)
         aq, ascale = torch.ops.lowbit.quantize_act_f8(torch.nn.functional.silu(gate) * up)
         slots = torch.ops.lowbit.linear_f8_grouped(aq, ascale, None, offsets, self.down, self.down_scale,
                                                    None, self.dtype)
-        back = torch.empty_like(order)
-        back[order] = torch.arange(order.numel(), device=order.device)
-        out = slots[back].view(T, k, self.hidden).float() * weights.reshape(T, k, 1).float()
-        # (rows of no expert are undefined)
-        used = ((ids >= 0) & (ids < self.num_experts)).view(T, k, 1)
-        return torch.where(used, out, 0.0).sum(1).to(self.dtype)
+        # (rows of no expert are undefined; their slots have position -1 and add nothing)
+        return torch.ops.lowbit.moe_combine(slots, position, weights.reshape(T, k).float(), None)
 
     def extra_repr(self) -> str:
         return (f"num_experts={self.num_experts}, hidden={self.hidden}, intermediate={self.intermediate}, "
                 f"dtype={self.dtype}")
+
+
+class MoeRouter(torch.nn.Module):
+    """Chooses each token's experts for F8Experts from the router's logits.
+
+    ``score`` "softmax" or "sigmoid"; the experts of largest score (plus ``bias`` where the router
+    has one for balance, which the weights leave out) among the ``topk_groups`` best of ``groups``
+    groups, a group's value being its largest choice (``group_best`` 1) or the sum of its two
+    largest (2); weights renormalized over the chosen, times ``scale``.  The bias is a float32 buffer
+    and stays one when the module is cast.
+    """
+
+    def __init__(self, num_experts: int, topk: int, score: str = "softmax", bias: bool = False, groups: int = 1,
+                 topk_groups: int = 1, group_best: int = 1, renormalize: bool = True, scale: float = 1.0,
+                 device: Optional[torch.device] = None):
+        super().__init__()
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError(f'score must be "softmax" or "sigmoid", got {score!r}')
+        self.num_experts, self.topk, self.score, self.scale = num_experts, topk, score, float(scale)
+        self.groups, self.topk_groups, self.group_best = groups, topk_groups, group_best
+        self.renormalize = bool(renormalize)
+        _check_route(torch.empty((1, num_experts), device="meta"), None, topk, self._score(), groups, topk_groups,
+                     group_best)
+        if bias:
+            self.register_buffer("bias", torch.zeros((num_experts,), dtype=torch.float32, device=device))
+        else:
+            self.bias = None
+
+    def _score(self) -> int:
+        return _lb.ROUTE_SOFTMAX if self.score == "softmax" else _lb.ROUTE_SIGMOID
+
+    def _apply(self, fn, recurse=True):
+        def keep(t):
+            moved = fn(t)
+            return moved if moved.dtype == t.dtype else t.to(moved.device)
+
+        return super()._apply(keep, recurse)
+
+    def forward(self, logits: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+        """logits[..., E] -> (experts int32, weights float32), both [..., topk]."""
+        if logits.shape[-1:] != (self.num_experts,):
+            raise ValueError(f"logits must be [..., {self.num_experts}], got {list(logits.shape)}")
+        return torch.ops.lowbit.moe_route(logits, self.bias, self.topk, self._score(), self.groups,
+                                          self.topk_groups, self.group_best, self.renormalize, self.scale)
+
+    def extra_repr(self) -> str:
+        return (f"num_experts={self.num_experts}, topk={self.topk}, score={self.score}, groups={self.groups}, "
+                f"topk_groups={self.topk_groups}, renormalize={self.renormalize}, scale={self.scale}, "
+                f"bias={self.bias is not None}")
+
+
+def adapter_plan(ids: torch.Tensor, num_adapters: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The plan of a batch for its LoraLinear layers, from each row's adapter (any integer type;
+    outside 0..num_adapters-1: none): (rows, offsets), made on the GPU, good for every layer."""
+    ids = ids.reshape(-1, 1)
+    if ids.dtype not in (torch.int32, torch.int64):
+        ids = ids.long()
+    rows, offsets, _ = torch.ops.lowbit.group_rows(ids, num_adapters)
+    return rows, offsets
+
+
+class LoraLinear(torch.nn.Module):
+    """A linear (LowbitLinear, F8Linear, nn.Linear) shared by all rows with low-rank adapters of
+    many requests beside it:
+
+        y = linear(x) + scales[l] * b[l] (a[l] x),  l each row's adapter
+
+    Buffers: ``a`` (``[num_adapters, rank, K]``), ``b`` (``[num_adapters, N, rank]``, both in
+    ``dtype``, that of x and y) and ``scales`` (float32).  ``set_adapter`` puts an adapter of that
+    rank or less into its place while others are in use.
+    """
+
+    def __init__(self, linear: torch.nn.Module, num_adapters: int, rank: int,
+                 dtype: Optional[torch.dtype] = None, device: Optional[torch.device] = None):
+        super().__init__()
+        K, N = linear.in_features, linear.out_features
+        held = next((t for t in (*linear.buffers(), *linear.parameters())), None)
+        if device is None and held is not None:
+            device = held.device
+        if dtype is None:
+            dtype = getattr(linear, "dtype", None) or linear.weight.dtype
+        if dtype not in _SZ_DTYPES:
+            raise ValueError(f"dtype must be one of {_SZ_DTYPES}")
+        if num_adapters < 1 or K % 16 or rank <= 0 or rank % 8 or rank > _lb.LORA_MAX_RANK:
+            raise ValueError(f"num_adapters must be positive, in_features a multiple of 16 and rank one of 8 up to "
+                             f"{_lb.LORA_MAX_RANK}")
+        self.linear, self.num_adapters, self.rank = linear, num_adapters, rank
+        self.in_features, self.out_features = K, N
+        self.register_buffer("a", torch.zeros((num_adapters, rank, K), dtype=dtype, device=device))
+        self.register_buffer("b", torch.zeros((num_adapters, N, rank), dtype=dtype, device=device))
+        self.register_buffer("scales", torch.ones((num_adapters,), dtype=torch.float32, device=device))
+
+    def _apply(self, fn, recurse=True):
+        scales = self.scales
+
+        def keep(t):
+            moved = fn(t)
+            return t.to(moved.device) if t is scales else moved
+
+        return super()._apply(keep, recurse)
+
+    @torch.no_grad()
+    def set_adapter(self, index: int, a: torch.Tensor, b: torch.Tensor, scale: float = 1.0) -> "LoraLinear":
+        """Adapter ``index``: ``a[r, K]``, ``b[N, r]`` (r up to ``rank``) and its factor."""
+        r = a.shape[0]
+        if not 0 <= index < self.num_adapters:
+            raise ValueError(f"index={index} not in 0..{self.num_adapters - 1}")
+        if a.shape != (r, self.in_features) or b.shape != (self.out_features, r) or r > self.rank:
+            raise ValueError(f"a must be [r, {self.in_features}] and b [{self.out_features}, r], r at most {self.rank}")
+        self.a[index].zero_()
+        self.b[index].zero_()
+        self.a[index, :r].copy_(a)
+        self.b[index, :, :r].copy_(b)
+        self.scales[index] = scale
+        return self
+
+    def forward(self, x: torch.Tensor, plan: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> torch.Tensor:
+        """x[..., K] -> [..., N]; ``plan`` = adapter_plan(ids, num_adapters) for x's rows, None for
+        no adapters."""
+        y = self.linear(x)
+        if plan is None:
+            return y
+        return torch.ops.lowbit.lora(x, self.a, self.b, self.scales, plan[0], plan[1], y)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"num_adapters={self.num_adapters}, rank={self.rank}, dtype={self.a.dtype}")

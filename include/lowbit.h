@@ -433,6 +433,136 @@ lowbit_status lowbit_linear_f8_grouped(const uint8_t* xq, const float* xscale, c
                                        int64_t E, int64_t N, int64_t K, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the experts, and adapters beside a linear: the router that chooses
+ * each token's experts, the order of rows that lowbit_linear_f8_grouped and
+ * lowbit_lora take, the sum of a token's experts, and low-rank adapters of
+ * many requests.  All asynchronous and deterministic; nothing waits for
+ * device data on the host.
+ * ---------------------------------------------------------------------- */
+
+/* The score that lowbit_moe_route makes of a logit. */
+typedef enum lowbit_route_score {
+  LOWBIT_ROUTE_SOFTMAX = 0,  /* s_e = exp(l_e) / sum over all experts           */
+  LOWBIT_ROUTE_SIGMOID = 1   /* s_e = 1 / (1 + exp(-l_e))                       */
+} lowbit_route_score;
+
+#define LOWBIT_ROUTE_MAX_EXPERTS 1024
+#define LOWBIT_ROUTE_MAX_TOPK 64
+#define LOWBIT_ROUTE_MAX_GROUPS 64
+
+/* Each token's experts and their weights.  Per row of logits l:
+ *   c_e = s_e + bias_e                the value experts are chosen by
+ *   the experts stand in `groups` groups of E / groups neighbours; a group's
+ *   value is its largest c (group_best 1) or the sum of its two largest
+ *   (group_best 2; one, where the others are masked); the topk_groups groups
+ *   of largest value stay
+ *   experts[t] = the topk experts of largest c among those, in that order
+ *   weights[t, j] = scale * s_e, e = experts[t, j], with `renormalize` divided
+ *   by the sum of the row's chosen s
+ * Equal values: the lowest index first.  Without a bias (groups by group_best
+ * 1) experts are ordered by their logits; otherwise c is computed in 64 bits,
+ * so that rounding does not decide.  Weights are rounded once.
+ *
+ *   logits   device, T x E row-major, dtype, aligned to its element size.
+ *   bias     device, E fp32, or NULL.
+ *   T >= 0 (0 is a no-op; at most 2^30), 1 <= E <= 1024, 1 <= topk <=
+ *            min(E, 64), groups 1 .. 64 and a divisor of E, topk_groups 1 ..
+ *            groups, group_best 1 or 2, scale finite.
+ *   experts  device, T x topk int32.  Written.
+ *   weights  device, T x topk fp32.  Written.
+ *
+ * A logit or bias of -inf masks its expert.  Where fewer than topk experts are
+ * left, the row ends in experts -1 with weight 0 (lowbit_group_rows and
+ * lowbit_moe_combine leave such slots out).  A row with a NaN among its logits
+ * or choices (softmax: or a logit of +inf) gets experts 0 .. topk - 1 and
+ * weights NaN. */
+lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const float* bias, int64_t T,
+                               int64_t E, int64_t topk, lowbit_route_score score, int64_t groups,
+                               int64_t topk_groups, int group_best, int renormalize, float scale,
+                               int32_t* experts, float* weights, void* stream);
+
+/* Rows in the order of their expert (or adapter): a stable sort of the S = T *
+ * topk slots of `ids` by id.
+ *   position[s] = where slot s comes, -1 for an id outside 0 .. E - 1
+ *   rows[position[s]] = s / topk, the slot's token: the `rows` of
+ *            lowbit_linear_f8_grouped (and, with topk 1, of lowbit_lora)
+ *   offsets[e] = where expert e's rows begin; offsets[0] = 0, offsets[E] = the
+ *            number of slots that have an expert
+ * Slots without an expert come behind offsets[E] in `rows`, in their order.
+ *
+ *   ids      device, T x topk int32 or int64 (id_bytes 4 or 8), aligned to it.
+ *   T >= 0, topk >= 1, T * topk at most 2^30 (with T = 0 the offsets are
+ *            written, as 0), 1 <= E <= 2^16.
+ *   rows     device, T * topk int32.  Written.
+ *   offsets  device, E + 1 int32.  Written.
+ *   position device, T * topk int32, or NULL.  Written. */
+lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_t topk, int64_t E,
+                                int32_t* rows, int32_t* offsets, int32_t* position, void* stream);
+
+/* Each token's weighted sum of its experts' rows:
+ *   out[t] = sum over j of weights[t, j] * y[position[t, j]] (+ residual[t])
+ * in fp32, in the order of j, rounded once.  A slot of negative position adds
+ * nothing, whatever its weight; a position of R or more makes the row NaN.
+ *
+ *   y        device, R x N row-major, dtype (the rows of
+ *            lowbit_linear_f8_grouped).
+ *   position, weights   device, T x topk int32 and fp32, as
+ *            lowbit_group_rows and lowbit_moe_route write them.
+ *   residual device, T x N, dtype, or NULL.
+ *   out      device, T x N, dtype.  Overwritten; may be residual itself, must
+ *            not overlap an input otherwise.
+ *   T >= 0 (0 is a no-op; at most 2^30), 0 <= R <= 2^30, topk 1 .. 2^16,
+ *            N 1 .. 2^30, T * ceil(N / 256) < 2^24.
+ *   Every array is aligned to its element size; rows of whole 16-byte pieces
+ *   on 16-byte aligned arrays are the fast case. */
+lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const float* weights,
+                                 const void* residual, void* out, lowbit_dtype dtype, int64_t R, int64_t T,
+                                 int64_t topk, int64_t N, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   y[m] = base[m] + scales[l] * (x[m] . a[l]^T) . b[l]^T
+ * l the adapter of row m; a row without one keeps base[m] (0 without a base).
+ *
+ *   x        device, M x K row-major, dtype.
+ *   a, b     device, L x rank x K and L x N x rank row-major, dtype: each
+ *            adapter's two matrices as linears hold them ([out, in]); adapters
+ *            of smaller rank are filled up with zeros.
+ *   scales   device, L fp32, or NULL (ones).
+ *   rows     device, T int32, or NULL (then T == M and position t is row t):
+ *            the rows in the order of their adapter.  An index outside 0 ..
+ *            M - 1 is left out; a row named twice gets unspecified values; a
+ *            row that is not named keeps what y holds.
+ *   offsets  device, L + 1 int32, not decreasing, within 0 .. T: adapter l has
+ *            positions offsets[l] .. offsets[l + 1] - 1.  The positions before
+ *            offsets[0] and from offsets[L] on are rows without an adapter.
+ *            (Offsets are read on the device and cannot be refused: bad ones
+ *            leave unspecified values in y, and nothing outside the arrays is
+ *            read or written.)
+ *   base     device, M x N, dtype, or NULL.
+ *   y        device, M x N, dtype.  May be base itself (the delta is added in
+ *            place), must not overlap an input otherwise.
+ *   M, T >= 0 (0 is a no-op; at most 2^30), 1 <= L <= 2^16, rank a multiple of
+ *            8 up to 256, K a positive multiple of 16 up to 2^23, N 1 .. 2^23,
+ *            (floor(T / 16) + min(T, L + 2)) * ceil(N / 256) < 2^24.
+ *   x, a and b 16-byte aligned, the other arrays to their element size; rows
+ *   of base and y of whole 16-byte pieces are the fast case.
+ *   workspace: at least lowbit_lora_workspace_bytes(), 256-byte aligned (NULL
+ *            where that is 0); its contents on entry do not matter; calls that
+ *            may run at the same time must not share one.
+ *
+ * Sums are fp32.  x . a^T stays fp32, and enters the second product as a sum
+ * of two numbers of dtype (2^-16 of it in bf16, less in fp16; fp32: as it is);
+ * y is rounded once, to nearest even. */
+lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const float* scales,
+                          const int32_t* rows, const int32_t* offsets, const void* base, void* y,
+                          lowbit_dtype dtype, int64_t M, int64_t T, int64_t L, int64_t rank, int64_t N,
+                          int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that lowbit_lora needs on the current device (0: none). */
+size_t lowbit_lora_workspace_bytes(int64_t T, int64_t L, int64_t rank, int64_t N, int64_t K,
+                                   lowbit_dtype dtype);
+
 /* Static text for a status code. */
 const char* lowbit_status_string(lowbit_status status);
 
