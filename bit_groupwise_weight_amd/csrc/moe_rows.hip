@@ -7,7 +7,8 @@
 // Slots whose id is no expert come behind all others, with position -1.
 //
 // combine: out[t] = sum_j weights[t, j] * y[position[t, j]] (+ residual[t]) in
-// fp32, products rounded before they are added, in the order of j.
+// fp32, products rounded before they are added: four sums, of the slots j, j +
+// 4, ..., which then meet in order, and the residual last.
 #include "f8_common.h"
 
 namespace lowbit {
@@ -101,11 +102,11 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(CombinePar
   const int n = (run * kCombineThreads + static_cast<int>(threadIdx.x)) * PIECE;
   if (n >= p.N) return;
   const T* y = static_cast<const T*>(p.y);
-  float sum[PIECE] = {};
-  for (int j = 0; j < p.topk; ++j) {
+  float part[4][PIECE] = {};
+  auto add = [&](int j, float (&sum)[PIECE]) {
     const int64_t at = p.position[t * p.topk + j];
     const float w = p.weights[t * p.topk + j];
-    if (at < 0) continue;
+    if (at < 0) return;
     float v[PIECE];
     if (at >= p.R) {
 #pragma unroll
@@ -117,7 +118,15 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(CombinePar
     }
 #pragma unroll
     for (int i = 0; i < PIECE; ++i) sum[i] += w * v[i];
+  };
+  for (int j0 = 0; j0 < p.topk; j0 += 4) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (j0 + q < p.topk) add(j0 + q, part[q]);
   }
+  float sum[PIECE];
+#pragma unroll
+  for (int i = 0; i < PIECE; ++i) sum[i] = ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i];
   if (p.residual) {
     float v[PIECE];
     const T* r = static_cast<const T*>(p.residual) + t * p.N;

@@ -502,8 +502,9 @@ lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_
 
 /* Each token's weighted sum of its experts' rows:
  *   out[t] = sum over j of weights[t, j] * y[position[t, j]] (+ residual[t])
- * in fp32, in the order of j, rounded once.  A slot of negative position adds
- * nothing, whatever its weight; a position of R or more makes the row NaN.
+ * in fp32 (four sums, of the slots j, j + 4, ..., which then meet in order, and
+ * the residual last), rounded once.  A slot of negative position adds nothing,
+ * whatever its weight; a position of R or more makes the row NaN.
  *
  *   y        device, R x N row-major, dtype (the rows of
  *            lowbit_linear_f8_grouped).

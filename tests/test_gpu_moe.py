@@ -3,7 +3,7 @@ the experts' sum, and the run of them with the linears by expert.
 
 Tolerances, from the arithmetic (u = 2^-24, half a step of fp32):
   * route: experts are equal.  Weights are computed in 64 bits from the logits and rounded once: u of
-    themselves, taken as 1.01 u for the 64-bit steps.  Softmax without renormalization, without a
+    themselves, taken as 1.01 u for the 64-bit steps (scale is the call's, an fp32 number).  Softmax without renormalization, without a
     bias, divides by a sum of fp32 exps: an exp of x = l - top is off by x's rounding, u |x| e^x <=
     0.37 u, and by its own, 2 u (a unit in the last place); up to 32 values of a lane and 6 steps
     over the lanes add 38 u: 42 u with the rounding of the result;
@@ -47,7 +47,7 @@ def check_route(logits, k, bias=None, sigmoid=False, groups=1, topk_groups=1, be
                               score=lb.ROUTE_SIGMOID if sigmoid else lb.ROUTE_SOFTMAX, groups=groups,
                               topk_groups=topk_groups, group_best=best, renormalize=renormalize, scale=scale)
     e, w = o.route(f64(logits), k, bias=None if bias is None else f64(bias), sigmoid=sigmoid, groups=groups,
-                   topk_groups=topk_groups, best=best, renormalize=renormalize, scale=scale)
+                   topk_groups=topk_groups, best=best, renormalize=renormalize, scale=float(np.float32(scale)))
     assert got[0].dtype == torch.int32 and got[1].dtype == torch.float32
     assert np.array_equal(got[0].cpu().numpy(), e)
     g = f64(got[1])
