@@ -154,10 +154,13 @@ ENTRY(lowbit_moe_route, 15, const void* a1 = PTR(1); lowbit_dtype a2 = (lowbit_d
       int a10 = INT(10); int a11 = INT(11); float a12 = (float)PyFloat_AsDouble(args[12]);
       int32_t* a13 = (int32_t*)PTR(13); float* a14 = (float*)PTR(14); void* a15 = PTR(15);)
 #undef CALL
-#define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9)
-ENTRY(lowbit_group_rows, 9, const void* a1 = PTR(1); int a2 = INT(2); int64_t a3 = I64(3); int64_t a4 = I64(4);
+#define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11)
+ENTRY(lowbit_group_rows, 11, const void* a1 = PTR(1); int a2 = INT(2); int64_t a3 = I64(3); int64_t a4 = I64(4);
       int64_t a5 = I64(5); int32_t* a6 = (int32_t*)PTR(6); int32_t* a7 = (int32_t*)PTR(7);
-      int32_t* a8 = (int32_t*)PTR(8); void* a9 = PTR(9);)
+      int32_t* a8 = (int32_t*)PTR(8); void* a9 = PTR(9); size_t a10 = (size_t)I64(10); void* a11 = PTR(11);)
+#undef CALL
+#define CALL fn(a1, a2, a3)
+ENTRY(lowbit_group_rows_workspace_bytes, 3, int64_t a1 = I64(1); int64_t a2 = I64(2); int64_t a3 = I64(3);)
 #undef CALL
 #define CALL fn(a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11)
 ENTRY(lowbit_moe_combine, 11, const void* a1 = PTR(1); const int32_t* a2 = (const int32_t*)PTR(2);
@@ -183,7 +186,7 @@ ENTRY(lowbit_lora_workspace_bytes, 6, int64_t a1 = I64(1); int64_t a2 = I64(2); 
 static PyMethodDef kMethods[] = {
     METHOD(lowbit_add_rmsnorm_q8), METHOD(lowbit_quantize_act_f8), METHOD(lowbit_linear_f8),
     METHOD(lowbit_linear_f8_grouped), METHOD(lowbit_linear_f8_workspace_bytes), METHOD(lowbit_moe_route),
-    METHOD(lowbit_group_rows), METHOD(lowbit_moe_combine), METHOD(lowbit_lora), METHOD(lowbit_lora_workspace_bytes),
+    METHOD(lowbit_group_rows), METHOD(lowbit_group_rows_workspace_bytes), METHOD(lowbit_moe_combine), METHOD(lowbit_lora), METHOD(lowbit_lora_workspace_bytes),
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind one layer's fixed arguments"},
     {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call lowbit_linear for a bound layer"},
     {NULL, NULL, 0, NULL}};

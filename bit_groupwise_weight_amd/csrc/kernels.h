@@ -275,13 +275,18 @@ struct RouteParams {
 };
 hipError_t launch_moe_route(const RouteParams&, int act, hipStream_t);
 
+// Slots of a block of group_rows' two launches.
+constexpr int64_t group_chunk(int64_t S) { return S <= 128 * 1024 ? 1024 : 4096; }
 struct GroupRowsParams {
   const void* ids;        // S = T x topk, int32 or int64
   int32_t* rows;          // S
   int32_t* offsets;       // E + 1
   int32_t* position;      // S, or nullptr
-  int64_t S;
-  int topk, E;
+  int64_t S;              // at most 2^30
+  int E;
+  uint32_t topk_mul;      // s / topk == (s * topk_mul) >> topk_shift for 0 <= s < 2^30
+  int topk_shift;
+  int* counts;            // workspace: ceil(S / group_chunk(S)) x (E + 1), or nullptr (one launch)
 };
 hipError_t launch_group_rows(const GroupRowsParams&, int id_bytes, hipStream_t);
 

@@ -748,6 +748,10 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
 
 // ------------------------------------------- around the experts, adapters --
 
+// group_rows: the slots that one launch, a block an expert, sorts no slower than
+// two over chunks (both sides' times stand at the kernels), and the experts whose
+// counts by wave fit the LDS that the two take (18 arrays of E + 2 in 64 KiB).
+constexpr int64_t kGroupOneLaunch = 16384, kGroupChunkExperts = 900;
 constexpr int64_t kLoraMaxN = int64_t(1) << 23;
 constexpr int64_t kLaunchBlocks = lowbit::kF8MaxThreads / 256;   // of 256 threads
 
@@ -1170,8 +1174,16 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
   return LOWBIT_OK;
 }
 
+size_t lowbit_group_rows_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
+  if (T <= 0 || T > kMaxDim || topk < 1 || topk > kMaxDim || T * topk > kMaxDim || E < 1 || E > kF8MaxExperts) return 0;
+  const int64_t S = T * topk;
+  if (S <= kGroupOneLaunch || E > kGroupChunkExperts) return 0;
+  return static_cast<size_t>((S + lowbit::group_chunk(S) - 1) / lowbit::group_chunk(S)) * (E + 1) * sizeof(int);
+}
+
 lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_t topk, int64_t E,
-                                int32_t* rows, int32_t* offsets, int32_t* position, void* stream) {
+                                int32_t* rows, int32_t* offsets, int32_t* position, void* workspace,
+                                size_t workspace_bytes, void* stream) {
   g_last_error.clear();
   if (id_bytes != 4 && id_bytes != 8) return fail(LOWBIT_ERR_UNSUPPORTED, "id_bytes=%d not 4 or 8", id_bytes);
   if (T < 0 || T > kMaxDim || topk < 1 || topk > kMaxDim || T * topk > kMaxDim)
@@ -1181,8 +1193,19 @@ lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_
   if (!offsets || (T > 0 && (!ids || !rows))) return fail(LOWBIT_ERR_INVALID_ARG, "NULL ids, rows or offsets");
   if (!aligned(ids, id_bytes) || !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(position, 4))
     return fail(LOWBIT_ERR_MISALIGNED, "arrays must be aligned to their element size");
-  const lowbit::GroupRowsParams p{ids, rows, offsets, position, T * topk, static_cast<int>(topk),
-                                  static_cast<int>(E)};
+  if (workspace == nullptr && workspace_bytes != 0)
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace_bytes > 0 with a NULL workspace");
+  if (workspace != nullptr && !aligned(workspace, 256))
+    return fail(LOWBIT_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  // Division by topk: with m = floor(2^b / topk) + 1, b = 30 + ceil(log2(topk)),
+  // s * m / 2^b is s / topk plus less than s * topk / (2^b topk) <= s / (2^30 topk),
+  // too little to reach the next whole number for s < 2^30.
+  int shift = 30;
+  while ((int64_t{1} << (shift - 30)) < topk) ++shift;
+  const uint32_t mul = static_cast<uint32_t>((uint64_t{1} << shift) / static_cast<uint64_t>(topk) + 1);
+  const size_t need = lowbit_group_rows_workspace_bytes(T, topk, E);
+  const lowbit::GroupRowsParams p{ids, rows, offsets, position, T * topk, static_cast<int>(E), mul, shift,
+                                  need > 0 && workspace_bytes >= need ? static_cast<int*>(workspace) : nullptr};
   const hipError_t e = lowbit::launch_group_rows(p, id_bytes, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "group_rows launch");
   return LOWBIT_OK;

@@ -9,157 +9,368 @@
 // combine: out[t] = sum_j weights[t, j] * y[position[t, j]] (+ residual[t]) in
 // fp32, products rounded before they are added: four sums, of the slots j, j +
 // 4, ..., which then meet in order, and the residual last.
-#include "f8_common.h"
+#include "pieces.h"
 
 namespace lowbit {
 
 namespace {
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+// An id as an expert: E for one that is none.
+__device__ __forceinline__ uint32_t expert_of(int32_t id, uint32_t E) {
+  return min(static_cast<uint32_t>(id), E);              // (a negative one is large)
+}
+__device__ __forceinline__ uint32_t expert_of(int64_t id, uint32_t E) {
+  return (static_cast<uint64_t>(id) >> 32) != 0 ? E : min(static_cast<uint32_t>(id), E);
 }
 
 }  // namespace
 
 // Block e finds the slots of expert e by itself (block E: those of none): it
 // reads all ids, which lie in cache, counts the smaller ones and its own, and
-// then writes its own in order.  No block waits for another, and nothing hangs
-// on the order of atomics.  Wave w has a run of the slots.
+// then writes its own in order.  No block waits for another, nothing hangs on
+// the order of atomics, and one launch does.  A wave takes runs of 64 steps of
+// 64 slots; step i's own slots are a 64-bit mask that lane i keeps, so that the
+// second pass costs a prefix sum and a turn for each bit of the fullest mask.
+// (One run a wave where S allows it; otherwise the masks are made again.)
+// Bound by a launch up to some 4096 slots (64 tokens of 8 in 64 experts: 3.1
+// us, an empty launch 2.7) and by every block's reading of all ids from there.
 template <class ID, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupRowsParams p) {
   __shared__ int s_below[WAVES], s_own[WAVES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = static_cast<int>(blockIdx.x);
-  const ID* ids = static_cast<const ID*>(p.ids);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int STEPS = 16;                  // asked for at once
+  const uint32_t e = blockIdx.x, E = static_cast<uint32_t>(p.E);
   const int S = static_cast<int>(p.S);
-  const int run = (S + WAVES * 64 - 1) / (WAVES * 64) * 64;
-  const int begin = min(wave * run, S), end = min(begin + run, S);
-  auto id_at = [&](int s) {
-    const ID id = ids[s];
-    return id >= 0 && id < p.E ? static_cast<int>(id) : p.E;
-  };
+  const int steps = (S + WAVES * 64 - 1) / (WAVES * 64);   // of a wave
+  const int runs = (steps + 63) / 64;
+  const int begin = wave * steps * 64;       // (may be past S: less than 2^30 + 2^10)
 
-  int below = 0, own = 0;
-  for (int s = begin + lane; s < end; s += 64) {
-    const int id = id_at(s);
-    below += id < e;
-    own += id == e;
-  }
-  below = wave_sum(below);
-  own = wave_sum(own);
-  if (lane == 0) {
-    s_below[wave] = below;
-    s_own[wave] = own;
-  }
-  __syncthreads();
-  int first = 0, before = 0;
+  int below = 0;
+  uint64_t mask = 0;                         // of step `lane` of the run
+  auto scan = [&](int run) {
+    uint32_t lo = 0, hi = 0;
+    const int last = min(steps, 64 * run + 64);
+    const ID* ids = static_cast<const ID*>(p.ids);
+    for (int i0 = 64 * run; i0 < last; i0 += STEPS) {
+      const int s0 = begin + i0 * 64;
+      ID v[STEPS];
+      uint32_t x[STEPS];
+      if (i0 + STEPS <= last && s0 + STEPS * 64 <= S) {
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    first += s_below[w];
-    before += w < wave ? s_own[w] : 0;
+        for (int j = 0; j < STEPS; ++j) v[j] = ids[s0 + lane + j * 64];
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) x[j] = expert_of(v[j], E);
+      } else {                               // past the wave's steps or the last slot: E + 1, no block's
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) v[j] = ids[min(s0 + lane + j * 64, S - 1)];
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j)
+          x[j] = i0 + j < last && s0 + lane + j * 64 < S ? expert_of(v[j], E) : E + 1;
+      }
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        below += __popcll(__ballot(x[j] < e));
+        const uint64_t own = __ballot(x[j] == e);
+        const bool keep = lane == ((i0 + j) & 63);
+        lo = keep ? static_cast<uint32_t>(own) : lo;
+        hi = keep ? static_cast<uint32_t>(own >> 32) : hi;
+      }
+    }
+    mask = (static_cast<uint64_t>(hi) << 32) | lo;
+  };
+  int own = 0;                               // of this lane's masks
+  for (int run = 0; run < runs; ++run) {
+    scan(run);
+    own += __popcll(mask);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) own += __shfl_xor(own, o);
+  int first = below, at = below;
+  if constexpr (WAVES > 1) {
+    if (lane == 0) {
+      s_below[wave] = below;
+      s_own[wave] = own;
+    }
+    __syncthreads();
+    first = at = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      first += s_below[w];
+      at += w < wave ? s_own[w] : 0;
+    }
+    at += first;
   }
   if (threadIdx.x == 0) p.offsets[e] = first;
 
-  int at = first + before;
-  for (int s0 = begin; s0 < end; s0 += 64) {
-    const int s = s0 + lane;
-    const bool hit = s < end && id_at(s) == e;
-    const uint64_t hits = __ballot(hit);
-    if (hit) {
-      const int to = at + __popcll(hits & ((uint64_t{1} << lane) - 1));
-      p.rows[to] = s / p.topk;
-      if (p.position) p.position[s] = e < p.E ? to : -1;
-    }
-    at += __popcll(hits);
-  }
-}
-
-hipError_t launch_group_rows(const GroupRowsParams& p, int id_bytes, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.E + 1));
-  if (p.S <= 1024) {
-    if (id_bytes == 8) group_rows_kernel<int64_t, 1><<<grid, 64, 0, stream>>>(p);
-    else group_rows_kernel<int32_t, 1><<<grid, 64, 0, stream>>>(p);
-  } else {
-    if (id_bytes == 8) group_rows_kernel<int64_t, 16><<<grid, 1024, 0, stream>>>(p);
-    else group_rows_kernel<int32_t, 16><<<grid, 1024, 0, stream>>>(p);
-  }
-  return hipGetLastError();
-}
-
-// A block has a token's row, or a run of it: each thread PIECE columns at a
-// time (16 bytes of them where rows are whole 16-byte pieces, one element
-// otherwise).  Bound by the bytes of the experts' rows.
-constexpr int kCombineThreads = 256;
-
-template <int ACT, bool WIDE>
-__global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(CombineParams p, int runs) {
-  constexpr int PIECE = WIDE ? 8 : 1;
-  typedef typename Act<ACT>::bits_t T;
-  const int64_t t = blockIdx.x / static_cast<unsigned>(runs);
-  const int run = static_cast<int>(blockIdx.x % static_cast<unsigned>(runs));
-  const int n = (run * kCombineThreads + static_cast<int>(threadIdx.x)) * PIECE;
-  if (n >= p.N) return;
-  const T* y = static_cast<const T*>(p.y);
-  float part[4][PIECE] = {};
-  auto add = [&](int j, float (&sum)[PIECE]) {
-    const int64_t at = p.position[t * p.topk + j];
-    const float w = p.weights[t * p.topk + j];
-    if (at < 0) return;
-    float v[PIECE];
-    if (at >= p.R) {
+  for (int run = 0; run < runs; ++run) {
+    if (runs > 1) scan(run);
+    const int mine = __popcll(mask);
+    int upto = mine;                         // inclusive prefix sum over the lanes
 #pragma unroll
-      for (int i = 0; i < PIECE; ++i) v[i] = __builtin_nanf("");
-    } else if constexpr (WIDE) {
-      load8<ACT>(y + at * p.N, n / 8, v);
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
+    }
+    int to = at + upto - mine;
+    at += __builtin_amdgcn_readlane(upto, 63);
+    const int slot = begin + (64 * run + lane) * 64;
+    for (; mask != 0; mask &= mask - 1) {
+      const int s = slot + __builtin_ctzll(mask);
+      p.rows[to] = static_cast<int>((static_cast<uint64_t>(s) * p.topk_mul) >> p.topk_shift);   // s / topk
+      if (p.position) p.position[s] = e < E ? to : -1;
+      ++to;
+    }
+  }
+}
+
+// The same for many slots in two launches, a chunk of 1024 STEPS slots a block:
+// each chunk's count of every expert, into the workspace, and then each chunk's
+// places, from the counts of all chunks before it.  Taken above 16384 slots (us,
+// one launch / two: 4096 slots, 64 experts 3.4 / 5.9; 16384, 256 experts 6.9 /
+// 8.2, 8 experts 6.2 / 5.9; 65536, 64 experts 8.5 / 7.0, 256 experts 14.1 / 9.1;
+// 524288, 256 experts 141 / 17; two empty launches are 4.9).  Chunks of 1024
+// slots up to 128 of them, of 4096 beyond (65536 slots 9.1 against 11.0 in
+// chunks of 2048, 524288 slots 29 against 17.5): what a block adds up of the
+// others' counts grows with their number.
+constexpr int kChunkWaves = 16;
+
+template <class ID>
+__device__ __forceinline__ uint32_t chunk_id(const GroupRowsParams& p, int64_t s) {
+  const uint32_t E = static_cast<uint32_t>(p.E);
+  return s < p.S ? expert_of(static_cast<const ID*>(p.ids)[s], E) : E + 1;
+}
+
+template <class ID, int STEPS>
+__global__ __launch_bounds__(64 * kChunkWaves) void group_count_kernel(GroupRowsParams p) {
+  extern __shared__ int s_count[];           // E + 2: the experts, none, past the last slot
+  for (int e = threadIdx.x; e < p.E + 2; e += blockDim.x) s_count[e] = 0;
+  __syncthreads();
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * (1024 * STEPS);
+  uint32_t x[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID>(p, begin + i * 64 * kChunkWaves + threadIdx.x);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    // (a wave of one id, as where all tokens go one way, would queue at its count)
+    const uint32_t one = __builtin_amdgcn_readfirstlane(x[i]);
+    if (__ballot(x[i] == one) == ~uint64_t{0}) {
+      if ((threadIdx.x & 63) == 0) atomicAdd(&s_count[one], 64);
     } else {
-      v[0] = load_act<ACT>(y + at * p.N, n);
+      atomicAdd(&s_count[x[i]], 1);
     }
-#pragma unroll
-    for (int i = 0; i < PIECE; ++i) sum[i] += w * v[i];
-  };
-  for (int j0 = 0; j0 < p.topk; j0 += 4) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (j0 + q < p.topk) add(j0 + q, part[q]);
   }
-  float sum[PIECE];
+  __syncthreads();
+  int* to = p.counts + static_cast<size_t>(blockIdx.x) * (p.E + 1);
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) to[e] = s_count[e];
+}
+
+template <class ID, int STEPS>
+__global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRowsParams p, int chunks, int bits) {
+  extern __shared__ int s_mem[];
+  const int ids = p.E + 2;
+  int* s_all = s_mem;                        // [ids] an id's slots in all chunks
+  int* s_base = s_mem + ids;                 // [ids] in the chunks before this one, then its first place here
+  int* s_wave = s_mem + 2 * ids;             // [kChunkWaves][ids] its slots by wave, then those of the waves before
+  __shared__ int s_part[kChunkWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t E = static_cast<uint32_t>(p.E);
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * (1024 * STEPS) + wave * (64 * STEPS);
+  uint32_t x[STEPS];
 #pragma unroll
-  for (int i = 0; i < PIECE; ++i) sum[i] = ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i];
-  if (p.residual) {
-    float v[PIECE];
-    const T* r = static_cast<const T*>(p.residual) + t * p.N;
-    if constexpr (WIDE) load8<ACT>(r, n / 8, v);
-    else v[0] = load_act<ACT>(r, n);
-#pragma unroll
-    for (int i = 0; i < PIECE; ++i) sum[i] += v[i];
+  for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID>(p, begin + i * 64 + lane);
+  for (int i = threadIdx.x; i < (2 + kChunkWaves) * ids; i += blockDim.x) s_mem[i] = 0;
+  __syncthreads();
+  for (int e = lane; e <= p.E; e += 64) {    // the waves take the chunks in turn
+    int before = 0, all = 0;
+    const int* from = p.counts + e;
+#pragma unroll 4
+    for (int c = wave; c < chunks; c += kChunkWaves) {
+      const int v = from[static_cast<size_t>(c) * (p.E + 1)];
+      all += v;
+      before += c < static_cast<int>(blockIdx.x) ? v : 0;
+    }
+    if (all != 0) atomicAdd(&s_all[e], all);
+    if (before != 0) atomicAdd(&s_base[e], before);
   }
-  T* out = static_cast<T*>(p.out) + t * p.N;
-  if constexpr (WIDE) store8<ACT>(out, n / 8, sum);
-  else store_act<ACT>(out, n, sum[0]);
+  __syncthreads();
+  int carry = 0;
+  for (int e0 = 0; e0 <= p.E; e0 += 64 * kChunkWaves) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    const int all = e <= p.E ? s_all[e] : 0;
+    int upto = all;                          // inclusive prefix sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (e0 > 0) __syncthreads();             // (s_part's last round is read)
+    if (lane == 63) s_part[wave] = upto;
+    __syncthreads();
+    int less = carry;
+#pragma unroll
+    for (int w = 0; w < kChunkWaves; ++w) {
+      less += w < wave ? s_part[w] : 0;
+      carry += s_part[w];
+    }
+    if (e <= p.E) {
+      const int first = less + upto - all;
+      s_base[e] += first;
+      if (blockIdx.x == 0) p.offsets[e] = first;
+    }
+  }
+
+  // each slot's rank among the wave's slots of its id, step after step
+  int* mine = s_wave + wave * ids;
+  int rank[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    uint64_t same = ~uint64_t{0};            // lanes with this lane's id
+    for (int b = 0; b < bits; ++b) {
+      const bool bit = (x[i] >> b) & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
+    }
+    const int lower = __popcll(same & ((uint64_t{1} << lane) - 1));
+    rank[i] = mine[x[i]] + lower;
+    __builtin_amdgcn_wave_barrier();
+    if (lower == 0) mine[x[i]] = rank[i] + __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kChunkWaves; ++w) {
+      const int v = s_wave[w * ids + e];
+      s_wave[w * ids + e] = sum;
+      sum += v;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    if (x[i] > E) continue;
+    const int64_t s = begin + i * 64 + lane;
+    const int to = s_base[x[i]] + mine[x[i]] + rank[i];
+    p.rows[to] = static_cast<int>((static_cast<uint64_t>(s) * p.topk_mul) >> p.topk_shift);
+    if (p.position) p.position[s] = x[i] < E ? to : -1;
+  }
 }
 
 namespace {
 
+template <class ID, int STEPS>
+void launch_chunks_as(const GroupRowsParams& p, int bits, hipStream_t stream) {
+  const int chunks = static_cast<int>((p.S + 1024 * STEPS - 1) / (1024 * STEPS)), threads = 64 * kChunkWaves;
+  const size_t row = (p.E + 2) * sizeof(int);
+  group_count_kernel<ID, STEPS><<<chunks, threads, row, stream>>>(p);
+  group_place_kernel<ID, STEPS><<<chunks, threads, (kChunkWaves + 2) * row, stream>>>(p, chunks, bits);
+}
+template <class ID>
+void launch_group_as(const GroupRowsParams& p, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.E + 1));
+  if (p.counts) {
+    int bits = 1;
+    while ((1 << bits) < p.E + 2) ++bits;
+    if (group_chunk(p.S) == 1024) launch_chunks_as<ID, 1>(p, bits, stream);
+    else launch_chunks_as<ID, 4>(p, bits, stream);
+  } else if (p.S <= 1024) {
+    group_rows_kernel<ID, 1><<<grid, 64, 0, stream>>>(p);
+  } else if (p.S <= 4096) {
+    group_rows_kernel<ID, 4><<<grid, 256, 0, stream>>>(p);
+  } else {
+    group_rows_kernel<ID, 16><<<grid, 1024, 0, stream>>>(p);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_group_rows(const GroupRowsParams& p, int id_bytes, hipStream_t stream) {
+  if (id_bytes == 8) launch_group_as<int64_t>(p, stream);
+  else launch_group_as<int32_t>(p, stream);
+  return hipGetLastError();
+}
+
+// LX lanes a row, eight columns each (LX < 256: 256 / LX rows a block; wider
+// rows: several blocks).  The rows of eight slots are all asked for before the
+// first is used.
+constexpr int kCombineThreads = 256;
+
+template <int ACT, int LX>
+__global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(CombineParams p, int runs) {
+  typedef typename Act<ACT>::bits_t T;
+  const unsigned block = blockIdx.x / static_cast<unsigned>(runs);
+  const int run = static_cast<int>(blockIdx.x - block * static_cast<unsigned>(runs));
+  int row_of_block = static_cast<int>(threadIdx.x) / LX;
+  if constexpr (LX >= 64) row_of_block = __builtin_amdgcn_readfirstlane(row_of_block);   // positions: scalar loads
+  const int64_t t = static_cast<int64_t>(block) * (kCombineThreads / LX) + row_of_block;
+  const int n = (run * LX + static_cast<int>(threadIdx.x) % LX) * 8, left = p.N - n;
+  if (t >= p.T || left <= 0) return;
+  const T* y = static_cast<const T*>(p.y) + n;
+  const int32_t* position = p.position + t * p.topk;
+  const float* weights = p.weights + t * p.topk;
+  Piece<ACT> residual;
+  if (p.residual) load_piece<ACT>(static_cast<const T*>(p.residual) + t * p.N + n, left, residual);
+
+  float part[4][8] = {};
+  for (int j0 = 0; j0 < p.topk; j0 += 8) {
+    Piece<ACT> v[8];
+    int64_t at[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) at[q] = j0 + q < p.topk ? position[j0 + q] : -1;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (at[q] >= 0 && at[q] < p.R) load_piece<ACT>(y + at[q] * p.N, left, v[q]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (at[q] < 0) continue;
+      const float w = at[q] < p.R ? weights[j0 + q] : __builtin_nanf("");
+      float f[8];
+      piece_to_float<ACT>(v[q], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[q & 3][i] += w * f[i];
+    }
+  }
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i];
+  if (p.residual) {
+    float f[8];
+    piece_to_float<ACT>(residual, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += f[i];
+  }
+  store_piece<ACT>(static_cast<T*>(p.out) + t * p.N + n, left, sum);
+}
+
+namespace {
+
+template <int ACT, int LX>
+void launch_combine_rows(const CombineParams& p, int pieces, hipStream_t stream) {
+  const int runs = (pieces + LX - 1) / LX;
+  const int64_t blocks = (p.T + kCombineThreads / LX - 1) / (kCombineThreads / LX) * runs;
+  moe_combine_kernel<ACT, LX><<<static_cast<unsigned>(blocks), kCombineThreads, 0, stream>>>(p, runs);
+}
 template <int ACT>
-void launch_combine_as(const CombineParams& p, bool wide, hipStream_t stream) {
-  const int per = kCombineThreads * (wide ? 8 : 1);
-  const int runs = (p.N + per - 1) / per;
-  const dim3 grid(static_cast<unsigned>(p.T * runs));
-  if (wide) moe_combine_kernel<ACT, true><<<grid, kCombineThreads, 0, stream>>>(p, runs);
-  else moe_combine_kernel<ACT, false><<<grid, kCombineThreads, 0, stream>>>(p, runs);
+void launch_combine_as(const CombineParams& p, hipStream_t stream) {
+  const int pieces = (p.N + 7) / 8;
+  if (pieces <= 8) launch_combine_rows<ACT, 8>(p, pieces, stream);
+  else if (pieces <= 16) launch_combine_rows<ACT, 16>(p, pieces, stream);
+  else if (pieces <= 32) launch_combine_rows<ACT, 32>(p, pieces, stream);
+  else if (pieces <= 128) launch_combine_rows<ACT, 64>(p, pieces, stream);
+  else launch_combine_rows<ACT, 256>(p, pieces, stream);
 }
 
 }  // namespace
 
 hipError_t launch_moe_combine(const CombineParams& p, int act, hipStream_t stream) {
-  auto whole = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  const bool wide = p.N % 8 == 0 && whole(p.y) && whole(p.residual) && whole(p.out);
   switch (act) {
-    case ACT_F32: launch_combine_as<ACT_F32>(p, wide, stream); break;
-    case ACT_F16: launch_combine_as<ACT_F16>(p, wide, stream); break;
-    default: launch_combine_as<ACT_BF16>(p, wide, stream); break;
+    case ACT_F32: launch_combine_as<ACT_F32>(p, stream); break;
+    case ACT_F16: launch_combine_as<ACT_F16>(p, stream); break;
+    default: launch_combine_as<ACT_BF16>(p, stream); break;
   }
   return hipGetLastError();
 }

@@ -41,7 +41,7 @@ EXPORTED_SYMBOLS = (
     "lowbit_quantize_act_i8", "lowbit_linear_a8", "lowbit_add_rmsnorm_q8", "lowbit_quantize_act_f8",
     "lowbit_quantize_weight_f8", "lowbit_linear_f8", "lowbit_linear_f8_grouped",
     "lowbit_linear_f8_workspace_bytes", "lowbit_moe_route", "lowbit_group_rows", "lowbit_moe_combine",
-    "lowbit_lora", "lowbit_lora_workspace_bytes",
+    "lowbit_group_rows_workspace_bytes", "lowbit_lora", "lowbit_lora_workspace_bytes",
 )
 ABI_VERSION = 3
 # schedule overrides (include/lowbit_tuning.h)
@@ -134,7 +134,9 @@ def load() -> ctypes.CDLL:
     lib.lowbit_moe_route.restype = ci
     lib.lowbit_moe_route.argtypes = [vp, ci, vp, c_i64, c_i64, c_i64, ci, c_i64, c_i64, ci, ci, cf, vp, vp, vp]
     lib.lowbit_group_rows.restype = ci
-    lib.lowbit_group_rows.argtypes = [vp, ci, c_i64, c_i64, c_i64, vp, vp, vp, vp]
+    lib.lowbit_group_rows.argtypes = [vp, ci, c_i64, c_i64, c_i64, vp, vp, vp, vp, c_sz, vp]
+    lib.lowbit_group_rows_workspace_bytes.restype = c_sz
+    lib.lowbit_group_rows_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
     lib.lowbit_moe_combine.restype = ci
     lib.lowbit_moe_combine.argtypes = [vp, vp, vp, vp, vp, ci, c_i64, c_i64, c_i64, c_i64, vp]
     lib.lowbit_lora.restype = ci
@@ -860,6 +862,7 @@ _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 def lowbit_group_rows(ids: torch.Tensor, E: int, rows: Optional[torch.Tensor] = None,
                       offsets: Optional[torch.Tensor] = None, position: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
                       stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """The slots of ids[T, k] (int32 or int64, on the GPU) in the order of their expert, 0..E-1.
 
@@ -886,9 +889,15 @@ def lowbit_group_rows(ids: torch.Tensor, E: int, rows: Optional[torch.Tensor] = 
         position = _made_on((T, k), torch.int32, ids, stream)
     else:
         _expect_tensor(position, "position", (T, k), torch.int32)
-    dev = _placed(ids, rows, offsets, position)
+    if workspace is not None and workspace.dtype is not torch.uint8:
+        raise ValueError("workspace must be uint8")
+    dev = _placed(ids, rows, offsets, position, workspace)
+    if workspace is None and T * k > 16384:      # (fewer slots need none)
+        need = _call_on(dev, "lowbit_group_rows_workspace_bytes", T, k, E)
+        workspace = None if need == 0 else _made_on((need,), torch.uint8, ids, stream)
     st = _call_on(dev, "lowbit_group_rows", _ptr(ids), _ID_BYTES[ids.dtype], T, k, E, _ptr(rows), _ptr(offsets),
-                  _ptr(position), _stream_of(dev, stream))
+                  _ptr(position), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                  _stream_of(dev, stream))
     if st != LOWBIT_OK:
         _check(st, "lowbit_group_rows")
     return rows, offsets, position

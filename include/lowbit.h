@@ -496,9 +496,18 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
  *            written, as 0), 1 <= E <= 2^16.
  *   rows     device, T * topk int32.  Written.
  *   offsets  device, E + 1 int32.  Written.
- *   position device, T * topk int32, or NULL.  Written. */
+ *   position device, T * topk int32, or NULL.  Written.
+ *   workspace/workspace_bytes: device scratch or NULL/0, at least
+ *            lowbit_group_rows_workspace_bytes() to be used; when non-NULL it
+ *            must be 256-byte aligned.  Its contents on entry do not matter;
+ *            calls that may run at the same time must not share one. */
 lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_t topk, int64_t E,
-                                int32_t* rows, int32_t* offsets, int32_t* position, void* stream);
+                                int32_t* rows, int32_t* offsets, int32_t* position, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that lowbit_group_rows can use (0: none).  With less, the
+ * call reads the ids once for each expert. */
+size_t lowbit_group_rows_workspace_bytes(int64_t T, int64_t topk, int64_t E);
 
 /* Each token's weighted sum of its experts' rows:
  *   out[t] = sum over j of weights[t, j] * y[position[t, j]] (+ residual[t])

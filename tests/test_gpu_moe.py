@@ -250,6 +250,24 @@ def test_group_rows_of_many_experts():
     check_group(torch.randint(0, 5000, (700, 2), generator=g), 5000)
 
 
+@pytest.mark.parametrize("T, k, E", [(3, 5, 4), (700, 3, 60), (2049, 8, 256), (5001, 4, 900), (70000, 2, 33)])
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+def test_group_rows_with_and_without_workspace(T, k, E, kind):
+    """Both schedules: the same rows, also where all tokens go one way; the workspace's end kept."""
+    g = torch.Generator().manual_seed(T)
+    for ids in (torch.randint(-1, E + 1, (T, k), generator=g), torch.full((T, k), E // 2),
+                torch.randint(0, 2, (T, k), generator=g) * (E - 1)):
+        ids = ids.to(kind).to(DEV)
+        need = lb.load().lowbit_group_rows_workspace_bytes(T, k, E)
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
+        a = lb.lowbit_group_rows(ids, E)
+        b = lb.lowbit_group_rows(ids, E, workspace=ws[:need] if need else None)
+        c = lb.lowbit_group_rows(ids, E, workspace=ws[:0] if need else None)      # too small: one launch
+        for x, y, z in zip(a, b, c):
+            assert torch.equal(x, y) and torch.equal(x, z)
+        assert (ws[need:] == 255).all()
+
+
 def test_group_rows_none():
     rows, offsets, position = lb.lowbit_group_rows(torch.empty(0, 4, dtype=torch.int32, device=DEV), 7,
                                                    offsets=torch.full((8,), 9, dtype=torch.int32, device=DEV))

@@ -39,12 +39,13 @@ def test_route_validation(lowbit_lib, kw, status):
     (dict(E=(1 << 16) + 1), INVALID), (dict(ids=None), INVALID), (dict(rows=None), INVALID), (dict(off=None), INVALID),
     (dict(ids=A + 2), MISALIGNED), (dict(bytes=8, ids=A + 4), MISALIGNED), (dict(rows=A + 2), MISALIGNED),
     (dict(off=A + 1), MISALIGNED), (dict(pos=A + 2), MISALIGNED), (dict(T=0, off=None), INVALID),
+    (dict(wb=256), WORKSPACE), (dict(ws=A + 64, wb=256), WORKSPACE),
 ])
 def test_group_rows_validation(lowbit_lib, kw, status):
-    a = dict(ids=A, bytes=4, T=4, k=2, E=8, rows=A, off=A, pos=A)
+    a = dict(ids=A, bytes=4, T=4, k=2, E=8, rows=A, off=A, pos=A, ws=None, wb=0)
     a.update(kw)
     assert lowbit_lib.lowbit_group_rows(a["ids"], a["bytes"], a["T"], a["k"], a["E"], a["rows"], a["off"], a["pos"],
-                                        None) == status
+                                        a["ws"], a["wb"], None) == status
     assert lb.lowbit_last_error() != ""
 
 
@@ -157,8 +158,8 @@ def test_lora_refuses(lowbit_lib, kw, match):
 
 
 def test_signatures_are_declared(lowbit_lib):
-    for name, n in (("lowbit_moe_route", 15), ("lowbit_group_rows", 9), ("lowbit_moe_combine", 11), ("lowbit_lora", 18),
-                    ("lowbit_lora_workspace_bytes", 6)):
+    for name, n in (("lowbit_moe_route", 15), ("lowbit_group_rows", 11), ("lowbit_moe_combine", 11), ("lowbit_lora", 18),
+                    ("lowbit_lora_workspace_bytes", 6), ("lowbit_group_rows_workspace_bytes", 3)):
         assert len(getattr(lowbit_lib, name).argtypes) == n
 
 
