@@ -315,11 +315,13 @@ struct LoraParams {
   int64_t M, T;
   int L, N, K;              // K % 16 == 0
   int rank, rank_pad;       // rank % 8 == 0; rounded up to 16
-  int splits, k_split;      // K ranges of the first product, multiples of 32
-  int wide;                 // rows of base and y are whole 16-byte pieces
+  int splits, units_split;  // K ranges of the first product, in units of 128 bytes of a row
 };
 struct LoraPlan {
-  int shrink_mt, expand_mt; // row tiles of 16 in a block: 1 or 4
+  bool fused;               // one launch (rank up to 32), no workspace
+  bool many;                // two launches, of 32 rows a tile in the second (else 16)
+  int shrink_rows;          // rows a tile in the first of two launches: 16, 64 or 128
+  int cols;                 // columns of a block, a multiple of what its waves take at a time
 };
 hipError_t launch_lora(const LoraParams&, const LoraPlan&, int act, hipStream_t);
 

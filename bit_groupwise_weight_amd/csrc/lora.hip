@@ -18,7 +18,7 @@
 // the call is bound by memory.  fp16 pairs are taken of t times a power of two
 // that brings a row's largest |t| to 1 .. 2, so that t may be any fp32 number.
 // fp32 calls use the fp32 matrix instruction throughout.
-#include "f8_common.h"
+#include "pieces.h"
 
 #include <algorithm>
 
@@ -33,6 +33,7 @@ template <int ACT> struct Chunk {      // 16-bit types
     w = *reinterpret_cast<const u32v4_t*>(static_cast<const uint16_t*>(p) + at);
   }
   __device__ __forceinline__ void zero() { w = u32v4_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void keep(bool in) { w = in ? w : u32v4_t{0u, 0u, 0u, 0u}; }
 };
 template <> struct Chunk<ACT_F32> {
   f32x4_t v[2];
@@ -42,6 +43,9 @@ template <> struct Chunk<ACT_F32> {
     v[1] = q[1];
   }
   __device__ __forceinline__ void zero() { v[0] = v[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ __forceinline__ void keep(bool in) {
+    if (!in) zero();
+  }
 };
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -119,272 +123,647 @@ __device__ __forceinline__ int row_of(const LoraParams& p, int t) {
   return r >= 0 && r < p.M ? static_cast<int>(r) : -1;
 }
 
+// Direct global -> LDS loads of 16 bytes a lane, lane l to LDS at m0 + 16 l, and
+// their waits.  Operands go through LDS because in an MFMA's layout neighbouring
+// lanes hold different rows: loaded straight to registers, each lane's 16 bytes
+// are a cache access of their own, four times as many as here (adapters of
+// rank 64 on 8192 rows, 4096 -> 14336: 1.3 TB/s in the first product so).
+__device__ __forceinline__ void dma16(const void* vaddr, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               : : "v"(vaddr), "s"(m0) : "memory", "m0");
+}
+// At most N of this wave's loads and stores still in flight.
+template <int N> __device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// This wave's LDS reads are done (before loads overwrite what they read).
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+__device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
+template <typename T>
+__device__ __forceinline__ uint32_t lds_address(T* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)p));
+}
+
+// What positions past K are read from.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
+// A unit: 128 bytes of each of 16 rows, 2 KiB in LDS from two loads.  Chunk c (16
+// bytes) of row r sits at position c ^ ((r >> 1) & 7) of the row, so that the 16
+// rows of a read at one chunk start in 16 different 4-bank groups.
+constexpr int kUnitBytes = 2048;
+template <int ACT> constexpr int kUnitK = 128 / Act<ACT>::bytes;       // positions
+template <int ACT> constexpr int kUnitSteps = kUnitK<ACT> / 32;        // MFMA steps
+template <int ACT> constexpr int kChunkK = 16 / Act<ACT>::bytes;       // positions of a chunk
+
+// The lane's chunk of a step of a row's unit in LDS.
+template <int ACT>
+__device__ __forceinline__ void read_unit(const uint8_t* unit, int step, Chunk<ACT>& v) {
+  const int c16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4, swz = (c16 >> 1) & 7;
+  const uint8_t* row = unit + c16 * 128;
+  if constexpr (ACT == ACT_F32) {
+    v.v[0] = *reinterpret_cast<const f32x4_t*>(row + 16 * ((2 * g) ^ swz));
+    v.v[1] = *reinterpret_cast<const f32x4_t*>(row + 16 * ((2 * g + 1) ^ swz));
+  } else {
+    v.w = *reinterpret_cast<const u32v4_t*>(row + 16 * ((4 * step + g) ^ swz));
+  }
+}
+
+// acc += A . x^T of a tile of 16 NT ranks (from r0) and 16 positions over the
+// units first, first + WAVES, .. below last of K; ring: the wave's own STAGES
+// stages of 1 + NT units.
+template <int ACT, int NT, int WAVES, int STAGES>
+__device__ __forceinline__ void shrink_tile(const LoraParams& p, const RowTile& rt, int r0, int first, int last,
+                                            uint8_t* ring, f32x4_t (&acc)[NT]) {
+  constexpr int LOADS = 2 * (1 + NT), STAGE = (1 + NT) * kUnitBytes;
+  const int lane = threadIdx.x & 63;
+  // load h of a unit: rows 8 h + lane / 8; the lane fills position lane % 8
+  const uint8_t* from[LOADS];
+  int chunk[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) chunk[h] = (lane & 7) ^ (((8 * h + (lane >> 3)) >> 1) & 7);
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int tile = i / 2, r = 8 * (i & 1) + (lane >> 3);
+    const uint8_t* base;
+    size_t row;
+    if (tile == 0) {                   // (positions past the tile: its last one again; rows that are none: row 0)
+      base = static_cast<const uint8_t*>(p.x);
+      row = static_cast<size_t>(max(row_of(p, min(rt.begin + r, rt.end - 1)), 0));
+    } else {
+      base = static_cast<const uint8_t*>(p.a);
+      row = static_cast<size_t>(rt.adapter) * p.rank + min(r0 + 16 * (tile - 1) + r, p.rank - 1);
+    }
+    from[i] = base + row * p.K * Act<ACT>::bytes + 16 * chunk[i & 1];
+  }
+  const uint32_t to = lds_address(ring);
+  auto load = [&](int unit, int stage) {
+    const uint32_t dst = to + stage * STAGE;
+    const size_t at = static_cast<size_t>(unit) * 128;
+    const bool whole = (unit + 1) * kUnitK<ACT> <= p.K;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      dma16(whole || unit * kUnitK<ACT> + chunk[i & 1] * kChunkK<ACT> < p.K
+                ? from[i] + at : reinterpret_cast<const uint8_t*>(kZeros),
+            dst + i * 1024);
+  };
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int units = last > first ? (last - first + WAVES - 1) / WAVES : 0;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s)
+    if (s < units) load(first + s * WAVES, s);
+  int stage = 0;
+#pragma unroll 1
+  for (int u = 0; u < units; ++u) {
+    const int ahead = units - 1 - u;   // units behind this one: their loads may stay in flight
+    if (ahead >= STAGES - 1) {
+      int next = stage + STAGES - 1;
+      if (next >= STAGES) next -= STAGES;
+      wait_lds();
+      load(first + (u + STAGES - 1) * WAVES, next);
+      wait_loads<LOADS * (STAGES - 1)>();
+    } else if (STAGES > 3 && ahead == 2) {
+      wait_loads<LOADS * (STAGES > 3 ? 2 : 0)>();
+    } else if (STAGES > 2 && ahead == 1) {
+      wait_loads<LOADS * (STAGES > 2 ? 1 : 0)>();
+    } else {
+      wait_loads<0>();
+    }
+    const uint8_t* at = ring + stage * STAGE;
+#pragma unroll
+    for (int s = 0; s < kUnitSteps<ACT>; ++s) {
+      Chunk<ACT> x, a[NT];
+      read_unit<ACT>(at, s, x);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) read_unit<ACT>(at + (1 + i) * kUnitBytes, s, a[i]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] = mfma<ACT>(a[i], x, acc[i]);
+    }
+    if (++stage == STAGES) stage = 0;
+  }
+}
+
 }  // namespace
 
-constexpr int kLoraThreads = 256, kLoraWaves = 4;
-
-// t of a tile of 16 MT positions and 16 NT ranks, over the K range of
-// blockIdx.y: the waves take its steps of 32 in turn, their sums meet in LDS.
-template <int ACT, int MT, int NT>
-__global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraParams p) {
-  __shared__ f32x4_t s_sum[kLoraWaves][NT * MT][64];
+// t of a tile of 16 positions and 16 NT ranks, over the units of K of blockIdx.y:
+// the waves share them, their sums meet in LDS.
+template <int ACT, int NT, int WAVES, int STAGES>
+__global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(LoraParams p) {
+  constexpr int RING = STAGES * (1 + NT) * kUnitBytes;
+  static_assert(RING >= NT * 1024, "the sums fit the rings");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[WAVES][RING];
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const RowTile rt = find_rows<16 * MT>(p, static_cast<int>(blockIdx.x));
+  const RowTile rt = find_rows<16>(p, static_cast<int>(blockIdx.x));
   if (!rt.found || rt.adapter < 0 || rt.adapter >= p.L) return;
   const int r0 = static_cast<int>(blockIdx.z) * 16 * NT;
-  const int k_begin = static_cast<int>(blockIdx.y) * p.k_split, k_end = min(k_begin + p.k_split, p.K);
-
-  size_t x_at[MT], a_at[NT];
+  const int all = (p.K + kUnitK<ACT> - 1) / kUnitK<ACT>;
+  const int first = static_cast<int>(blockIdx.y) * p.units_split, last = min(first + p.units_split, all);
+  f32x4_t acc[NT];
+  shrink_tile<ACT, NT, WAVES, STAGES>(p, rt, r0, first + wave, last, s_ring[wave], acc);
+  // (a wave's own ring has no loads in flight and no reads that are not done)
+  f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_ring[wave]);
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int row = row_of(p, min(rt.begin + 16 * j + c16, rt.end - 1));
-    x_at[j] = static_cast<size_t>(max(row, 0)) * p.K;
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-    a_at[i] = (static_cast<size_t>(rt.adapter) * p.rank + min(r0 + 16 * i + c16, p.rank - 1)) * p.K;
-
-  f32x4_t acc[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-  for (int k0 = k_begin + 32 * wave; k0 < k_end; k0 += 32 * kLoraWaves) {
-    const int k = k0 + 8 * g;
-    Chunk<ACT> x[MT], a[NT];
-    if (k < p.K) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j) x[j].load(p.x, x_at[j] + k);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) a[i].load(p.a, a_at[i] + k);
-    } else {                           // (K is a multiple of 16: the last step may be half)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) x[j].zero();
-#pragma unroll
-      for (int i = 0; i < NT; ++i) a[i].zero();
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = mfma<ACT>(a[i], x[j], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) s_sum[wave][i * MT + j][lane] = acc[i][j];
+  for (int i = 0; i < NT; ++i) sum[i * 64 + lane] = acc[i];
   __syncthreads();
   float* plane = p.t + static_cast<size_t>(blockIdx.y) * p.T * p.rank_pad;
-  for (int q = wave; q < NT * MT; q += kLoraWaves) {
-    const int i = q / MT, j = q % MT;
-    f32x4_t v = s_sum[0][q][lane];
+  for (int i = wave; i < NT; i += WAVES) {
+    f32x4_t v = reinterpret_cast<const f32x4_t*>(s_ring[0])[i * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < kLoraWaves; ++w) v += s_sum[w][q][lane];
-    const int t = rt.begin + 16 * j + c16, r = r0 + 16 * i + 4 * g;
+    for (int w = 1; w < WAVES; ++w) v += reinterpret_cast<const f32x4_t*>(s_ring[w])[i * 64 + lane];
+    const int t = rt.begin + c16, r = r0 + 16 * i + 4 * g;
     if (t < rt.end && r < p.rank_pad)
       *reinterpret_cast<f32x4_t*>(plane + static_cast<size_t>(t) * p.rank_pad + r) = v;
   }
 }
 
-namespace {
+// The same for many rows: each of the WAVES waves has 16 positions of its own
+// and all share A's units, through a ring of STAGES stages.  A unit has one
+// barrier, before which a wave waits for its own loads of it; the loads of later
+// units go out behind it, into the stage that the unit before has left.
+template <int ACT, int NT, int WAVES, int STAGES>
+__global__ __launch_bounds__(64 * WAVES) void lora_shrink_rows_kernel(LoraParams p) {
+  constexpr int A_LOADS = 2 * NT >= WAVES ? 2 * NT / WAVES : 1;   // of a wave (NT 1: two waves each the same)
+  constexpr int LOADS = A_LOADS + 2, STAGE = (NT + WAVES) * kUnitBytes;
+  static_assert(2 * NT % WAVES == 0 || WAVES % (2 * NT) == 0, "whole loads");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[STAGES][STAGE];
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowTile rt = find_rows<16 * WAVES>(p, static_cast<int>(blockIdx.x));
+  if (!rt.found || rt.adapter < 0 || rt.adapter >= p.L) return;
+  const int r0 = static_cast<int>(blockIdx.z) * 16 * NT;
+  const int all = (p.K + kUnitK<ACT> - 1) / kUnitK<ACT>;
+  const int first = static_cast<int>(blockIdx.y) * p.units_split, units = min(p.units_split, all - first);
+  const int mine = rt.begin + 16 * wave;               // the wave's first position
 
-// t of a tile's BM rows in LDS, ready for the second product: rows of `pitch`
-// elements, an odd number of 16-byte pieces, so that the 16 rows of a read
-// start in different banks; 16-bit types have the hi halves of all rows and
-// then the lo halves.
-__device__ __forceinline__ int t_lanes(int rank) {   // lanes of a row, 8 ranks each
-  int lanes = 4;
-  while (lanes * 8 < rank) lanes *= 2;
-  return lanes;
-}
-__device__ __forceinline__ int t_pitch(int rank) { return t_lanes(rank) * 8 + 8; }
-
-// Eight values of t for row r from rank k on; the `lanes` lanes of a row call it
-// together.
-template <int ACT, int BM>
-__device__ __forceinline__ void put_t(void* lds, float* unscale, int pitch, int r, int k, float (&v)[8],
-                                      int lanes) {
-  if constexpr (ACT == ACT_F32) {
-    f32x4_t* to = reinterpret_cast<f32x4_t*>(static_cast<float*>(lds) + r * pitch + k);
-    to[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-    to[1] = f32x4_t{v[4], v[5], v[6], v[7]};
-  } else {
-    if constexpr (ACT == ACT_F16) {
-      uint32_t top = 0;                // bits of the row's largest magnitude
+  const uint8_t* from[LOADS];
+  int chunk[LOADS], to[LOADS];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-      for (int o = 1; o < lanes; o <<= 1)
-        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o)));
-      // 2^-e with e the exponent of the largest, within fp32's normal powers
-      const int e = min(max(static_cast<int>(top >> 23), 1), 253);
-      const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-      if (k == 0) unscale[r] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= scale;
+  for (int i = 0; i < LOADS; ++i) {
+    // loads 0 and 1: the wave's x; then load `half` of A's 2 NT
+    const int half = i < 2 ? i : (wave * A_LOADS + i - 2) % (2 * NT);
+    const int r = 8 * (half & 1) + (lane >> 3);        // of the unit
+    const uint8_t* base;
+    size_t row;
+    if (i < 2) {                       // (positions past the tile: its last one again; rows that are none: row 0)
+      base = static_cast<const uint8_t*>(p.x);
+      row = static_cast<size_t>(max(row_of(p, min(mine + r, rt.end - 1)), 0));
+      to[i] = (NT + wave) * kUnitBytes + 1024 * i;
+    } else {
+      base = static_cast<const uint8_t*>(p.a);
+      row = static_cast<size_t>(rt.adapter) * p.rank + min(r0 + 16 * (half / 2) + r, p.rank - 1);
+      to[i] = 1024 * half;
     }
-    uint32_t hi[4], lo[4];
+    chunk[i] = (lane & 7) ^ ((r >> 1) & 7);
+    from[i] = base + row * p.K * Act<ACT>::bytes + 16 * chunk[i];
+  }
+  const uint32_t ring = lds_address(&s_ring[0][0]);
+  auto load = [&](int unit, int stage) {
+    const uint32_t dst = ring + stage * STAGE;
+    const size_t at = static_cast<size_t>(unit) * 128;
+    const bool whole = (unit + 1) * kUnitK<ACT> <= p.K;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hi[i] = pack2<ACT>(v[2 * i], v[2 * i + 1]);
-      const float h0 = act_bits_to_float<ACT>(hi[i] & 0xffffu), h1 = act_bits_to_float<ACT>(hi[i] >> 16);
-      // (an infinity has no rest)
-      lo[i] = pack2<ACT>(fabsf(h0) <= 3.402823466e38f ? v[2 * i] - h0 : 0.0f,
-                         fabsf(h1) <= 3.402823466e38f ? v[2 * i + 1] - h1 : 0.0f);
+    for (int i = 0; i < LOADS; ++i)
+      dma16(whole || unit * kUnitK<ACT> + chunk[i] * kChunkK<ACT> < p.K ? from[i] + at
+                                                                      : reinterpret_cast<const uint8_t*>(kZeros),
+            dst + to[i]);
+  };
+  f32x4_t acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s)
+    if (s < units) load(first + s, s);
+  int stage = 0;
+#pragma unroll 1
+  for (int u = 0; u < units; ++u) {
+    const int ahead = units - 1 - u;   // units behind this one: their loads may stay in flight
+    if (ahead >= STAGES - 2) wait_loads<LOADS * (STAGES - 2)>();
+    else if (STAGES > 3 && ahead == 1) wait_loads<LOADS>();
+    else wait_loads<0>();
+    barrier();
+    int next = stage + STAGES - 1;
+    if (next >= STAGES) next -= STAGES;
+    if (ahead >= STAGES - 1) load(first + u + STAGES - 1, next);
+    const uint8_t* at = s_ring[stage];
+#pragma unroll
+    for (int s = 0; s < kUnitSteps<ACT>; ++s) {
+      Chunk<ACT> x, a[NT];
+      read_unit<ACT>(at + (NT + wave) * kUnitBytes, s, x);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) read_unit<ACT>(at + i * kUnitBytes, s, a[i]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] = mfma<ACT>(a[i], x, acc[i]);
     }
-    uint16_t* to = static_cast<uint16_t*>(lds) + r * pitch + k;
-    *reinterpret_cast<u32v4_t*>(to) = u32v4_t{hi[0], hi[1], hi[2], hi[3]};
-    *reinterpret_cast<u32v4_t*>(to + BM * pitch) = u32v4_t{lo[0], lo[1], lo[2], lo[3]};
+    if (++stage == STAGES) stage = 0;
+  }
+  float* plane = p.t + static_cast<size_t>(blockIdx.y) * p.T * p.rank_pad;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int t = mine + c16, r = r0 + 16 * i + 4 * g;
+    if (t < rt.end && r < p.rank_pad)
+      *reinterpret_cast<f32x4_t*>(plane + static_cast<size_t>(t) * p.rank_pad + r) = acc[i];
   }
 }
 
-// base (or 0) + delta for 8 consecutive columns of a row.
-template <int ACT>
-__device__ __forceinline__ void add_row8(const LoraParams& p, int row, int n, const float (&d)[8], bool wide) {
+namespace {
+
+// t of a tile's BM rows in LDS, ready for the second product: rows of RANKS + 8
+// elements, an odd number of 16-byte pieces, so that the 16 rows of a read
+// start in different banks; 16-bit types have the hi halves of all rows and
+// then the lo halves.  from(r, k, v) gives eight ranks of row r.
+template <int ACT, int BM, int RANKS> struct TileT {
   typedef typename Act<ACT>::bits_t T;
-  const size_t at = static_cast<size_t>(row) * p.N + n;
-  const T* base = static_cast<const T*>(p.base);
-  T* y = static_cast<T*>(p.y);
-  if (wide) {                          // (N % 8 == 0: all eight are columns)
+  static constexpr int PITCH = RANKS + 8, HALVES = ACT == ACT_F32 ? 1 : 2;
+  T v[HALVES][BM][PITCH];
+  float unscale[BM];                   // fp16
+};
+template <int ACT, int BM, int RANKS, int THREADS, class From>
+__device__ __forceinline__ void prepare_t(const LoraParams& p, int rows, float scale, TileT<ACT, BM, RANKS>& t,
+                                          From from) {
+  constexpr int LANES = RANKS / 8;     // of a row, a power of two
+  const int k = threadIdx.x % LANES * 8;
+  for (int r = threadIdx.x / LANES; r < BM; r += THREADS / LANES) {
     float v[8] = {};
-    if (base) load8<ACT>(base + at, 0, v);
+    if (k < p.rank && r < rows) {
+      from(r, k, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += d[i];
-    store8<ACT>(y + at, 0, v);
-  } else {
+      for (int i = 0; i < 8; ++i) v[i] *= scale;
+    }
+    if constexpr (ACT == ACT_F32) {
+      f32x4_t* to = reinterpret_cast<f32x4_t*>(&t.v[0][r][k]);
+      to[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+      to[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    } else {
+      if constexpr (ACT == ACT_F16) {
+        uint32_t top = 0;              // bits of the row's largest magnitude
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (n + i < p.N) store_act<ACT>(y, at + i, (base ? load_act<ACT>(base, at + i) : 0.0f) + d[i]);
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+          top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o)));
+        // 2^-e with e the exponent of the largest, within fp32's normal powers
+        const int e = min(max(static_cast<int>(top >> 23), 1), 253);
+        const float by = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        if (k == 0) t.unscale[r] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= by;
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = pack2<ACT>(v[2 * i], v[2 * i + 1]);
+        const float h0 = act_bits_to_float<ACT>(hi[i] & 0xffffu), h1 = act_bits_to_float<ACT>(hi[i] >> 16);
+        // (an infinity has no rest)
+        lo[i] = pack2<ACT>(fabsf(h0) <= 3.402823466e38f ? v[2 * i] - h0 : 0.0f,
+                           fabsf(h1) <= 3.402823466e38f ? v[2 * i + 1] - h1 : 0.0f);
+      }
+      *reinterpret_cast<u32v4_t*>(&t.v[0][r][k]) = u32v4_t{hi[0], hi[1], hi[2], hi[3]};
+      *reinterpret_cast<u32v4_t*>(&t.v[1][r][k]) = u32v4_t{lo[0], lo[1], lo[2], lo[3]};
+    }
+  }
+}
+
+// B of consecutive columns in LDS, the ranks of pass `pass` (128 bytes of each
+// column, or what is left of the rank): chunk c of column n, of u chunks, is
+// logical chunk n u + c, and logical chunk q sits at q ^ turn(q), within its 16:
+// the 16 columns n, n + 8, ... of a read then start in different banks (for odd
+// u: nearly).
+template <int ACT> constexpr int kPassRanks = 128 / Act<ACT>::bytes;
+struct BLayout {
+  int u, inv, shift;
+  __device__ __forceinline__ int turn(int q) const { return (q >> shift) & 15; }
+};
+template <int ACT> __device__ __forceinline__ BLayout b_layout(const LoraParams& p, int pass) {
+  BLayout l;
+  l.u = min(kPassRanks<ACT>, p.rank - pass * kPassRanks<ACT>) / kChunkK<ACT>;
+  l.inv = (65536 + l.u - 1) / l.u;     // q / u == (q * inv) >> 16 for q < 2^13, u <= 8
+  l.shift = 4 + ((l.u & 7) == 0 ? 2 : (l.u & 3) == 0 ? 1 : 0);
+  return l;
+}
+// The share of wave `wave` of WAVES in loading COLS columns from n0 on.
+template <int ACT, int COLS, int WAVES>
+__device__ __forceinline__ void load_b(const LoraParams& p, int adapter, int n0, int pass, const BLayout& l,
+                                       uint32_t to, int wave) {
+  const uint8_t* b = static_cast<const uint8_t*>(p.b);
+  const size_t col0 = static_cast<size_t>(adapter) * p.N;
+  for (int i = wave; i < COLS * l.u / 64; i += WAVES) {
+    const int at = 64 * i + static_cast<int>(threadIdx.x & 63), q = at ^ l.turn(at);
+    const int n = (q * l.inv) >> 16, c = q - n * l.u;
+    dma16(b + ((col0 + min(n0 + n, p.N - 1)) * p.rank + pass * kPassRanks<ACT> + c * kChunkK<ACT>) * Act<ACT>::bytes,
+          to + 1024 * i);
+  }
+}
+
+// acc += t B^T for 16 rows (from row m0 of the tile on) and 128 columns, ranks of
+// one pass: MFMA tile j has the columns 8 c + j, c = 0 .. 15 (from column n0 of
+// lds on), so that a lane ends with 8 consecutive columns of four rows, and 16
+// lanes with 256 bytes of a row.
+template <int ACT, int BM, int RANKS>
+__device__ __forceinline__ void multiply_pass(const LoraParams& p, const TileT<ACT, BM, RANKS>& t, int m0,
+                                              const uint8_t* lds, const BLayout& l, int n0, int pass,
+                                              f32x4_t (&acc)[8]) {
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const bool both = ACT != ACT_F32 && p.rank_pad == 16;       // hi and lo in one step
+  auto read_b = [&](int j, int chunk, bool in) {
+    const int q = (n0 + 8 * c16 + j) * l.u + (in ? chunk : 0);
+    return *reinterpret_cast<const u32v4_t*>(lds + 16 * (q ^ l.turn(q)));
+  };
+  const int left = p.rank_pad - pass * kPassRanks<ACT>;
+#pragma unroll
+  for (int s = 0; s < kUnitSteps<ACT>; ++s) {
+    if (32 * s >= left) break;
+    const int k = both ? 8 * (g & 1) : 32 * s + 8 * g;        // of the pass
+    const bool in = pass * kPassRanks<ACT> + k < p.rank;      // (B past the rank: zeros)
+    Chunk<ACT> b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (ACT == ACT_F32) {
+        b[j].v[0] = __builtin_bit_cast(f32x4_t, read_b(j, 2 * g, in));
+        b[j].v[1] = __builtin_bit_cast(f32x4_t, read_b(j, 2 * g + 1, in));
+      } else {
+        b[j].w = read_b(j, k / 8, in);
+      }
+      b[j].keep(in);
+    }
+    const int kt = pass * kPassRanks<ACT> + k;
+    const int r = m0 + c16;
+    Chunk<ACT> v;
+    v.load(ACT != ACT_F32 && both && g >= 2 ? &t.v[t.HALVES - 1][r][kt] : &t.v[0][r][kt], 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = mfma<ACT>(v, b[j], acc[j]);
+    if constexpr (ACT != ACT_F32) {
+      if (!both) {
+        v.load(&t.v[1][r][kt], 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = mfma<ACT>(v, b[j], acc[j]);
+      }
+    }
+  }
+}
+
+// The rows and columns that a lane ends with.
+template <int ACT> struct Outputs {
+  typedef typename Act<ACT>::bits_t T;
+  static constexpr int LOADS = 4 * (ACT == ACT_F32 ? 2 : 1);   // or stores, of a full step
+  int row[4];             // -1: none
+  float unscale[4];       // fp16
+  Piece<ACT> old[4];
+
+  // rows 4 g + i of the wave's 16, from row m0 of the tile on
+  __device__ __forceinline__ void set_rows(const int* rows, int m0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row[i] = rows[m0 + 4 * ((threadIdx.x & 63) >> 4) + i];
+  }
+  template <int BM, int RANKS> __device__ __forceinline__ void set_factors(const TileT<ACT, BM, RANKS>& t, int m0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      unscale[i] = ACT == ACT_F16 ? t.unscale[m0 + 4 * ((threadIdx.x & 63) >> 4) + i] : 1.0f;
+  }
+  __device__ __forceinline__ bool all_rows() const {
+    return __ballot(row[0] < 0 || row[1] < 0 || row[2] < 0 || row[3] < 0) == 0;
+  }
+  // FULL: every row and column of the step is there
+  template <bool FULL> __device__ __forceinline__ void load(const LoraParams& p, int n0) {
+    if (p.base == nullptr) return;
+    const int n = n0 + 8 * static_cast<int>(threadIdx.x & 15);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (FULL || (row[i] >= 0 && n < p.N))
+        load_piece<ACT>(static_cast<const T*>(p.base) + static_cast<size_t>(row[i]) * p.N + n, FULL ? 8 : p.N - n,
+                        old[i]);
+  }
+  template <bool FULL> __device__ __forceinline__ void store(const LoraParams& p, int n0, const f32x4_t (&acc)[8]) {
+    const int n = n0 + 8 * static_cast<int>(threadIdx.x & 15);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!FULL && (row[i] < 0 || n >= p.N)) continue;
+      float v[8] = {};
+      if (p.base) piece_to_float<ACT>(old[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += acc[j][i] * unscale[i];
+      store_piece<ACT>(static_cast<T*>(p.y) + static_cast<size_t>(row[i]) * p.N + n, FULL ? 8 : p.N - n, v);
+    }
+  }
+};
+
+__device__ __forceinline__ void clear(f32x4_t (&acc)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// Rows without an adapter: base, or 0, to another array.
+template <int ACT>
+__device__ __forceinline__ void copy_columns(const LoraParams& p, Outputs<ACT>& o, int n0, int n_end, int stride) {
+  f32x4_t acc[8];
+  clear(acc);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.unscale[i] = 0.0f;
+  for (; n0 < n_end; n0 += stride) {
+    o.template load<false>(p, n0);
+    o.template store<false>(p, n0, acc);
   }
 }
 
 }  // namespace
 
-// y of a tile of 16 MT positions and 256 columns, 64 a wave.
-template <int ACT, int MT>
-__global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraParams p) {
-  constexpr int BM = 16 * MT;
-  extern __shared__ __attribute__((aligned(16))) uint8_t s_t[];
+// y of a tile of BM = 16 WM positions: WN waves next to each other take 128
+// columns each, and the block `cols` columns, 128 WN at a time, whose B the
+// waves load together.  A step's B is asked for behind the products of the step
+// before and ahead of that one's stores, its base behind them.
+template <int ACT, int WM, int WN, int RANKS>
+__global__ __launch_bounds__(64 * WM * WN) void lora_expand_kernel(LoraParams p, int cols) {
+  constexpr int BM = 16 * WM, WAVES = WM * WN, COLS = 128 * WN;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_b[COLS * 128];
+  __shared__ __attribute__((aligned(16))) TileT<ACT, BM, RANKS> s_t;
   __shared__ int s_row[BM];
-  __shared__ float s_unscale[BM];
-  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const RowTile rt = find_rows<BM>(p, static_cast<int>(blockIdx.x));
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
+  const unsigned across = static_cast<unsigned>((p.N + cols - 1) / cols), tile = blockIdx.x / across;
+  const RowTile rt = find_rows<BM>(p, static_cast<int>(tile));
   if (!rt.found) return;
   const bool bare = rt.adapter < 0 || rt.adapter >= p.L;
   if (bare && p.base == p.y) return;
-  const int n0 = (static_cast<int>(blockIdx.y) * kLoraWaves + wave) * 64;
-  const bool wide = p.wide;
-
-  for (int r = threadIdx.x; r < BM; r += kLoraThreads)
-    s_row[r] = rt.begin + r < rt.end ? row_of(p, rt.begin + r) : -1;
-  const int steps = (p.rank_pad + 31) / 32, pitch = t_pitch(p.rank);
+  const int first = static_cast<int>(blockIdx.x - tile * across) * cols, last = min(first + cols, p.N);
+  const int passes = (p.rank + kPassRanks<ACT> - 1) / kPassRanks<ACT>;
+  const uint32_t b_at = lds_address(s_b);
+  BLayout l = b_layout<ACT>(p, 0);
+  if (!bare) load_b<ACT, COLS, WAVES>(p, rt.adapter, first, 0, l, b_at, wave);
+  for (int r = threadIdx.x; r < BM; r += 64 * WAVES) s_row[r] = rt.begin + r < rt.end ? row_of(p, rt.begin + r) : -1;
   if (!bare) {
-    const float scale = p.scales ? p.scales[rt.adapter] : 1.0f;
-    const int lanes = t_lanes(p.rank);
-    for (int r = threadIdx.x / lanes; r < BM; r += kLoraThreads / lanes) {
-      const int k = threadIdx.x % lanes * 8;
-      float v[8] = {};
-      if (k < p.rank && rt.begin + r < rt.end) {
-        for (int s = 0; s < p.splits; ++s) {
-          const f32x4_t* from = reinterpret_cast<const f32x4_t*>(
-              p.t + (static_cast<size_t>(s) * p.T + rt.begin + r) * p.rank_pad + k);
-          const f32x4_t a = from[0], b = from[1];
+    prepare_t<ACT, BM, RANKS, 64 * WAVES>(
+        p, rt.end - rt.begin, p.scales ? p.scales[rt.adapter] : 1.0f, s_t, [&](int r, int k, float (&v)[8]) {
+          // (four planes asked for at once)
+          const float* from = p.t + static_cast<size_t>(rt.begin + r) * p.rank_pad + k;
+          const size_t plane = static_cast<size_t>(p.T) * p.rank_pad;
+          for (int s0 = 0; s0 < p.splits; s0 += 4) {
+            f32x4_t a[4], b[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] += a[i];
-            v[4 + i] += b[i];
-          }
-        }
+            for (int q = 0; q < 4; ++q) {
+              const f32x4_t* at = reinterpret_cast<const f32x4_t*>(from + min(s0 + q, p.splits - 1) * plane);
+              a[q] = at[0];
+              b[q] = at[1];
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= scale;
-      }
-      put_t<ACT, BM>(s_t, s_unscale, pitch, r, k, v, lanes);
-    }
-  }
-  __syncthreads();
-
-  // two MFMA tiles make 32 columns: row 4 g + i of tile j is column 8 g + 4 j + i,
-  // so that a lane ends with 8 consecutive ones
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const int n = n0 + 32 * h;
-    if (n >= p.N) break;
-    f32x4_t acc[2][MT];
+            for (int q = 0; q < 4; ++q) {
+              if (s0 + q >= p.splits) break;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[j][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (!bare) {
-      size_t b_at[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        b_at[j] = (static_cast<size_t>(rt.adapter) * p.N + min(n + 8 * (c16 >> 2) + 4 * j + (c16 & 3), p.N - 1)) *
-                  p.rank;
-      const bool both = ACT != ACT_F32 && p.rank_pad == 16;   // hi and lo in one step
-#pragma unroll 1
-      for (int s = 0; s < steps; ++s) {
-        const int k = both ? 8 * (g & 1) : 32 * s + 8 * g;
-        Chunk<ACT> b[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (k < p.rank) b[j].load(p.b, b_at[j] + k);
-          else b[j].zero();
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int t_at = (16 * m + c16) * pitch + k, t_lo = BM * pitch;
-          Chunk<ACT> t;
-          t.load(s_t, t_at + (both && g >= 2 ? t_lo : 0));
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[j][m] = mfma<ACT>(b[j], t, acc[j][m]);
-          if constexpr (ACT != ACT_F32) {
-            if (!both) {
-              t.load(s_t, t_at + t_lo);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) acc[j][m] = mfma<ACT>(b[j], t, acc[j][m]);
+              for (int i = 0; i < 4; ++i) {
+                v[i] += a[q][i];
+                v[4 + i] += b[q][i];
+              }
             }
           }
-        }
+        });
+  }
+  __syncthreads();
+  Outputs<ACT> o;
+  o.set_rows(s_row, 16 * wm);
+  if (bare) {
+    copy_columns<ACT>(p, o, first + 128 * wn, last, COLS);
+    return;
+  }
+  o.set_factors(s_t, 16 * wm);
+  const bool rows = o.all_rows() && p.base != nullptr;
+  f32x4_t acc[8];
+  for (int n0 = first; n0 < last; n0 += COLS) {
+    const int n = n0 + 128 * wn;
+    const bool full = rows && n + 128 <= p.N;
+    if (full) o.template load<true>(p, n);
+    else o.template load<false>(p, n);
+    clear(acc);
+    for (int pass = 0; pass < passes; ++pass) {
+      // (behind a full first pass's B are the stores of the step before, which is
+      // full, too, and the base: they stay in flight)
+      if (full && pass == 0) {
+        if (n0 == first) wait_loads<Outputs<ACT>::LOADS>();
+        else wait_loads<2 * Outputs<ACT>::LOADS>();
+      } else {
+        wait_loads<0>();
+      }
+      barrier();
+      multiply_pass<ACT, BM, RANKS>(p, s_t, 16 * wm, s_b, l, 128 * wn, pass, acc);
+      barrier();
+      const bool more = pass + 1 < passes;
+      if (more || n0 + COLS < last) {
+        l = b_layout<ACT>(p, more ? pass + 1 : 0);
+        load_b<ACT, COLS, WAVES>(p, rt.adapter, more ? n0 : n0 + COLS, more ? pass + 1 : 0, l, b_at, wave);
       }
     }
-    if (n + 8 * g >= p.N) continue;
+    if (full) o.template store<true>(p, n, acc);
+    else o.template store<false>(p, n, acc);
+  }
+}
+
+// Both products of a tile of 16 positions in one launch, for few rows: every
+// block of a tile's columns makes the tile's t by itself.  Each wave has 128
+// columns at a time and loads their B alone, the first of it ahead of the first
+// product.
+template <int ACT, int NT, int WAVES, int STAGES>
+__global__ __launch_bounds__(64 * WAVES) void lora_fused_kernel(LoraParams p, int cols) {
+  constexpr int RANKS = 32, RING = STAGES * (1 + NT) * kUnitBytes, B = 128 * 16 * NT * Act<ACT>::bytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_ring[WAVES][RING];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_b[WAVES][B];
+  __shared__ __attribute__((aligned(16))) TileT<ACT, 16, RANKS> s_t;
+  __shared__ __attribute__((aligned(16))) float s_f[16][16 * NT + 4];
+  __shared__ int s_row[16];
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowTile rt = find_rows<16>(p, static_cast<int>(blockIdx.x));
+  if (!rt.found) return;
+  const bool bare = rt.adapter < 0 || rt.adapter >= p.L;
+  if (bare && p.base == p.y) return;
+  const int first = static_cast<int>(blockIdx.y) * cols + 128 * wave;
+  const int last = min((static_cast<int>(blockIdx.y) + 1) * cols, p.N);
+  const BLayout l = b_layout<ACT>(p, 0);
+  const uint32_t b_at = lds_address(s_b[wave]);
+  Outputs<ACT> o;
+  if (threadIdx.x < 16) s_row[threadIdx.x] = rt.begin + static_cast<int>(threadIdx.x) < rt.end
+                                                 ? row_of(p, rt.begin + threadIdx.x) : -1;
+  if (!bare && first < last) load_b<ACT, 128, 1>(p, rt.adapter, first, 0, l, b_at, 0);
+  __syncthreads();
+  o.set_rows(s_row, 0);
+  if (bare) {
+    copy_columns<ACT>(p, o, first, last, 128 * WAVES);
+    return;
+  }
+  o.template load<false>(p, first < last ? first : p.N);
+  {
+    f32x4_t acc[NT];
+    shrink_tile<ACT, NT, WAVES, STAGES>(p, rt, 0, wave, (p.K + kUnitK<ACT> - 1) / kUnitK<ACT>, s_ring[wave], acc);
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(s_ring[wave]);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = s_row[16 * m + c16];
-      if (row < 0) continue;
-      float by = 1.0f;
-      if constexpr (ACT == ACT_F16) by = bare ? 1.0f : s_unscale[16 * m + c16];
-      float d[8];
+    for (int i = 0; i < NT; ++i) sum[i * 64 + lane] = acc[i];
+  }
+  __syncthreads();
+  {
+    if (wave < NT) {
+      f32x4_t v = reinterpret_cast<const f32x4_t*>(s_ring[0])[wave * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = acc[i >> 2][m][i & 3] * by;
-      add_row8<ACT>(p, row, n + 8 * g, d, wide);
+      for (int w = 1; w < WAVES; ++w) v += reinterpret_cast<const f32x4_t*>(s_ring[w])[wave * 64 + lane];
+      *reinterpret_cast<f32x4_t*>(&s_f[c16][16 * wave + 4 * g]) = v;
     }
+    __syncthreads();
+    prepare_t<ACT, 16, RANKS, 64 * WAVES>(p, rt.end - rt.begin, p.scales ? p.scales[rt.adapter] : 1.0f, s_t,
+                                          [&](int r, int k, float (&v)[8]) {
+#pragma unroll
+                                            for (int i = 0; i < 8; ++i) v[i] = s_f[r][k + i];
+                                          });
+    __syncthreads();
+  }
+  o.set_factors(s_t, 0);
+  for (int n0 = first; n0 < last; n0 += 128 * WAVES) {
+    if (n0 != first) {
+      load_b<ACT, 128, 1>(p, rt.adapter, n0, 0, l, b_at, 0);
+      o.template load<false>(p, n0);
+    }
+    wait_loads<0>();
+    f32x4_t acc[8];
+    clear(acc);
+    multiply_pass<ACT, 16, RANKS>(p, s_t, 0, s_b[wave], l, 0, 0, acc);
+    o.template store<false>(p, n0, acc);
+    wait_lds();
   }
 }
 
 namespace {
 
+unsigned row_tiles(const LoraParams& p, int bm) {
+  return static_cast<unsigned>(p.T / bm + std::min<int64_t>(p.T, p.L + 2));
+}
+
+template <int ACT, int NT>
+void launch_shrink(const LoraParams& p, int rows, hipStream_t stream) {
+  const dim3 grid(row_tiles(p, rows), p.splits, (p.rank + 16 * NT - 1) / (16 * NT));
+  if (rows == 128) lora_shrink_rows_kernel<ACT, NT, 8, 3><<<grid, 512, 0, stream>>>(p);
+  else if (rows == 64) lora_shrink_rows_kernel<ACT, NT, 4, 3><<<grid, 256, 0, stream>>>(p);
+  else lora_shrink_kernel<ACT, NT, 4, NT == 4 ? 3 : 4><<<grid, 256, 0, stream>>>(p);
+}
+template <int ACT, int WM, int WN>
+void launch_expand(const LoraParams& p, int cols, hipStream_t stream) {
+  const dim3 grid(row_tiles(p, 16 * WM) * ((p.N + cols - 1) / cols));
+  constexpr int threads = 64 * WM * WN;
+  if (p.rank <= 64) lora_expand_kernel<ACT, WM, WN, 64><<<grid, threads, 0, stream>>>(p, cols);
+  else if (p.rank <= 128) lora_expand_kernel<ACT, WM, WN, 128><<<grid, threads, 0, stream>>>(p, cols);
+  else lora_expand_kernel<ACT, WM, WN, 256><<<grid, threads, 0, stream>>>(p, cols);
+}
+
 template <int ACT>
 hipError_t launch_lora_as(const LoraParams& p, const LoraPlan& plan, hipStream_t stream) {
-  auto tiles = [&](int bm) { return static_cast<unsigned>(p.T / bm + std::min<int64_t>(p.T, p.L + 2)); };
-  if (plan.shrink_mt == 4) {
-    const dim3 grid(tiles(64), p.splits, (p.rank + 63) / 64);
-    lora_shrink_kernel<ACT, 4, 4><<<grid, kLoraThreads, 0, stream>>>(p);
-  } else {
-    const dim3 grid(tiles(16), p.splits, (p.rank + 63) / 64);
-    lora_shrink_kernel<ACT, 1, 4><<<grid, kLoraThreads, 0, stream>>>(p);
+  if (plan.fused) {                    // (the stages and the columns' B fill most of the LDS)
+    const dim3 grid(row_tiles(p, 16), (p.N + plan.cols - 1) / plan.cols);
+    if (p.rank <= 16) lora_fused_kernel<ACT, 1, 8, ACT == ACT_F32 ? 2 : 3><<<grid, 512, 0, stream>>>(p, plan.cols);
+    else lora_fused_kernel<ACT, 2, 4, ACT == ACT_F32 ? 3 : 4><<<grid, 256, 0, stream>>>(p, plan.cols);
+    return hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
+  if (p.rank <= 16) launch_shrink<ACT, 1>(p, plan.shrink_rows, stream);
+  else if (p.rank <= 32) launch_shrink<ACT, 2>(p, plan.shrink_rows, stream);
+  else launch_shrink<ACT, 4>(p, plan.shrink_rows, stream);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const unsigned columns = static_cast<unsigned>((p.N + 255) / 256);
-  int pitch = 32;                      // as t_pitch
-  while (pitch < p.rank) pitch *= 2;
-  const size_t row_bytes = static_cast<size_t>(pitch + 8) * 4;       // hi and lo, or fp32
-  if (plan.expand_mt == 4)
-    lora_expand_kernel<ACT, 4><<<dim3(tiles(64), columns), kLoraThreads, 64 * row_bytes, stream>>>(p);
-  else
-    lora_expand_kernel<ACT, 1><<<dim3(tiles(16), columns), kLoraThreads, 16 * row_bytes, stream>>>(p);
+  if (plan.many) launch_expand<ACT, 2, 2>(p, plan.cols, stream);
+  else launch_expand<ACT, 1, 2>(p, plan.cols, stream);
   return hipGetLastError();
 }
 

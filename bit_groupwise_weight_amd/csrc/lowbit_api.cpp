@@ -755,33 +755,67 @@ constexpr int64_t kGroupOneLaunch = 16384, kGroupChunkExperts = 900;
 constexpr int64_t kLoraMaxN = int64_t(1) << 23;
 constexpr int64_t kLaunchBlocks = lowbit::kF8MaxThreads / 256;   // of 256 threads
 
-// Schedule of the adapters' two products: 64-row tiles where adapters have
-// rows for them, and enough K ranges of the first product to fill the device.
+// Schedule of the adapters' two products.
 struct LoraSchedule {
   lowbit::LoraPlan plan;
-  int rank_pad, splits, k_split;
+  int rank_pad, splits, units_split;
   size_t bytes;
 };
-LoraSchedule lora_schedule(int64_t T, int64_t L, int64_t rank, int64_t K) {
+LoraSchedule lora_schedule(int64_t T, int64_t L, int64_t rank, int64_t N, int64_t K, lowbit_dtype dtype) {
   LoraSchedule s{};
-  const int64_t each = T / std::min(T, L);
-  const int mt = each >= 32 && rank <= 128 ? 4 : 1;
-  s.plan = {mt, mt};
+  const int64_t each = T / std::min(T, L), cus = device_cus();   // rows an adapter
+  const int64_t units = (K * static_cast<int64_t>(dtype_bytes(dtype)) + 127) / 128;
   s.rank_pad = static_cast<int>((rank + 15) / 16 * 16);
-  const int64_t tiles = std::max<int64_t>((T + 16 * mt - 1) / (16 * mt), 1) * ((rank + 63) / 64);
-  const int64_t want = std::max<int64_t>(2 * device_cus() / tiles, 1);
-  const int64_t most = std::max<int64_t>((K + 255) / 256, 1);
-  int64_t splits = std::min<int64_t>({want, most, 64});
-  s.k_split = static_cast<int>(((K + splits - 1) / splits + 127) / 128 * 128);
-  s.splits = static_cast<int>((K + s.k_split - 1) / s.k_split);
-  s.bytes = static_cast<size_t>(s.splits) * T * s.rank_pad * sizeof(float);
+  s.splits = 1;
+  s.units_split = static_cast<int>(units);
+  // tiles that hold rows: those of all rows, and a part of one for each adapter
+  auto tiles = [&](int64_t rows) { return (T + rows - 1) / rows + std::min(T, L) / 2; };
+
+  // One launch for few rows.  Each block reads its tile's A and x whole (some 125
+  // KB a us, beside 4 us of latencies), and takes `step` columns at a time (2.5
+  // us more for a second step, up to 3 us more where every CU has a block); two
+  // launches are 11 to 12 us.  Measured, one / two launches, us, bf16: 1 row of
+  // rank 16, 4096 -> 4096 6.6 / 9.5, 14336 -> 4096 11.2 / 11.6, rank 32 7.5 /
+  // 11.2; 64 rows of 32 adapters of rank 16, 4096 -> 14336 10.5 / 14.6, 14336 ->
+  // 4096 15.1 / 14.6, of rank 32, 4096 -> 14336 24 / 16; 512 rows of 32 adapters,
+  // 4096 -> 14336 25 / 21.
+  const int64_t step = rank <= 16 ? 1024 : 512, steps = (N + step - 1) / step;
+  const int64_t across = std::max<int64_t>(1, std::min(steps, cus / tiles(16)));
+  const int64_t turns = (steps + across - 1) / across;
+  const double one_us = 4.0 + static_cast<double>((rank + 16) * units * 128) / 125e3 +
+                        2.5 * static_cast<double>(turns - 1) +
+                        3.0 * static_cast<double>(tiles(16) * across) / static_cast<double>(cus);
+  if (each < 32 && rank <= 32 && turns <= 2 && tiles(16) <= cus / 2 && one_us < 11.5) {
+    s.plan.fused = true;
+    s.plan.cols = static_cast<int>(turns * step);
+    return s;
+  }
+
+  // Two launches.  Tiles of 16 rows whose K the waves share, or, where adapters
+  // have rows for them, of 64 or 128 in the first product (8192 rows, rank 64:
+  // 27 us in tiles of 128, 33 of 64) and of 32 in the second.
+  s.plan.many = each >= 32;
+  s.plan.shrink_rows = each >= 256 ? 128 : each >= 32 ? 64 : 16;
+  // as many K ranges as there are CUs for: the second product adds their sums up
+  // (8192 rows: 111 us with 4 of them, 125 with 16)
+  const int64_t want = std::max<int64_t>(cus / (tiles(s.plan.shrink_rows) * ((rank + 63) / 64)), 1);
+  const int64_t splits = std::min<int64_t>({want, (units + 7) / 8, 16});
+  s.units_split = static_cast<int>((units + splits - 1) / splits);
+  s.splits = static_cast<int>((units + s.units_split - 1) / s.units_split);
+  // columns of a block: the most that leave each CU two blocks (64 rows of 32
+  // adapters, 14336 columns: 512 10.4 us, 256 12.8, 1024 15.2; 777 rows of 7,
+  // 5001 columns: 256 11.2, 512 14.0; 8192 rows: 1024 109, 2048 134)
+  s.plan.cols = 1024;
+  while (s.plan.cols > 256 && tiles(s.plan.many ? 32 : 16) * ((N + s.plan.cols - 1) / s.plan.cols) < 2 * cus)
+    s.plan.cols /= 2;
+  s.bytes = static_cast<size_t>(s.splits) * static_cast<size_t>(T) * s.rank_pad * sizeof(float);
   return s;
 }
 
 bool lora_sizes_ok(int64_t T, int64_t L, int64_t rank, int64_t N, int64_t K) {
   return T >= 0 && T <= kMaxDim && L >= 1 && L <= kF8MaxExperts && rank >= 8 && rank % 8 == 0 &&
          rank <= lowbit::kLoraMaxRank && N >= 1 && N <= kLoraMaxN && K >= 16 && K % 16 == 0 && K <= kQ8MaxK &&
-         (T / 16 + std::min(T, L + 2)) * ((N + 255) / 256) < kLaunchBlocks;
+         (T / 16 + std::min(T, L + 2)) * std::max((N + 255) / 256, (rank + 63) / 64) < kLaunchBlocks;
 }
 
 }  // namespace
@@ -1238,7 +1272,7 @@ lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const f
 size_t lowbit_lora_workspace_bytes(int64_t T, int64_t L, int64_t rank, int64_t N, int64_t K,
                                    lowbit_dtype dtype) {
   if (!lora_sizes_ok(T, L, rank, N, K) || T == 0 || !valid_dtype(dtype)) return 0;
-  return lora_schedule(T, L, rank, K).bytes;
+  return lora_schedule(T, L, rank, N, K, dtype).bytes;
 }
 
 lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const float* scales,
@@ -1250,7 +1284,8 @@ lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const flo
   if (M < 0 || M > kMaxDim || !lora_sizes_ok(T, L, rank, N, K))
     return fail(LOWBIT_ERR_INVALID_ARG,
                 "M=%lld T=%lld L=%lld rank=%lld N=%lld K=%lld: rows in 0..2^30, L in 1..2^16, rank a multiple of 8 "
-                "up to 256, K a multiple of 16 up to 2^23, N in 1..2^23, fewer than 2^24 tiles of 16 x 256",
+                "up to 256, K a multiple of 16 up to 2^23, N in 1..2^23, fewer than 2^24 tiles of 16 x 256 outputs or 16 x 64 "
+                "of x . a",
                 (long long)M, (long long)T, (long long)L, (long long)rank, (long long)N, (long long)K);
   if (!rows && M != T) return fail(LOWBIT_ERR_INVALID_ARG, "without rows, M=%lld must be T=%lld", (long long)M, (long long)T);
   if (!a || !b || !offsets) return fail(LOWBIT_ERR_INVALID_ARG, "NULL a, b or offsets");
@@ -1265,7 +1300,7 @@ lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const flo
     return fail(LOWBIT_ERR_MISALIGNED, "x, a and b must be 16-byte aligned");
   if (!aligned(scales, 4) || !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(base, e) || !aligned(y, e))
     return fail(LOWBIT_ERR_MISALIGNED, "scales, rows, offsets, base and y must be aligned to their element size");
-  const LoraSchedule s = lora_schedule(T, L, rank, K);
+  const LoraSchedule s = lora_schedule(T, L, rank, N, K, dtype);
   if (workspace_bytes < s.bytes)
     return fail(LOWBIT_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, s.bytes);
   lowbit::LoraParams p{};
@@ -1286,8 +1321,7 @@ lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const flo
   p.rank = static_cast<int>(rank);
   p.rank_pad = s.rank_pad;
   p.splits = s.splits;
-  p.k_split = s.k_split;
-  p.wide = N % 8 == 0 && aligned(base, 16) && aligned(y, 16);
+  p.units_split = s.units_split;
   const hipError_t he = lowbit::launch_lora(p, s.plan, act_kind(dtype), static_cast<hipStream_t>(stream));
   if (he != hipSuccess) return hip_fail(he, "lora launch");
   return LOWBIT_OK;

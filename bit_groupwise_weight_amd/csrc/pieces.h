@@ -7,30 +7,26 @@
 
 namespace lowbit {
 
-template <int ACT> struct Piece {                  // 16-bit types
-  struct __attribute__((packed, aligned(2))) Raw { u32v4_t w; };
-  Raw r;
-};
-template <> struct Piece<ACT_F32> {
-  struct __attribute__((packed, aligned(4))) Raw { u32v4_t w[2]; };
-  Raw r;
-};
+typedef u32v4_t u32v4_any_t __attribute__((aligned(2)));
+
+template <int ACT> struct Piece { u32v4_t w[Act<ACT>::bytes / 2]; };
 
 // The first `n` elements from p on, zeros behind them (n < 1: only zeros).
 template <int ACT>
 __device__ __forceinline__ void load_piece(const typename Act<ACT>::bits_t* p, int n, Piece<ACT>& v) {
   if (n >= 8) {
-    v.r = *reinterpret_cast<const typename Piece<ACT>::Raw*>(p);
+#pragma unroll
+    for (int q = 0; q < Act<ACT>::bytes / 2; ++q) v.w[q] = reinterpret_cast<const u32v4_any_t*>(p)[q];
     return;
   }
   uint32_t e[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : 0u;
   if constexpr (ACT == ACT_F32) {
-    v.r.w[0] = u32v4_t{e[0], e[1], e[2], e[3]};
-    v.r.w[1] = u32v4_t{e[4], e[5], e[6], e[7]};
+    v.w[0] = u32v4_t{e[0], e[1], e[2], e[3]};
+    v.w[1] = u32v4_t{e[4], e[5], e[6], e[7]};
   } else {
-    v.r.w = u32v4_t{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
+    v.w[0] = u32v4_t{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
   }
 }
 
@@ -38,12 +34,12 @@ template <int ACT>
 __device__ __forceinline__ void piece_to_float(const Piece<ACT>& v, float (&f)[8]) {
   if constexpr (ACT == ACT_F32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v.r.w[i >> 2][i & 3]);
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v.w[i >> 2][i & 3]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[2 * i] = act_bits_to_float<ACT>(v.r.w[i] & 0xffffu);
-      f[2 * i + 1] = act_bits_to_float<ACT>(v.r.w[i] >> 16);
+      f[2 * i] = act_bits_to_float<ACT>(v.w[0][i] & 0xffffu);
+      f[2 * i + 1] = act_bits_to_float<ACT>(v.w[0][i] >> 16);
     }
   }
 }
@@ -53,20 +49,22 @@ template <int ACT>
 __device__ __forceinline__ void store_piece(typename Act<ACT>::bits_t* p, int n, const float (&f)[8]) {
   Piece<ACT> v;
   if constexpr (ACT == ACT_F32) {
-    v.r.w[0] = u32v4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-    v.r.w[1] = u32v4_t{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i >> 2][i & 3] = __float_as_uint(f[i]);
   } else {
-    v.r.w = u32v4_t{pack2<ACT>(f[0], f[1]), pack2<ACT>(f[2], f[3]), pack2<ACT>(f[4], f[5]), pack2<ACT>(f[6], f[7])};
+    v.w[0] = u32v4_t{pack2<ACT>(f[0], f[1]), pack2<ACT>(f[2], f[3]), pack2<ACT>(f[4], f[5]), pack2<ACT>(f[6], f[7])};
   }
   if (n >= 8) {
-    *reinterpret_cast<typename Piece<ACT>::Raw*>(p) = v.r;
+#pragma unroll
+    for (int q = 0; q < Act<ACT>::bytes / 2; ++q)
+      __builtin_nontemporal_store(v.w[q], reinterpret_cast<u32v4_any_t*>(p) + q);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (i < n) {
-      if constexpr (ACT == ACT_F32) p[i] = v.r.w[i >> 2][i & 3];
-      else p[i] = static_cast<uint16_t>(v.r.w[i >> 1] >> (16 * (i & 1)));
+      if constexpr (ACT == ACT_F32) p[i] = v.w[i >> 2][i & 3];
+      else p[i] = static_cast<uint16_t>(v.w[0][i >> 1] >> (16 * (i & 1)));
     }
   }
 }

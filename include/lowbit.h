@@ -554,7 +554,8 @@ lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const f
  *            place), must not overlap an input otherwise.
  *   M, T >= 0 (0 is a no-op; at most 2^30), 1 <= L <= 2^16, rank a multiple of
  *            8 up to 256, K a positive multiple of 16 up to 2^23, N 1 .. 2^23,
- *            (floor(T / 16) + min(T, L + 2)) * ceil(N / 256) < 2^24.
+ *            (floor(T / 16) + min(T, L + 2)) * max(ceil(N / 256),
+ *            ceil(rank / 64)) < 2^24.
  *   x, a and b 16-byte aligned, the other arrays to their element size; rows
  *   of base and y of whole 16-byte pieces are the fast case.
  *   workspace: at least lowbit_lora_workspace_bytes(), 256-byte aligned (NULL

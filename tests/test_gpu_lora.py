@@ -97,6 +97,29 @@ def test_lora(M, L, rank, K, N, dtype):
     check(t, call(t))
 
 
+SCHEDULES = [  # one launch: one and two turns of columns, ranks to 32
+             (16, 1, 16, 272, 2600), (200, 40, 16, 2064, 2100), (300, 80, 8, 144, 5200), (9, 3, 32, 4112, 700),
+             (90, 30, 24, 528, 3300),
+             # two launches of 16 rows a tile: long K in ranges, ranks past a pass
+             (40, 20, 64, 4112, 300), (20, 20, 128, 2064, 520), (50, 2, 256, 1040, 129), (17, 17, 96, 16400, 40),
+             # of 64 and of 128, every number of rank tiles, whole tiles and parts, many turns of columns
+             (128, 1, 16, 528, 1300), (192, 2, 32, 144, 2600), (256, 4, 72, 1040, 520), (600, 2, 16, 1040, 264),
+             (600, 2, 24, 272, 1032), (1024, 2, 64, 2064, 520), (700, 2, 256, 272, 272), (900, 3, 8, 16, 5),
+             (515, 1, 200, 4112, 65)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M, L, rank, K, N", SCHEDULES)
+def test_lora_schedules(M, L, rank, K, N, dtype):
+    t = inputs(M * 3 + rank + N, M, L, rank, K, N, dtype, bare=0.0 if M % 2 == 0 else 0.1)
+    y = call(t)
+    check(t, y)
+    rows, offsets = plan(t)
+    own = t["base"].to(DEV)                            # in place: the same
+    lb.lowbit_lora(t["x"].to(DEV), t["a"].to(DEV), t["b"].to(DEV), t["scales"].to(DEV), rows, offsets, own, y=own)
+    assert torch.equal(own, y)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_lora_without_base_or_scales(dtype):
     for M, L, rank, K, N in ((3, 2, 16, 64, 40), (150, 2, 64, 272, 250)):
