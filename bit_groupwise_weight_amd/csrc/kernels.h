@@ -270,6 +270,7 @@ struct RouteParams {
   int groups;             // divides E
   int groups_shift;       // log2(groups), rounded up
   int topk_groups, group_best;
+  int index_bits;         // of an expert's index
   int renormalize;
   float scale;
 };

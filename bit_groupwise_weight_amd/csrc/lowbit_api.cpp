@@ -1199,6 +1199,7 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
   p.sigmoid = score == LOWBIT_ROUTE_SIGMOID;
   p.groups = static_cast<int>(groups);
   while ((int64_t{1} << p.groups_shift) < groups) ++p.groups_shift;
+  while ((int64_t{1} << p.index_bits) < E) ++p.index_bits;
   p.topk_groups = static_cast<int>(topk_groups);
   p.group_best = group_best;
   p.renormalize = renormalize != 0;

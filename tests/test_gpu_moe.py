@@ -118,6 +118,52 @@ def test_route_neighbours_below_fp32(sigmoid, with_bias):
     check_route(logits, 7, bias=bias, sigmoid=sigmoid)
 
 
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("E, groups, topk_groups", [(64, 4, 2), (256, 8, 4), (320, 5, 1), (512, 32, 9)])
+def test_route_neighbouring_groups_and_rows_of_one_value(E, groups, topk_groups, with_bias):
+    """Groups whose values fp32 cannot tell apart, and rows full of experts that it cannot."""
+    g = torch.Generator().manual_seed(E)
+    up = lambda t: torch.nextafter(t, torch.tensor(9.0))
+    for T in (6, 5000):                                  # both layouts of lanes
+        logits = torch.full((T, E), 0.4)
+        for _ in range(2):
+            logits = torch.where(torch.rand(T, E, generator=g) < 0.3, up(logits), logits)
+        logits[T // 2:] = 0.4                            # all alike
+        far = torch.randn(T, E, generator=g) - 3         # ... or only the largest of each group
+        far.view(T, groups, -1)[:, :, 1] = logits[:, :groups]
+        far.view(T, groups, -1)[:, :, 3] = logits[:, groups:2 * groups]
+        bias = None
+        if with_bias:
+            bias = torch.where(torch.rand(E, generator=g) < 0.5, 0.25, float(np.nextafter(np.float32(0.25), np.float32(1))))
+        rows = torch.arange(0, T, max(T // 40, 1))
+        for l in (logits, far):
+            got = lb.lowbit_moe_route(l.to(DEV), 6, bias=None if bias is None else bias.to(DEV), score=lb.ROUTE_SIGMOID,
+                                      groups=groups, topk_groups=topk_groups, group_best=2)
+            e, _ = o.route(f64(l[rows]), 6, bias=None if bias is None else f64(bias), sigmoid=True, groups=groups,
+                           topk_groups=topk_groups, best=2)
+            assert np.array_equal(got[0][rows.to(DEV)].cpu().numpy(), e)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bias", "groups"])
+def test_route_many_rows(kind):
+    """Some ten million scores: every choice that of 64 bits."""
+    T, E, k = 40000, 256, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(17)
+    logits = 1.5 * torch.randn(T, E, generator=g, device=DEV)
+    kw, c = {}, logits.double()
+    if kind != "f32":
+        bias = 0.1 * torch.randn(E, generator=g, device=DEV)
+        kw, c = dict(bias=bias, score=lb.ROUTE_SIGMOID), torch.sigmoid(c) + bias.double()
+    if kind == "groups":
+        kw.update(groups=8, topk_groups=4, group_best=2)
+        value = c.view(T, 8, 32).topk(2, 2).values.sum(2)
+        keep = torch.zeros(T, 8, dtype=torch.bool, device=DEV).scatter_(1, value.topk(4, 1).indices, True)
+        c = torch.where(keep.repeat_interleave(32, 1), c, NEG)
+    want = c.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(lb.lowbit_moe_route(logits, k, **kw)[0].long(), want)
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("groups, topk_groups, best", [(1, 1, 1), (6, 2, 1), (6, 2, 2)])
 @pytest.mark.parametrize("with_bias", [False, True])
