@@ -276,6 +276,8 @@ struct RouteParams {
 };
 hipError_t launch_moe_route(const RouteParams&, int act, hipStream_t);
 
+constexpr int kGroupChunkExperts = 900;   // 18 arrays of E + 2 in 64 KiB of LDS
+constexpr int64_t kGroupAlone = 65536;    // slots that one launch without workspace sorts
 // Slots of a block of group_rows' two launches.
 constexpr int64_t group_chunk(int64_t S) { return S <= 128 * 1024 ? 1024 : 4096; }
 struct GroupRowsParams {

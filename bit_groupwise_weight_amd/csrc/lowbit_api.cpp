@@ -748,10 +748,6 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
 
 // ------------------------------------------- around the experts, adapters --
 
-// group_rows: the slots that one launch, a block an expert, sorts no slower than
-// two over chunks (both sides' times stand at the kernels), and the experts whose
-// counts by wave fit the LDS that the two take (18 arrays of E + 2 in 64 KiB).
-constexpr int64_t kGroupOneLaunch = 16384, kGroupChunkExperts = 900;
 constexpr int64_t kLoraMaxN = int64_t(1) << 23;
 constexpr int64_t kLaunchBlocks = lowbit::kF8MaxThreads / 256;   // of 256 threads
 
@@ -1212,7 +1208,7 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
 size_t lowbit_group_rows_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
   if (T <= 0 || T > kMaxDim || topk < 1 || topk > kMaxDim || T * topk > kMaxDim || E < 1 || E > kF8MaxExperts) return 0;
   const int64_t S = T * topk;
-  if (S <= kGroupOneLaunch || E > kGroupChunkExperts) return 0;
+  if (S <= lowbit::kGroupAlone || E > lowbit::kGroupChunkExperts) return 0;
   return static_cast<size_t>((S + lowbit::group_chunk(S) - 1) / lowbit::group_chunk(S)) * (E + 1) * sizeof(int);
 }
 

@@ -33,7 +33,8 @@ __device__ __forceinline__ uint32_t expert_of(int64_t id, uint32_t E) {
 // second pass costs a prefix sum and a turn for each bit of the fullest mask.
 // (One run a wave where S allows it; otherwise the masks are made again.)
 // Bound by a launch up to some 4096 slots (64 tokens of 8 in 64 experts: 3.1
-// us, an empty launch 2.7) and by every block's reading of all ids from there.
+// us, an empty launch 2.7), by every block's reading of all ids from there: taken
+// up to 8192, and beyond for more experts than the chunks below count.
 template <class ID, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupRowsParams p) {
   __shared__ int s_below[WAVES], s_own[WAVES];
@@ -124,21 +125,33 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupRowsParams 
   }
 }
 
-// The same for many slots in two launches, a chunk of 1024 STEPS slots a block:
-// each chunk's count of every expert, into the workspace, and then each chunk's
-// places, from the counts of all chunks before it.  Taken above 16384 slots (us,
-// one launch / two: 4096 slots, 64 experts 3.4 / 5.9; 16384, 256 experts 6.9 /
-// 8.2, 8 experts 6.2 / 5.9; 65536, 64 experts 8.5 / 7.0, 256 experts 14.1 / 9.1;
-// 524288, 256 experts 141 / 17; two empty launches are 4.9).  Chunks of 1024
-// slots up to 128 of them, of 4096 beyond (65536 slots 9.1 against 11.0 in
-// chunks of 2048, 524288 slots 29 against 17.5): what a block adds up of the
-// others' counts grows with their number.
+// For more slots, a chunk of 1024 STEPS of them a block: each chunk's places, from
+// the counts of all chunks before it.  Up to 65536 slots every block counts all
+// of them itself (bound by the LDS's atomic additions, some 8 us for 65536);
+// beyond, a first launch counts each chunk into the workspace.  us, block an
+// expert / one launch of chunks / two: 4096 slots, 256 experts 3.3 / 5.8 / 7.7;
+// 16384 6.8 / 6.0 / 8.4; 32768 - / 7.7 / 9.7; 65536 14.1 / 11.2 / 9.1 (but an
+// eager call takes 13 with two launches and a workspace); 131072 - / 18.5 /
+// 11.0; 524288 141 / - / 17 (two empty launches are 4.9).  Chunks of 1024 slots
+// up to 128 of them, of 4096 beyond (524288 slots 29 against 17): what a block
+// adds up of the others' counts grows with their number.
 constexpr int kChunkWaves = 16;
 
 template <class ID>
 __device__ __forceinline__ uint32_t chunk_id(const GroupRowsParams& p, int64_t s) {
   const uint32_t E = static_cast<uint32_t>(p.E);
   return s < p.S ? expert_of(static_cast<const ID*>(p.ids)[s], E) : E + 1;
+}
+
+// counts[x] += 1 for each lane's x.  (A wave of one id, as where all tokens go one
+// way, would queue at its count.)
+__device__ __forceinline__ void count_one(int* counts, uint32_t x) {
+  const uint32_t one = __builtin_amdgcn_readfirstlane(x);
+  if (__ballot(x == one) == ~uint64_t{0}) {
+    if ((threadIdx.x & 63) == 0) atomicAdd(&counts[one], 64);
+  } else {
+    atomicAdd(&counts[x], 1);
+  }
 }
 
 template <class ID, int STEPS>
@@ -152,20 +165,31 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_count_kernel(GroupRows
   for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID>(p, begin + i * 64 * kChunkWaves + threadIdx.x);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    // (a wave of one id, as where all tokens go one way, would queue at its count)
-    const uint32_t one = __builtin_amdgcn_readfirstlane(x[i]);
-    if (__ballot(x[i] == one) == ~uint64_t{0}) {
-      if ((threadIdx.x & 63) == 0) atomicAdd(&s_count[one], 64);
-    } else {
-      atomicAdd(&s_count[x[i]], 1);
-    }
+    count_one(s_count, x[i]);
   }
   __syncthreads();
   int* to = p.counts + static_cast<size_t>(blockIdx.x) * (p.E + 1);
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x) to[e] = s_count[e];
 }
 
-template <class ID, int STEPS>
+// Four ids from slot s on, as experts (E + 1 past the last slot).
+template <class ID>
+__device__ __forceinline__ void load_four(const GroupRowsParams& p, int s, uint32_t (&x)[4]) {
+  const uint32_t E = static_cast<uint32_t>(p.E);
+  struct __attribute__((packed, aligned(sizeof(ID)))) Four { ID v[4]; };
+  const ID* from = static_cast<const ID*>(p.ids) + s;
+  if (s + 4 <= p.S) {
+    const Four f = *reinterpret_cast<const Four*>(from);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = expert_of(f.v[q], E);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = s + q < p.S ? expert_of(from[q], E) : E + 1;
+  }
+}
+
+// ALONE: in one launch, each block counting all slots itself.
+template <class ID, int STEPS, bool ALONE>
 __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRowsParams p, int chunks, int bits) {
   extern __shared__ int s_mem[];
   const int ids = p.E + 2;
@@ -182,17 +206,36 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
   for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID>(p, begin + i * 64 + lane);
   for (int i = threadIdx.x; i < (2 + kChunkWaves) * ids; i += blockDim.x) s_mem[i] = 0;
   __syncthreads();
-  for (int e = lane; e <= p.E; e += 64) {    // the waves take the chunks in turn
-    int before = 0, all = 0;
-    const int* from = p.counts + e;
-#pragma unroll 4
-    for (int c = wave; c < chunks; c += kChunkWaves) {
-      const int v = from[static_cast<size_t>(c) * (p.E + 1)];
-      all += v;
-      before += c < static_cast<int>(blockIdx.x) ? v : 0;
+  if constexpr (ALONE) {
+    const int here = static_cast<int>(blockIdx.x) * (1024 * STEPS), S = static_cast<int>(p.S);
+#pragma unroll 1
+    for (int s0 = 0; s0 < S; s0 += 4 * 4096) {
+      uint32_t v[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) load_four<ID>(p, min(s0 + 4096 * r + 4 * static_cast<int>(threadIdx.x), S), v[r]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // (a chunk begins at a multiple of 1024: a lane's four are all before it or none)
+        int* to = s0 + 4096 * r + 4 * static_cast<int>(threadIdx.x) < here ? s_base : s_all;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) count_one(to, v[r][q]);
+      }
     }
-    if (all != 0) atomicAdd(&s_all[e], all);
-    if (before != 0) atomicAdd(&s_base[e], before);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) s_all[e] += s_base[e];
+  } else {
+    for (int e = lane; e <= p.E; e += 64) {  // the waves take the chunks in turn
+      int before = 0, all = 0;
+      const int* from = p.counts + e;
+#pragma unroll 4
+      for (int c = wave; c < chunks; c += kChunkWaves) {
+        const int v = from[static_cast<size_t>(c) * (p.E + 1)];
+        all += v;
+        before += c < static_cast<int>(blockIdx.x) ? v : 0;
+      }
+      if (all != 0) atomicAdd(&s_all[e], all);
+      if (before != 0) atomicAdd(&s_base[e], before);
+    }
   }
   __syncthreads();
   int carry = 0;
@@ -267,20 +310,24 @@ void launch_chunks_as(const GroupRowsParams& p, int bits, hipStream_t stream) {
   const int chunks = static_cast<int>((p.S + 1024 * STEPS - 1) / (1024 * STEPS)), threads = 64 * kChunkWaves;
   const size_t row = (p.E + 2) * sizeof(int);
   group_count_kernel<ID, STEPS><<<chunks, threads, row, stream>>>(p);
-  group_place_kernel<ID, STEPS><<<chunks, threads, (kChunkWaves + 2) * row, stream>>>(p, chunks, bits);
+  group_place_kernel<ID, STEPS, false><<<chunks, threads, (kChunkWaves + 2) * row, stream>>>(p, chunks, bits);
 }
 template <class ID>
 void launch_group_as(const GroupRowsParams& p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.E + 1));
-  if (p.counts) {
-    int bits = 1;
-    while ((1 << bits) < p.E + 2) ++bits;
+  int bits = 1;
+  while ((1 << bits) < p.E + 2) ++bits;
+  if (p.S <= 1024) {
+    group_rows_kernel<ID, 1><<<grid, 64, 0, stream>>>(p);
+  } else if (p.S <= 8192) {
+    group_rows_kernel<ID, 4><<<grid, 256, 0, stream>>>(p);
+  } else if (p.S <= kGroupAlone && p.E <= kGroupChunkExperts) {
+    const int chunks = static_cast<int>((p.S + 1023) / 1024);
+    const size_t lds = (kChunkWaves + 2) * (p.E + 2) * sizeof(int);
+    group_place_kernel<ID, 1, true><<<chunks, 64 * kChunkWaves, lds, stream>>>(p, chunks, bits);
+  } else if (p.counts) {
     if (group_chunk(p.S) == 1024) launch_chunks_as<ID, 1>(p, bits, stream);
     else launch_chunks_as<ID, 4>(p, bits, stream);
-  } else if (p.S <= 1024) {
-    group_rows_kernel<ID, 1><<<grid, 64, 0, stream>>>(p);
-  } else if (p.S <= 4096) {
-    group_rows_kernel<ID, 4><<<grid, 256, 0, stream>>>(p);
   } else {
     group_rows_kernel<ID, 16><<<grid, 1024, 0, stream>>>(p);
   }

@@ -590,7 +590,7 @@ def _made_on(shape: Tuple[int, ...], dtype: torch.dtype, x: torch.Tensor, stream
     """An output that a call on `stream` makes, from that stream's memory: what the current stream
     freed may still be read there by work that the call's stream does not wait for."""
     if stream is None or not x.is_cuda:
-        return torch.empty(shape, dtype=dtype, device=x.device)
+        return x.new_empty(shape, dtype=dtype)
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream)
                   else torch.cuda.default_stream(x.device))
@@ -845,7 +845,8 @@ def lowbit_moe_route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tenso
     else:
         _expect_tensor(experts, "experts", (T, topk), torch.int32)
     if weights is None:
-        weights = _made_on((T, topk), torch.float32, logits, stream)
+        weights = (torch.empty_like(experts, dtype=torch.float32) if stream is None
+                   else _made_on((T, topk), torch.float32, logits, stream))
     else:
         _expect_tensor(weights, "weights", (T, topk), torch.float32)
     dev = _placed(logits, bias, experts, weights)
@@ -886,13 +887,14 @@ def lowbit_group_rows(ids: torch.Tensor, E: int, rows: Optional[torch.Tensor] = 
     else:
         _expect_tensor(offsets, "offsets", (E + 1,), torch.int32)
     if position is None:
-        position = _made_on((T, k), torch.int32, ids, stream)
+        position = (torch.empty_like(ids, dtype=torch.int32) if stream is None and ids.is_contiguous()
+                    else _made_on((T, k), torch.int32, ids, stream))
     else:
         _expect_tensor(position, "position", (T, k), torch.int32)
     if workspace is not None and workspace.dtype is not torch.uint8:
         raise ValueError("workspace must be uint8")
     dev = _placed(ids, rows, offsets, position, workspace)
-    if workspace is None and T * k > 16384:      # (fewer slots need none)
+    if workspace is None and T * k > 65536:      # (fewer slots need none)
         need = _call_on(dev, "lowbit_group_rows_workspace_bytes", T, k, E)
         workspace = None if need == 0 else _made_on((need,), torch.uint8, ids, stream)
     st = _call_on(dev, "lowbit_group_rows", _ptr(ids), _ID_BYTES[ids.dtype], T, k, E, _ptr(rows), _ptr(offsets),
@@ -972,7 +974,8 @@ def lowbit_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: Optio
     if base is not None:
         _expect_tensor(base, "base", (M, N), dt)
     if y is None:
-        y = _made_on((M, N), dt, x, stream)
+        y = (torch.empty_like(base) if stream is None and base is not None and base.is_contiguous()
+             else _made_on((M, N), dt, x, stream))
     else:
         _expect_tensor(y, "y", (M, N), dt)
     if workspace is not None and workspace.dtype is not torch.uint8:

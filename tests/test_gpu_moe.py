@@ -296,7 +296,8 @@ def test_group_rows_of_many_experts():
     check_group(torch.randint(0, 5000, (700, 2), generator=g), 5000)
 
 
-@pytest.mark.parametrize("T, k, E", [(3, 5, 4), (700, 3, 60), (2049, 8, 256), (5001, 4, 900), (70000, 2, 33)])
+@pytest.mark.parametrize("T, k, E", [(3, 5, 4), (700, 3, 60), (1025, 7, 5), (2049, 8, 256), (5001, 4, 900), (5001, 4, 1500),
+                                     (8192, 8, 61), (12001, 8, 256), (70000, 2, 33), (40000, 3, 900)])
 @pytest.mark.parametrize("kind", [torch.int32, torch.int64])
 def test_group_rows_with_and_without_workspace(T, k, E, kind):
     """Both schedules: the same rows, also where all tokens go one way; the workspace's end kept."""
