@@ -749,6 +749,7 @@ lowbit_status run_linear_f8(const uint8_t* xq, const float* xscale, const int32_
 // ------------------------------------------- around the experts, adapters --
 
 constexpr int64_t kLoraMaxN = int64_t(1) << 23;
+constexpr int64_t kRouteMaxT = int64_t(1) << 25;                 // (four rows a block of 256 threads)
 constexpr int64_t kLaunchBlocks = lowbit::kF8MaxThreads / 256;   // of 256 threads
 
 // Schedule of the adapters' two products.
@@ -1168,7 +1169,7 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
   if (!valid_dtype(dtype)) return fail(LOWBIT_ERR_UNSUPPORTED, "dtype=%d", (int)dtype);
   if (score != LOWBIT_ROUTE_SOFTMAX && score != LOWBIT_ROUTE_SIGMOID)
     return fail(LOWBIT_ERR_UNSUPPORTED, "score=%d", (int)score);
-  if (T < 0 || T > kMaxDim) return fail(LOWBIT_ERR_INVALID_ARG, "T=%lld not in 0..2^30", (long long)T);
+  if (T < 0 || T > kRouteMaxT) return fail(LOWBIT_ERR_INVALID_ARG, "T=%lld not in 0..2^25", (long long)T);
   if (E < 1 || E > lowbit::kRouteMaxExperts)
     return fail(LOWBIT_ERR_INVALID_ARG, "E=%lld not in 1..%d", (long long)E, lowbit::kRouteMaxExperts);
   if (topk < 1 || topk > E || topk > lowbit::kRouteMaxTopk)

@@ -348,7 +348,14 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_exact_kernel(RoutePar
 }
 
 // The selection on keys.  VALUED: sigmoid scores with a bias or groups by two;
-// otherwise the logits' order.
+// otherwise the logits' order.  A block stages its rows' logits in LDS with whole
+// loads, each lane takes a run of neighbours from there (V of them, in registers
+// throughout), and each choice is V comparisons and one maximum over the row's
+// lanes.  Bound by instructions where there are many rows (8192 x 256 fp32,
+// sigmoid, bias, 8 experts of 4 of 8 groups: 11.2 us, its 9 MB are 1.8; bf16 logits alone
+// 6.5), by a launch and one row's chain of choices where there are few (1 x 256,
+// 8 of 256 bf16 3.6 us, with groups 5.9, an empty launch 2.7).  The same with
+// 64-bit values throughout took 20 us.
 template <bool VALUED, int LANES, int V, int ACT>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p) {
   constexpr int ROWS = kRouteThreads / LANES;

@@ -466,7 +466,7 @@ typedef enum lowbit_route_score {
  *
  *   logits   device, T x E row-major, dtype, aligned to its element size.
  *   bias     device, E fp32, or NULL.
- *   T >= 0 (0 is a no-op; at most 2^30), 1 <= E <= 1024, 1 <= topk <=
+ *   T >= 0 (0 is a no-op; at most 2^25), 1 <= E <= 1024, 1 <= topk <=
  *            min(E, 64), groups 1 .. 64 and a divisor of E, topk_groups 1 ..
  *            groups, group_best 1 or 2, scale finite.
  *   experts  device, T x topk int32.  Written.

@@ -17,6 +17,7 @@ META = torch.device("meta")
 
 @pytest.mark.parametrize("kw, status", [
     (dict(dt=3), UNSUPPORTED), (dict(score=2), UNSUPPORTED), (dict(T=-1), INVALID), (dict(T=(1 << 30) + 1), INVALID),
+    (dict(T=(1 << 25) + 1), INVALID),        # more rows than a launch has blocks of four for
     (dict(E=0), INVALID), (dict(E=1025), INVALID), (dict(k=0), INVALID), (dict(k=65), INVALID),
     (dict(E=16, groups=4, k=17), INVALID), (dict(groups=0), INVALID), (dict(groups=5), INVALID),
     (dict(E=130, groups=65), INVALID), (dict(kg=0), INVALID), (dict(kg=9), INVALID), (dict(best=0), INVALID),
