@@ -455,15 +455,19 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
     key[i] = !stays || c[i] == kNegInf ? 0u
              : (ordered(c[i] + 0.0f) & ~mask) | (mask - static_cast<uint32_t>(r.first + i));   // (-0 is 0)
   const int count = EXACT_KEYS ? p.topk : p.topk + 3;         // at most LANES
+  // The next one is the largest key below the one before, and so the largest of
+  // key - before modulo 2^32: keys that were taken give less than those that were
+  // not, as 2^32 is more than any two differ by.  (0, none, comes again for ever:
+  // 0 - 1 is above all others.)
   uint32_t mine = 0;                   // the candidate of this lane: the lane-th largest
+  uint32_t before = 0;
   for (int j = 0; j < count; ++j) {
-    uint32_t m = key[0];
+    uint32_t m = key[0] - before;
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, key[i]);
-    m = row_max_key<LANES>(m);
+    for (int i = 1; i < V; ++i) m = max(m, key[i] - before);
+    m = row_max_key<LANES>(m) + before;
     mine = r.lane == j ? m : mine;
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = key[i] == m ? 0u : key[i];
+    before = max(m, 1u);
   }
   const int expert = mine == 0 ? -1 : static_cast<int>(mask - (mine & mask));
   if constexpr (EXACT_KEYS) {
