@@ -23,7 +23,7 @@
 // -inf masks an expert.  A row with fewer experts left than k ends in experts
 // -1 with weight 0; a row holding a NaN (softmax: or +inf) gets experts 0 ..
 // k - 1 and weights NaN, so that what it is used for shows it.
-#include "device_common.h"
+#include "f8_common.h"
 
 #include <type_traits>
 
@@ -109,14 +109,13 @@ __device__ __forceinline__ double sigmoid64(double l) {
   const double e = exp(-fabs(l));
   return (l > 0.0 ? 1.0 : e) / (1.0 + e);
 }
-// The same within 2^-21: the exponent's rounding, |l| log2(e) 2^-24 of an
-// exponential e^-|l| (below 2^-24), and those of the exponential, the sum, the
-// reciprocal and the product, at most 2^-23 each (the compiler's instructions
-// are good to a unit in the last place).
+// The same within 2^-21: with e = exp(-l) the exponent's rounding makes |l|
+// log2(e) 2^-24 of e, which is |l| 2^-23.4 s (1 - s) of s and less than 2^-25 (|l|
+// s (1 - s) is below 0.23), the exponential and the reciprocal (good to a unit in
+// the last place), the product and the sum at most 2^-23 s each.  (e may be
+// infinite, s then 0.)
 __device__ __forceinline__ float sigmoid32(float l) {
-  const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(l));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  return l > 0.0f ? r : e * r;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * l));
 }
 
 }  // namespace
@@ -147,9 +146,13 @@ __device__ __forceinline__ RouteLane route_lane(const RouteParams& p) {
 }
 
 // The two largest c of a lane, *a >= *b, and with one more.
-template <class C> __device__ __forceinline__ void add_to_two(C v, C* a, C* b) {
+__device__ __forceinline__ void add_to_two(double v, double* a, double* b) {
   *b = larger(*b, v > *a ? *a : v);
   *a = larger(*a, v);
+}
+__device__ __forceinline__ void add_to_two(float v, float* a, float* b) {
+  *b = __builtin_amdgcn_fmed3f(*a, *b, v);
+  *a = fmaxf(*a, v);
 }
 // The two largest of the group from those of its lanes, in every lane of it.
 template <class C> __device__ __forceinline__ void two_of_group(const RouteLane& r, C* a, C* b) {
@@ -200,10 +203,11 @@ __device__ __forceinline__ void select_exact(const RouteParams& p, const RouteLa
 }
 
 // The logits of a wave's rows (one or four, of at most 1024 in all) in LDS, as
-// fp32: value j at j + j / 16, so that lanes that read neighbouring runs of 16
-// do not meet in a bank.  Loaded in whole pieces, whatever the rows' alignment.
-constexpr int kWaveLogits = 1024, kWaveLds = kWaveLogits + kWaveLogits / 16;
-__device__ __forceinline__ int lds_at(int j) { return j + (j >> 4); }
+// fp32: value j at j + 4 (j / 16), so that lanes that read neighbouring runs of 16,
+// in pieces of four, do not meet in a bank.  Loaded in whole pieces, whatever the
+// rows' alignment.
+constexpr int kWaveLogits = 1024, kWaveLds = kWaveLogits + kWaveLogits / 4;
+__device__ __forceinline__ int lds_at(int j) { return j + 4 * (j >> 4); }
 template <int ACT>
 __device__ __forceinline__ void stage_logits(const void* logits, int64_t first, int n, float* lds) {
   typedef typename Act<ACT>::bits_t T;
@@ -214,13 +218,33 @@ __device__ __forceinline__ void stage_logits(const void* logits, int64_t first, 
     const int j = 256 * i + 4 * (threadIdx.x & 63);
     if (j + 4 <= n) {
       const Four f = *reinterpret_cast<const Four*>(from + j);
+      f32x4_t v;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) lds[lds_at(j) + q] = act_bits_to_float<ACT>(f.v[q]);
+      for (int q = 0; q < 4; ++q) v[q] = act_bits_to_float<ACT>(f.v[q]);
+      *reinterpret_cast<f32x4_t*>(lds + lds_at(j)) = v;
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (j + q < n) lds[lds_at(j) + q] = act_bits_to_float<ACT>(from[j + q]);
     }
+  }
+}
+// The values first .. first + held - 1 of a row that begins at `row` in such an
+// LDS array, `none` behind them; whole: V of them in every lane, from a multiple of
+// V on.
+template <int V>
+__device__ __forceinline__ void read_values(const float* lds, int row, const RouteLane& r, bool whole, float none,
+                                            float (&v)[V]) {
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f32x4_t f = *reinterpret_cast<const f32x4_t*>(lds + lds_at(row + r.first) + i + 4 * (i / 16));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[i + q] = f[q];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < r.held ? lds[lds_at(row + r.first + i)] : none;
   }
 }
 
@@ -286,7 +310,7 @@ template <int LANES, int V, int ACT>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_exact_kernel(RouteParams p) {
   constexpr int ROWS = kRouteThreads / LANES;
   __shared__ int s_chosen[ROWS][kRouteMaxTopk];
-  __shared__ float s_logits[kRouteThreads / 64][kWaveLds], s_bias[kWaveLds];
+  __shared__ __attribute__((aligned(16))) float s_logits[kRouteThreads / 64][kWaveLds], s_bias[kWaveLds];
   const RouteLane r = route_lane<LANES>(p);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
   int* chosen = s_chosen[threadIdx.x / LANES];
@@ -362,7 +386,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
   constexpr bool EXACT_KEYS = !VALUED && ACT != ACT_F32;      // 16-bit logits leave at least 13 bits
   constexpr float kOff = 0x1p-20f;     // of a score: sigmoid32's error, doubled
   __shared__ int s_chosen[ROWS][kRouteMaxTopk];
-  __shared__ float s_logits[kRouteThreads / 64][kWaveLds], s_bias[kWaveLds];
+  __shared__ __attribute__((aligned(16))) float s_logits[kRouteThreads / 64][kWaveLds], s_bias[kWaveLds];
   const RouteLane r = route_lane<LANES>(p);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
   int* chosen = s_chosen[threadIdx.x / LANES];
@@ -380,11 +404,14 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
   auto logit = [&](int e) { return logits[lds_at(row_at + e)]; };
   auto bias = [&](int e) { return p.bias != nullptr ? s_bias[lds_at(e)] : 0.0f; };
 
-  float l[V], b[VALUED ? V : 1], c[V];
+  float l[V], b[V], c[V];
+  const bool whole = p.E == p.groups * r.group_lanes * V && (LANES >> p.groups_shift) * p.groups == LANES;
+  read_values<V>(logits, row_at, r, whole, kNegInf, l);
+  if (VALUED && p.bias != nullptr) {
+    read_values<V>(s_bias, 0, r, whole, 0.0f, b);
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    l[i] = i < r.held ? logit(r.first + i) : kNegInf;
-    if constexpr (VALUED) b[i] = i < r.held ? bias(r.first + i) : 0.0f;
+    for (int i = 0; i < V; ++i) b[i] = 0.0f;
   }
   float top = kNegInf;
   double total = 1.0;
@@ -393,7 +420,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
   for (int i = 0; i < V; ++i) {
     if constexpr (VALUED) {
       c[i] = l[i] == kNegInf ? kNegInf : sigmoid32(l[i]) + b[i];
-      bad |= l[i] != l[i] || c[i] != c[i];
+      bad |= c[i] != c[i];
     } else {
       c[i] = l[i];
       bad |= l[i] != l[i] || (!p.sigmoid && l[i] > 3.402823466e38f);
@@ -411,7 +438,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
   bad = row_bits<LANES>(__ballot(bad)) != 0;
 
   auto exact = [&](int i) {            // (VALUED) c[i] in 64 bits
-    return l[i] == kNegInf ? static_cast<double>(kNegInf) : sigmoid64(l[i]) + static_cast<double>(b[VALUED ? i : 0]);
+    return l[i] == kNegInf ? static_cast<double>(kNegInf) : sigmoid64(l[i]) + static_cast<double>(b[i]);
   };
   bool stays = true;
   if (p.topk_groups < p.groups) {
@@ -424,10 +451,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
       // a value is the sum of up to two c, each within kOff + 2^-24 |c| (and 2^-24
       // of itself): where the border is narrower than the errors of two, the
       // groups are told apart in 64 bits, by those c that may be their largest
-      float most = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) most = larger(most, c[i] == kNegInf ? 0.0f : fabsf(c[i]));
-      most = row_max<LANES>(most);
+      // (which are as large as those that seem to be, within the errors)
+      const float most = row_max<LANES>(larger(a == kNegInf ? 0.0f : fabsf(a), b2 == kNegInf ? 0.0f : fabsf(b2)));
       if (__ballot(gap <= 4.0f * kOff + 0x1p-20f * most) != 0) {
         const float from = (p.group_best == 2 ? b2 : a) - 2.0f * (kOff + 0x1p-22f * most);
         uint32_t left = 0;
@@ -447,13 +472,16 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
     }
   }
 
-  // keys: c's order in the high bits, the lower index first in the low ones; 0: none
-  const uint32_t mask = (1u << p.index_bits) - 1;
+  // keys: c's order in the high bits, the lower index first in the low ones; none:
+  // 0, or an infinity's, below kNoKey
+  constexpr uint32_t kNoKey = 0x00800000u;
+  const uint32_t mask = (1u << p.index_bits) - 1, keep = stays ? ~0u : 0u;
   uint32_t key[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    key[i] = !stays || c[i] == kNegInf ? 0u
-             : (ordered(c[i] + 0.0f) & ~mask) | (mask - static_cast<uint32_t>(r.first + i));   // (-0 is 0)
+  for (int i = 0; i < V; ++i) {
+    const float v = VALUED ? c[i] : c[i] + 0.0f;              // (-0 is 0)
+    key[i] = ((ordered(v) & ~mask) | (~static_cast<uint32_t>(r.first + i) & mask)) & keep;
+  }
   const int count = EXACT_KEYS ? p.topk : p.topk + 3;         // at most LANES
   // The next one is the largest key below the one before, and so the largest of
   // key - before modulo 2^32: keys that were taken give less than those that were
@@ -469,6 +497,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
     mine = r.lane == j ? m : mine;
     before = max(m, 1u);
   }
+  if (mine < kNoKey) mine = 0;
   const int expert = mine == 0 ? -1 : static_cast<int>(mask - (mine & mask));
   if constexpr (EXACT_KEYS) {
     if (r.lane < p.topk) chosen[r.lane] = expert;
