@@ -376,9 +376,9 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_exact_kernel(RoutePar
 // loads, each lane takes a run of neighbours from there (V of them, in registers
 // throughout), and each choice is V comparisons and one maximum over the row's
 // lanes.  Bound by instructions where there are many rows (8192 x 256 fp32,
-// sigmoid, bias, 8 experts of 4 of 8 groups: 11.2 us, its 9 MB are 1.8; bf16 logits alone
-// 6.5), by a launch and one row's chain of choices where there are few (1 x 256,
-// 8 of 256 bf16 3.6 us, with groups 5.9, an empty launch 2.7).  The same with
+// sigmoid, bias, 8 experts of 4 of 8 groups: 9.2 us, its 9 MB are 1.8; bf16 logits
+// alone 5.2), by a launch and one row's chain of choices where there are few (1 x
+// 256, 8 of 256 bf16 3.3 us, with groups 5.4, an empty launch 2.7).  The same with
 // 64-bit values throughout took 20 us.
 template <bool VALUED, int LANES, int V, int ACT>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p) {
@@ -569,8 +569,8 @@ hipError_t launch_route_as(const RouteParams& p, int act, hipStream_t stream) {
 }
 // 16 lanes a row where its values and its candidates fit them and there are rows
 // enough, else 64 (us, 64 / 16 lanes, 256 experts: sigmoid, bias and groups by
-// two, 1 row 6.0 / 9.2, 4096 rows 10.5 / 12.6, 8192 16.4 / 13.9; bf16 logits
-// alone, 1 row 3.6 / 5.5, 1024 4.2 / 5.9, 4096 6.1 / 6.0, 8192 9.1 / 6.5).
+// two, 1 row 5.4 / 6.5, 2048 rows 7.6 / 8.0, 4096 9.6 / 8.2; bf16 logits alone, 1
+// row 3.3 / 4.0, 1024 3.8 / 4.4, 4096 5.4 / 4.5).
 template <int KIND>
 hipError_t launch_route_of(const RouteParams& p, int candidates, int act, hipStream_t stream) {
   const int per_group = p.E / p.groups;
@@ -579,7 +579,7 @@ hipError_t launch_route_of(const RouteParams& p, int candidates, int act, hipStr
     return g == 0 || candidates > lanes ? kRouteMaxExperts : (per_group + g - 1) / g;
   };
   if (held(16) <= 4) return launch_route_as<KIND, 16, 4>(p, act, stream);
-  if (p.T > (KIND == 0 ? 2048 : 4096)) {
+  if (p.T > 2048) {
     if (held(16) <= 8) return launch_route_as<KIND, 16, 8>(p, act, stream);
     if (held(16) <= 16) return launch_route_as<KIND, 16, 16>(p, act, stream);
   }
