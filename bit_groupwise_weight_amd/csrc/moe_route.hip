@@ -376,7 +376,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_exact_kernel(RoutePar
 // loads, each lane takes a run of neighbours from there (V of them, in registers
 // throughout), and each choice is V comparisons and one maximum over the row's
 // lanes.  Bound by instructions where there are many rows (8192 x 256 fp32,
-// sigmoid, bias, 8 experts of 4 of 8 groups: 9.2 us, its 9 MB are 1.8; bf16 logits
+// sigmoid, bias, 8 experts of 4 of 8 groups: 9.1 us, its 9 MB are 1.8; bf16 logits
 // alone 5.2), by a launch and one row's chain of choices where there are few (1 x
 // 256, 8 of 256 bf16 3.3 us, with groups 5.4, an empty launch 2.7).  The same with
 // 64-bit values throughout took 20 us.
@@ -419,7 +419,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if constexpr (VALUED) {
-      c[i] = l[i] == kNegInf ? kNegInf : sigmoid32(l[i]) + b[i];
+      b[i] = l[i] == kNegInf ? kNegInf : b[i];                // (its score is 0)
+      c[i] = sigmoid32(l[i]) + b[i];
       bad |= c[i] != c[i];
     } else {
       c[i] = l[i];
@@ -569,7 +570,7 @@ hipError_t launch_route_as(const RouteParams& p, int act, hipStream_t stream) {
 }
 // 16 lanes a row where its values and its candidates fit them and there are rows
 // enough, else 64 (us, 64 / 16 lanes, 256 experts: sigmoid, bias and groups by
-// two, 1 row 5.4 / 6.5, 2048 rows 7.6 / 8.0, 4096 9.6 / 8.2; bf16 logits alone, 1
+// two, 1 row 5.4 / 6.5, 2048 rows 7.6 / 8.0, 4096 9.6 / 7.6; bf16 logits alone, 1
 // row 3.3 / 4.0, 1024 3.8 / 4.4, 4096 5.4 / 4.5).
 template <int KIND>
 hipError_t launch_route_of(const RouteParams& p, int candidates, int act, hipStream_t stream) {
