@@ -305,6 +305,7 @@ struct CombineParams {
 hipError_t launch_moe_combine(const CombineParams&, int act, hipStream_t);
 
 constexpr int kLoraMaxRank = 256;
+constexpr int kLoraMaxSplits = 8;
 struct LoraParams {
   const void* x;            // M x K, act, 16-byte aligned
   const void* a;            // L x rank x K, act, 16-byte aligned

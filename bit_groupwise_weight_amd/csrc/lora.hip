@@ -376,56 +376,46 @@ namespace {
 // t of a tile's BM rows in LDS, ready for the second product: rows of RANKS + 8
 // elements, an odd number of 16-byte pieces, so that the 16 rows of a read
 // start in different banks; 16-bit types have the hi halves of all rows and
-// then the lo halves.  from(r, k, v) gives eight ranks of row r.
+// then the lo halves.  put_t: eight ranks of row r.
 template <int ACT, int BM, int RANKS> struct TileT {
   typedef typename Act<ACT>::bits_t T;
   static constexpr int PITCH = RANKS + 8, HALVES = ACT == ACT_F32 ? 1 : 2;
   T v[HALVES][BM][PITCH];
   float unscale[BM];                   // fp16
 };
-template <int ACT, int BM, int RANKS, int THREADS, class From>
-__device__ __forceinline__ void prepare_t(const LoraParams& p, int rows, float scale, TileT<ACT, BM, RANKS>& t,
-                                          From from) {
-  constexpr int LANES = RANKS / 8;     // of a row, a power of two
-  const int k = threadIdx.x % LANES * 8;
-  for (int r = threadIdx.x / LANES; r < BM; r += THREADS / LANES) {
-    float v[8] = {};
-    if (k < p.rank && r < rows) {
-      from(r, k, v);
+template <int ACT, int BM, int RANKS>
+__device__ __forceinline__ void put_t(TileT<ACT, BM, RANKS>& t, int r, int k, float (&v)[8]) {
+  constexpr int LANES = RANKS / 8;     // of a row, a power of two, which call together
+  if constexpr (ACT == ACT_F32) {
+    f32x4_t* to = reinterpret_cast<f32x4_t*>(&t.v[0][r][k]);
+    to[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+    to[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+  } else {
+    if constexpr (ACT == ACT_F16) {
+      uint32_t top = 0;              // bits of the row's largest magnitude
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1)
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o)));
+      // 2^-e with e the exponent of the largest, within fp32's normal powers
+      const int e = min(max(static_cast<int>(top >> 23), 1), 253);
+      const float by = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      if (k == 0) t.unscale[r] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= by;
     }
-    if constexpr (ACT == ACT_F32) {
-      f32x4_t* to = reinterpret_cast<f32x4_t*>(&t.v[0][r][k]);
-      to[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-      to[1] = f32x4_t{v[4], v[5], v[6], v[7]};
-    } else {
-      if constexpr (ACT == ACT_F16) {
-        uint32_t top = 0;              // bits of the row's largest magnitude
+    uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1)
-          top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o)));
-        // 2^-e with e the exponent of the largest, within fp32's normal powers
-        const int e = min(max(static_cast<int>(top >> 23), 1), 253);
-        const float by = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        if (k == 0) t.unscale[r] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= by;
-      }
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        hi[i] = pack2<ACT>(v[2 * i], v[2 * i + 1]);
-        const float h0 = act_bits_to_float<ACT>(hi[i] & 0xffffu), h1 = act_bits_to_float<ACT>(hi[i] >> 16);
-        // (an infinity has no rest)
-        lo[i] = pack2<ACT>(fabsf(h0) <= 3.402823466e38f ? v[2 * i] - h0 : 0.0f,
-                           fabsf(h1) <= 3.402823466e38f ? v[2 * i + 1] - h1 : 0.0f);
-      }
-      *reinterpret_cast<u32v4_t*>(&t.v[0][r][k]) = u32v4_t{hi[0], hi[1], hi[2], hi[3]};
-      *reinterpret_cast<u32v4_t*>(&t.v[1][r][k]) = u32v4_t{lo[0], lo[1], lo[2], lo[3]};
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = pack2<ACT>(v[2 * i], v[2 * i + 1]);
+      const float h0 = act_bits_to_float<ACT>(hi[i] & 0xffffu), h1 = act_bits_to_float<ACT>(hi[i] >> 16);
+      // (an infinity has no rest)
+      lo[i] = pack2<ACT>(fabsf(h0) <= 3.402823466e38f ? v[2 * i] - h0 : 0.0f,
+                         fabsf(h1) <= 3.402823466e38f ? v[2 * i + 1] - h1 : 0.0f);
     }
+    *reinterpret_cast<u32v4_t*>(&t.v[0][r][k]) = u32v4_t{hi[0], hi[1], hi[2], hi[3]};
+    *reinterpret_cast<u32v4_t*>(&t.v[1][r][k]) = u32v4_t{lo[0], lo[1], lo[2], lo[3]};
   }
 }
 
@@ -577,11 +567,12 @@ __device__ __forceinline__ void copy_columns(const LoraParams& p, Outputs<ACT>& 
 // waves load together.  A step's B is asked for behind the products of the step
 // before and ahead of that one's stores, its base behind them.  Bound by memory:
 // base once in, y once out, past the caches (8192 rows, 14336 bf16 columns, rank
-// 64, 470 MB: 109 to 115 us, 4.1 to 4.3 TB/s, a copy of the base alone 89; 777
-// rows of 7 adapters, 5001 fp16 columns, rank 24: 11 us, most of it latencies that
-// follow each other: offsets, rows, t, base).  Measured and left: all first loads
-// at once (777 rows 10.9, 8192 rows 122), two row tiles a wave (8192 rows 110),
-// the base a step further ahead (110).
+// 64, 470 MB: 108 to 112 us, 4.2 to 4.4 TB/s, a copy of the base alone 89; 777
+// rows of 7 adapters, 5001 fp16 columns, rank 24: 10.5 us, most of it latencies
+// that follow each other: offsets, then t, B and rows, then base).  Measured and
+// left: the first base asked for with t (8192 rows 122), two row tiles a wave or
+// the base a step further ahead (no faster, more registers), t four planes at a
+// time behind the rows (777 rows 11.8, 8192 rows 113).
 template <int ACT, int WM, int WN, int RANKS>
 __global__ __launch_bounds__(64 * WM * WN) void lora_expand_kernel(LoraParams p, int cols) {
   constexpr int BM = 16 * WM, WAVES = WM * WN, COLS = 128 * WN;
@@ -599,33 +590,39 @@ __global__ __launch_bounds__(64 * WM * WN) void lora_expand_kernel(LoraParams p,
   const uint32_t b_at = lds_address(s_b);
   BLayout l = b_layout<ACT>(p, 0);
   if (!bare) load_b<ACT, COLS, WAVES>(p, rt.adapter, first, 0, l, b_at, wave);
-  for (int r = threadIdx.x; r < BM; r += 64 * WAVES) s_row[r] = rt.begin + r < rt.end ? row_of(p, rt.begin + r) : -1;
-  if (!bare) {
-    prepare_t<ACT, BM, RANKS, 64 * WAVES>(
-        p, rt.end - rt.begin, p.scales ? p.scales[rt.adapter] : 1.0f, s_t, [&](int r, int k, float (&v)[8]) {
-          // (four planes asked for at once)
-          const float* from = p.t + static_cast<size_t>(rt.begin + r) * p.rank_pad + k;
-          const size_t plane = static_cast<size_t>(p.T) * p.rank_pad;
-          for (int s0 = 0; s0 < p.splits; s0 += 4) {
-            f32x4_t a[4], b[4];
+  // t, eight ranks a lane, all planes of a turn asked for at once, and the rows
+  // behind those of the first
+  constexpr int LANES = RANKS / 8, AT_ONCE = 64 * WAVES / LANES;
+  const int k = threadIdx.x % LANES * 8;
+  const float scale = !bare && p.scales ? p.scales[rt.adapter] : 1.0f;
+  const bool one = threadIdx.x < BM && rt.begin + static_cast<int>(threadIdx.x) < rt.end;
+  int row = -1;
+  for (int r = threadIdx.x / LANES; r < BM; r += AT_ONCE) {
+    f32x4_t planes[kLoraMaxSplits][2];
+    if (!bare) {
+      const float* from = p.t + static_cast<size_t>(min(rt.begin + r, rt.end - 1)) * p.rank_pad + min(k, p.rank_pad - 8);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const f32x4_t* at = reinterpret_cast<const f32x4_t*>(from + min(s0 + q, p.splits - 1) * plane);
-              a[q] = at[0];
-              b[q] = at[1];
-            }
+      for (int s = 0; s < kLoraMaxSplits; ++s) {
+        if (s >= p.splits) break;
+        const f32x4_t* at = reinterpret_cast<const f32x4_t*>(from + static_cast<size_t>(s) * p.T * p.rank_pad);
+        planes[s][0] = at[0];
+        planes[s][1] = at[1];
+      }
+    }
+    if (one && r == static_cast<int>(threadIdx.x) / LANES) row = row_of(p, rt.begin + threadIdx.x);
+    if (bare) break;
+    float v[8] = {};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (s0 + q >= p.splits) break;
+    for (int s = 0; s < kLoraMaxSplits; ++s) {
+      if (s >= p.splits) break;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[i] += a[q][i];
-                v[4 + i] += b[q][i];
-              }
-            }
-          }
-        });
+      for (int i = 0; i < 8; ++i) v[i] += planes[s][i >> 2][i & 3];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k < p.rank && rt.begin + r < rt.end ? v[i] * scale : 0.0f;
+    put_t<ACT, BM, RANKS>(s_t, r, k, v);
   }
+  if (threadIdx.x < BM) s_row[threadIdx.x] = row;
   __syncthreads();
   Outputs<ACT> o;
   o.set_rows(s_row, 16 * wm);
@@ -716,11 +713,14 @@ __global__ __launch_bounds__(64 * WAVES) void lora_fused_kernel(LoraParams p, in
       *reinterpret_cast<f32x4_t*>(&s_f[c16][16 * wave + 4 * g]) = v;
     }
     __syncthreads();
-    prepare_t<ACT, 16, RANKS, 64 * WAVES>(p, rt.end - rt.begin, p.scales ? p.scales[rt.adapter] : 1.0f, s_t,
-                                          [&](int r, int k, float (&v)[8]) {
+    const int r = threadIdx.x / (RANKS / 8), k = threadIdx.x % (RANKS / 8) * 8;
+    if (r < 16) {
+      const float scale = p.scales ? p.scales[rt.adapter] : 1.0f;
+      float v[8];
 #pragma unroll
-                                            for (int i = 0; i < 8; ++i) v[i] = s_f[r][k + i];
-                                          });
+      for (int i = 0; i < 8; ++i) v[i] = k < p.rank && rt.begin + r < rt.end ? s_f[r][k + i] * scale : 0.0f;
+      put_t<ACT, 16, RANKS>(s_t, r, k, v);
+    }
     __syncthreads();
   }
   o.set_factors(s_t, 0);

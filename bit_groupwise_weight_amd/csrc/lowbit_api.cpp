@@ -796,7 +796,7 @@ LoraSchedule lora_schedule(int64_t T, int64_t L, int64_t rank, int64_t N, int64_
   // as many K ranges as there are CUs for: the second product adds their sums up
   // (8192 rows: 111 us with 4 of them, 125 with 16)
   const int64_t want = std::max<int64_t>(cus / (tiles(s.plan.shrink_rows) * ((rank + 63) / 64)), 1);
-  const int64_t splits = std::min<int64_t>({want, (units + 7) / 8, 16});
+  const int64_t splits = std::min<int64_t>({want, (units + 7) / 8, lowbit::kLoraMaxSplits});
   s.units_split = static_cast<int>((units + splits - 1) / splits);
   s.splits = static_cast<int>((units + s.units_split - 1) / s.units_split);
   // columns of a block: the most that leave each CU two blocks (64 rows of 32
