@@ -462,7 +462,10 @@ typedef enum lowbit_route_score {
  *   by the sum of the row's chosen s
  * Equal values: the lowest index first.  Without a bias (groups by group_best
  * 1) experts are ordered by their logits; otherwise c is computed in 64 bits,
- * so that rounding does not decide.  Weights are rounded once.
+ * so that rounding does not decide.  Weights are computed in 64 bits and
+ * rounded once, but for softmax's sum over all experts where weights without
+ * `renormalize` are divided by it: that is an fp32 sum unless there is a bias
+ * (or group_best 2).
  *
  *   logits   device, T x E row-major, dtype, aligned to its element size.
  *   bias     device, E fp32, or NULL.

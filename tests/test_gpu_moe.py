@@ -3,10 +3,10 @@ the experts' sum, and the run of them with the linears by expert.
 
 Tolerances, from the arithmetic (u = 2^-24, half a step of fp32):
   * route: experts are equal.  Weights are computed in 64 bits from the logits and rounded once: u of
-    themselves, taken as 1.01 u for the 64-bit steps (scale is the call's, an fp32 number).  Softmax without renormalization, without a
-    bias, divides by a sum of fp32 exps: an exp of x = l - top is off by x's rounding, u |x| e^x <=
-    0.37 u, and by its own, 2 u (a unit in the last place); up to 32 values of a lane and 6 steps
-    over the lanes add 38 u: 42 u with the rounding of the result;
+    themselves, taken as 1.01 u for the 64-bit steps (scale is the call's, an fp32 number).  Softmax
+    without renormalization, without a bias, divides by a sum of fp32 exps: an exp of x = l - top is
+    off by x's rounding, u |x| e^x <= 0.37 u, and by its own, 2 u (a unit in the last place); up to
+    32 values of a lane and 6 steps over the lanes add 38 u: 42 u with the rounding of the result;
   * combine: k products and k (+ 1) additions in fp32: (2 k + 1) u of the terms' magnitudes' sum,
     and half a step of the output type.
 """
