@@ -1251,9 +1251,7 @@ lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const f
   if (T < 0 || T > kMaxDim || R < 0 || R > kMaxDim)
     return fail(LOWBIT_ERR_INVALID_ARG, "rows T=%lld, R=%lld must be in 0..2^30", (long long)T, (long long)R);
   if (topk < 1 || topk > (int64_t(1) << 16)) return fail(LOWBIT_ERR_INVALID_ARG, "topk=%lld not in 1..2^16", (long long)topk);
-  if (N < 1 || N > kMaxDim || T * ((N + 255) / 256) >= kLaunchBlocks)
-    return fail(LOWBIT_ERR_INVALID_ARG, "N=%lld T=%lld: N must be in 1..2^30, T * ceil(N / 256) below 2^24",
-                (long long)N, (long long)T);
+  if (N < 1 || N > kMaxDim) return fail(LOWBIT_ERR_INVALID_ARG, "N=%lld not in 1..2^30", (long long)N);
   if (T == 0) return LOWBIT_OK;
   if (!position || !weights || !out || (R > 0 && !y))
     return fail(LOWBIT_ERR_INVALID_ARG, "NULL y, position, weights or out");

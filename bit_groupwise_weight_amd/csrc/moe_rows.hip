@@ -11,6 +11,8 @@
 // 4, ..., which then meet in order, and the residual last.
 #include "pieces.h"
 
+#include <algorithm>
+
 namespace lowbit {
 
 namespace {
@@ -401,9 +403,19 @@ namespace {
 
 template <int ACT, int LX>
 void launch_combine_rows(const CombineParams& p, int pieces, hipStream_t stream) {
+  typedef typename Act<ACT>::bits_t T;
   const int runs = (pieces + LX - 1) / LX;
-  const int64_t blocks = (p.T + kCombineThreads / LX - 1) / (kCombineThreads / LX) * runs;
-  moe_combine_kernel<ACT, LX><<<static_cast<unsigned>(blocks), kCombineThreads, 0, stream>>>(p, runs);
+  constexpr int ROWS = kCombineThreads / LX;
+  const int64_t most = kF8MaxThreads / kCombineThreads / runs * ROWS;        // of a launch
+  for (int64_t t = 0; t < p.T; t += most) {
+    CombineParams q = p;
+    q.T = std::min(p.T - t, most);
+    q.position += t * p.topk;
+    q.weights += t * p.topk;
+    q.out = static_cast<T*>(p.out) + t * p.N;
+    if (p.residual) q.residual = static_cast<const T*>(p.residual) + t * p.N;
+    moe_combine_kernel<ACT, LX><<<static_cast<unsigned>((q.T + ROWS - 1) / ROWS * runs), kCombineThreads, 0, stream>>>(q, runs);
+  }
 }
 template <int ACT>
 void launch_combine_as(const CombineParams& p, hipStream_t stream) {

@@ -736,7 +736,12 @@ class F8Experts(_F8Module):
         slots = torch.ops.lowbit.linear_f8_grouped(aq, ascale, None, offsets, self.down, self.down_scale,
                                                    None, self.dtype)
         # (rows of no expert are undefined; their slots have position -1 and add nothing)
-        return torch.ops.lowbit.moe_combine(slots, position, weights.reshape(T, k).float(), None)
+        weights = weights.reshape(T, k).float()
+        if torch.is_grad_enabled() and weights.requires_grad:
+            # the same sum from torch's operations, which know the gradient of the routing weights
+            out = slots[position.clamp(min=0).long()].float() * weights.unsqueeze(-1)
+            return torch.where((position >= 0).unsqueeze(-1), out, 0.0).sum(1).to(self.dtype)
+        return torch.ops.lowbit.moe_combine(slots, position, weights, None)
 
     def extra_repr(self) -> str:
         return (f"num_experts={self.num_experts}, hidden={self.hidden}, intermediate={self.intermediate}, "

@@ -526,7 +526,7 @@ size_t lowbit_group_rows_workspace_bytes(int64_t T, int64_t topk, int64_t E);
  *   out      device, T x N, dtype.  Overwritten; may be residual itself, must
  *            not overlap an input otherwise.
  *   T >= 0 (0 is a no-op; at most 2^30), 0 <= R <= 2^30, topk 1 .. 2^16,
- *            N 1 .. 2^30, T * ceil(N / 256) < 2^24.
+ *            N 1 .. 2^30.
  *   Every array is aligned to its element size; rows of whole 16-byte pieces
  *   on 16-byte aligned arrays are the fast case. */
 lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const float* weights,

@@ -410,6 +410,22 @@ def test_combine_rows_past_4_gib():
     assert (out[0] == 3).all() and (out[1] == 4).all() and torch.isnan(out[2]).all()
 
 
+def test_combine_more_rows_than_a_launch_has_blocks():
+    T, N, R = (1 << 24) + 70, 1032, 50                   # (a block a row at this width, 34 GB of sums)
+    y = torch.randn(R, N, device=DEV).bfloat16()
+    at = torch.arange(T, device=DEV)
+    position, w = (at % R).int().unsqueeze(1), ((at % 7) / 8).unsqueeze(1)
+    residual = torch.zeros(1, N, dtype=torch.bfloat16, device=DEV).expand(T, N).contiguous()
+    residual[-1] = 64.0
+    out = lb.lowbit_moe_combine(y, position, w, residual=residual, out=residual)
+    for t in (*range(0, T - (1 << 20), 1 << 20), (1 << 24) - (1 << 19)):
+        s = slice(t, min(t + (1 << 20), T))
+        want = y[position[s, 0].long()].float() * w[s]   # (w has three bits: the product is exact)
+        if s.stop == T:
+            want[-1] += 64.0
+        assert torch.equal(out[s], want.bfloat16())
+
+
 # ------------------------------------------------------- the run together --
 
 def moe_calls(t):
@@ -543,6 +559,30 @@ def test_modules_and_ops_match_the_calls():
     assert torch.equal(out, m(x, e.to(torch.uint8), w))
     fn = torch.compile(lambda l, x: m(x, *r(l)), fullgraph=True, backend="aot_eager")
     assert torch.equal(fn(logits, x), out)
+
+
+def test_experts_keep_the_gradient_of_the_routing_weights():
+    """As a router that is trained beside frozen experts needs it.  The sum is linear in the weights:
+    its gradient is the product of the output's with each slot's row, 64 products summed in fp32."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    m = lnn.F8Experts(6, 64, 48, dtype=torch.float32, device=DEV)
+    m.set_weight(torch.randn(6, 96, 64, generator=g, device=DEV) * 0.1, torch.randn(6, 64, 48, generator=g, device=DEV) * 0.1)
+    x = torch.randn(11, 64, generator=g, device=DEV)
+    e = torch.stack([torch.randperm(6, generator=g, device=DEV)[:3] for _ in range(11)])
+    e[2, 1] = e[5, 0] = -1
+    w = torch.rand(11, 3, generator=g, device=DEV)
+    up = torch.randn(11, 64, generator=g, device=DEV)
+    wg = w.clone().requires_grad_()
+    out = m(x, e, wg)
+    assert torch.equal(out.detach(), m(x, e, w))
+    (out * up).sum().backward()
+    for j in range(3):
+        one = torch.zeros_like(w)
+        one[:, j] = 1.0
+        terms = (up * m(x, e, one)).double()             # slot j's rows, exactly
+        assert torch.all((wg.grad[:, j] - terms.sum(-1)).abs() <= 2 * 65 * U * terms.abs().sum(-1))
+    assert wg.grad[2, 1] == 0 and wg.grad[5, 0] == 0
 
 
 def test_results_carry_no_gradient():

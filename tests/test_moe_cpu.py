@@ -53,7 +53,7 @@ def test_group_rows_validation(lowbit_lib, kw, status):
 @pytest.mark.parametrize("kw, status", [
     (dict(dt=3), UNSUPPORTED), (dict(T=-1), INVALID), (dict(R=-1), INVALID), (dict(k=0), INVALID),
     (dict(k=(1 << 16) + 1), INVALID), (dict(N=0), INVALID), (dict(N=(1 << 30) + 1), INVALID),
-    (dict(T=1 << 20, N=4096), INVALID), (dict(y=None), INVALID), (dict(pos=None), INVALID), (dict(w=None), INVALID),
+    (dict(T=(1 << 30) + 1), INVALID), (dict(y=None), INVALID), (dict(pos=None), INVALID), (dict(w=None), INVALID),
     (dict(out=None), INVALID), (dict(y=A + 1), MISALIGNED), (dict(res=A + 1), MISALIGNED), (dict(out=A + 1), MISALIGNED),
     (dict(pos=A + 2), MISALIGNED), (dict(w=A + 2), MISALIGNED), (dict(T=0), OK),
     (dict(T=0, y=None, pos=None, w=None, out=None), OK),
