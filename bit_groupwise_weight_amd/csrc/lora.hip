@@ -724,17 +724,27 @@ __global__ __launch_bounds__(64 * WAVES) void lora_fused_kernel(LoraParams p, in
     __syncthreads();
   }
   o.set_factors(s_t, 0);
+  // (B of the steps takes turns between its own place and the ring, which is free)
+  static_assert(B <= RING, "a step's B fits a wave's ring");
+  const uint8_t* b_now = s_b[wave];
+  const uint8_t* b_next = s_ring[wave];
   for (int n0 = first; n0 < last; n0 += 128 * WAVES) {
-    if (n0 != first) {
-      load_b<ACT, 128, 1>(p, rt.adapter, n0, 0, l, b_at, 0);
-      o.template load<false>(p, n0);
-    }
+    const int next = n0 + 128 * WAVES;
+    Outputs<ACT> behind = o;
     wait_loads<0>();
+    if (next < last) {
+      load_b<ACT, 128, 1>(p, rt.adapter, next, 0, l, lds_address(b_next), 0);
+      behind.template load<false>(p, next);
+    }
     f32x4_t acc[8];
     clear(acc);
-    multiply_pass<ACT, 16, RANKS>(p, s_t, 0, s_b[wave], l, 0, 0, acc);
+    multiply_pass<ACT, 16, RANKS>(p, s_t, 0, b_now, l, 0, 0, acc);
     o.template store<false>(p, n0, acc);
     wait_lds();
+    o = behind;
+    const uint8_t* was = b_now;
+    b_now = b_next;
+    b_next = was;
   }
 }
 
