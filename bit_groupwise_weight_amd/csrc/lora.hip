@@ -667,7 +667,9 @@ __global__ __launch_bounds__(64 * WM * WN) void lora_expand_kernel(LoraParams p,
 // columns at a time and loads their B alone, the first of it ahead of the first
 // product.  Bound by latencies and by A, which every block of a tile reads whole
 // (1 row of rank 16, 4096 -> 4096: 6.6 us, an empty launch 2.7; 64 rows of 32
-// adapters of rank 16, 4096 -> 14336 bf16, 20 MB: 10.4 us; two launches 14.6).
+// adapters of rank 16, 4096 -> 14336 bf16, 20 MB: 10.2 us; two launches 14.6, without
+// the next step's B and base ahead of the products 0.7 more).  Measured and left: a
+// fourth stage, x's rows past the tile not loaded (neither is faster).
 template <int ACT, int NT, int WAVES, int STAGES>
 __global__ __launch_bounds__(64 * WAVES) void lora_fused_kernel(LoraParams p, int cols) {
   constexpr int RANKS = 32, RING = STAGES * (1 + NT) * kUnitBytes, B = 128 * 16 * NT * Act<ACT>::bytes;
