@@ -768,21 +768,27 @@ LoraSchedule lora_schedule(int64_t T, int64_t L, int64_t rank, int64_t N, int64_
   // tiles that hold rows: those of all rows, and a part of one for each adapter
   auto tiles = [&](int64_t rows) { return (T + rows - 1) / rows + std::min(T, L) / 2; };
 
-  // One launch for few rows.  Each block reads its tile's A and x whole (some 125
-  // KB a us, beside 4 us of latencies), and takes `step` columns at a time (2.5
-  // us more for a second step, up to 3 us more where every CU has a block); two
-  // launches are 11 to 12 us.  Measured, one / two launches, us, bf16: 1 row of
-  // rank 16, 4096 -> 4096 6.6 / 9.5, 14336 -> 4096 11.2 / 11.6, rank 32 7.5 /
-  // 11.2; 64 rows of 32 adapters of rank 16, 4096 -> 14336 10.5 / 14.6, 14336 ->
-  // 4096 15.1 / 14.6, of rank 32, 4096 -> 14336 24 / 16; 512 rows of 32 adapters,
-  // 4096 -> 14336 25 / 21.
+  // One launch for few rows, whose blocks each make their tile's t: latencies, then
+  // a wave's units of K one after another (8 waves share them up to rank 16, 4
+  // beyond), up to 4.5 us more where every CU has a block, and a second turn of
+  // `step` columns.  Two launches are latencies and the bytes.  The estimates, fitted
+  // to both sides of 90 random shapes (1 to 200 rows, K 512 to 14336, N 256 to
+  // 14336), cost 0.5 % over the better of the two on them.  us, one / two launches:
+  // 1 row of rank 16, 4096 -> 4096 bf16 6.7 / 9.5; 4 rows of 1024 -> 256, rank 32 5.5
+  // / 9.1; 64 rows of 32 adapters of rank 16, 4096 -> 14336 10.2 / 14.6; rank 32,
+  // 200 rows of 16, 8192 -> 4096 16.2 / 10.5; 1 row, 14336 -> 1024 18 / 9.7; fp32,
+  // 16 rows of rank 24, 512 -> 256 8.3 / 10.1, 32 rows, 5120 -> 1024 24 / 14.
+  const bool fp32 = dtype == LOWBIT_F32;
   const int64_t step = rank <= 16 ? 1024 : 512, steps = (N + step - 1) / step;
   const int64_t across = std::max<int64_t>(1, std::min(steps, cus / tiles(16)));
   const int64_t turns = (steps + across - 1) / across;
-  const double one_us = 4.0 + static_cast<double>((rank + 16) * units * 128) / 125e3 +
-                        2.5 * static_cast<double>(turns - 1) +
-                        3.0 * static_cast<double>(tiles(16) * across) / static_cast<double>(cus);
-  if (each < 32 && rank <= 32 && turns <= 2 && tiles(16) <= cus / 2 && one_us < 11.5) {
+  const double one_us = (fp32 ? 7.3 : 4.6) + (fp32 ? 0.42 : 0.24) * static_cast<double>(units) / (rank <= 16 ? 8 : 4) +
+                        4.5 * static_cast<double>(tiles(16) * across) / static_cast<double>(cus) +
+                        static_cast<double>(turns - 1);
+  const double bytes = static_cast<double>(std::min(T, L) * rank * (K + N) + T * (2 * N + K)) *
+                       static_cast<double>(dtype_bytes(dtype));
+  const double two_us = (fp32 ? 10.0 : 8.7) + bytes / 6e6;
+  if (each < 32 && rank <= 32 && turns <= 2 && tiles(16) <= cus / 2 && one_us < two_us) {
     s.plan.fused = true;
     s.plan.cols = static_cast<int>(turns * step);
     return s;

@@ -99,9 +99,10 @@ def test_lora(M, L, rank, K, N, dtype):
 
 SCHEDULES = [  # one launch: one and two turns of columns, ranks to 32
              (16, 1, 16, 272, 2600), (200, 40, 16, 2064, 2100), (300, 80, 8, 144, 5200), (9, 3, 32, 4112, 700),
-             (90, 30, 24, 528, 3300),
+             (90, 30, 24, 528, 3300), (60, 30, 32, 144, 9000),
              # two launches of 16 rows a tile: long K in ranges, ranks past a pass
              (40, 20, 64, 4112, 300), (20, 20, 128, 2064, 520), (50, 2, 256, 1040, 129), (17, 17, 96, 16400, 40),
+             (33, 20, 16, 16400, 40),
              # of 64 and of 128, every number of rank tiles, whole tiles and parts, many turns of columns
              (128, 1, 16, 528, 1300), (192, 2, 32, 144, 2600), (256, 4, 72, 1040, 520), (600, 2, 16, 1040, 264),
              (600, 2, 24, 272, 1032), (1024, 2, 64, 2064, 520), (700, 2, 256, 272, 272), (900, 3, 8, 16, 5),
