@@ -103,6 +103,8 @@ SCHEDULES = [  # one launch: one and two turns of columns, ranks to 32
              # two launches of 16 rows a tile: long K in ranges, ranks past a pass
              (40, 20, 64, 4112, 300), (20, 20, 128, 2064, 520), (50, 2, 256, 1040, 129), (17, 17, 96, 16400, 40),
              (33, 20, 16, 16400, 40),
+             # more adapters than a wave looks through at a time
+             (150, 300, 16, 272, 200), (400, 700, 64, 144, 264), (70, 63, 8, 48, 24), (90, 255, 8, 16, 40),
              # of 64 and of 128, every number of rank tiles, whole tiles and parts, many turns of columns
              (128, 1, 16, 528, 1300), (192, 2, 32, 144, 2600), (256, 4, 72, 1040, 520), (600, 2, 16, 1040, 264),
              (600, 2, 24, 272, 1032), (1024, 2, 64, 2064, 520), (700, 2, 256, 272, 272), (900, 3, 8, 16, 5),
@@ -179,10 +181,11 @@ def test_lora_rows_named_in_part_and_out_of_range():
     assert (y[rest] == 9).all()
 
 
-@pytest.mark.parametrize("offsets", [[-5, 100, 200], [3, 1, 2], [0, 2 ** 31 - 1, -2 ** 31], [9, 9, 9]])
+@pytest.mark.parametrize("offsets", [[-5, 100, 200], [3, 1, 2], [0, 2 ** 31 - 1, -2 ** 31], [9, 9, 9],
+                                     [20, 0] * 100, [-2 ** 31, 2 ** 31 - 1, 7] * 100])
 def test_lora_bad_offsets_stay_inside(offsets):
     """Unspecified values in y, its neighbours untouched."""
-    t = inputs(7, 20, 2, 8, 32, 40, "bf16")
+    t = inputs(7, 20, len(offsets) - 1, 8, 32, 40, "bf16")
     flat = torch.full((22 * 40,), 5.0, dtype=torch.bfloat16, device=DEV)
     call(t, rows=torch.arange(20, dtype=torch.int32, device=DEV),
          offsets=torch.tensor(offsets, dtype=torch.int32, device=DEV), y=flat[40:21 * 40].view(20, 40))
