@@ -454,6 +454,17 @@ def _lora_fake(x, a, b, scales, rows, offsets, base):
 
 # --------------------------------------------------------------- module --
 
+def _derived(t: torch.Tensor) -> bool:
+    """Whether a derivative of t may be asked for: it requires one, carries a forward-mode tangent, or
+    a transform of torch.func (a derivative of either mode, vmap) is at work, under which only torch's
+    operations are differentiated and batched.  (torch has no public query for the last.)"""
+    if torch._C._are_functorch_transforms_active():
+        return True
+    if torch.is_grad_enabled() and t.requires_grad:
+        return True
+    return torch.autograd.forward_ad.unpack_dual(t).tangent is not None
+
+
 class LowbitLinear(torch.nn.Module):
     """``nn.Linear`` with a groupwise b-bit weight: w = s * q + z per group.
 
@@ -737,8 +748,8 @@ class F8Experts(_F8Module):
                                                    None, self.dtype)
         # (rows of no expert are undefined; their slots have position -1 and add nothing)
         weights = weights.reshape(T, k).float()
-        if torch.is_grad_enabled() and weights.requires_grad:
-            # the same sum from torch's operations, which know the gradient of the routing weights
+        if _derived(weights):
+            # the same sum from torch's operations, which know the derivatives of the routing weights
             out = slots[position.clamp(min=0).long()].float() * weights.unsqueeze(-1)
             return torch.where((position >= 0).unsqueeze(-1), out, 0.0).sum(1).to(self.dtype)
         return torch.ops.lowbit.moe_combine(slots, position, weights, None)
