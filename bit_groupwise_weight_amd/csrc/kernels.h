@@ -269,7 +269,8 @@ struct RouteParams {
   int sigmoid;            // 0: softmax
   int groups;             // divides E
   int groups_shift;       // log2(groups), rounded up
-  int topk_groups, group_best;
+  int topk_groups;
+  int group_best;         // 1 or 2; 1 where there is one group
   int index_bits;         // of an expert's index
   int renormalize;
   float scale;

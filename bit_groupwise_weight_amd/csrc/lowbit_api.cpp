@@ -1204,7 +1204,7 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
   while ((int64_t{1} << p.groups_shift) < groups) ++p.groups_shift;
   while ((int64_t{1} << p.index_bits) < E) ++p.index_bits;
   p.topk_groups = static_cast<int>(topk_groups);
-  p.group_best = group_best;
+  p.group_best = groups > 1 ? static_cast<int>(group_best) : 1;   // (one group has no value to compare)
   p.renormalize = renormalize != 0;
   p.scale = scale;
   const hipError_t e = lowbit::launch_moe_route(p, act_kind(dtype), static_cast<hipStream_t>(stream));

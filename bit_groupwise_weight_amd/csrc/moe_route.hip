@@ -593,7 +593,7 @@ hipError_t launch_route_of(const RouteParams& p, int candidates, int act, hipStr
 }  // namespace
 
 hipError_t launch_moe_route(const RouteParams& p, int act, hipStream_t stream) {
-  const bool valued = p.bias != nullptr || (p.groups > 1 && p.group_best == 2);
+  const bool valued = p.bias != nullptr || p.group_best == 2;      // (as the exact kernel has it)
   const bool exact_keys = !valued && act != ACT_F32;
   const int candidates = exact_keys ? p.topk : p.topk + 3;
   if ((valued && !p.sigmoid) || candidates > 64) return launch_route_of<2>(p, 0, act, stream);

@@ -460,9 +460,10 @@ typedef enum lowbit_route_score {
  *   experts[t] = the topk experts of largest c among those, in that order
  *   weights[t, j] = scale * s_e, e = experts[t, j], with `renormalize` divided
  *   by the sum of the row's chosen s
- * Equal values: the lowest index first.  Without a bias (groups by group_best
- * 1) experts are ordered by their logits; otherwise c is computed in 64 bits,
- * so that rounding does not decide.  Weights are computed in 64 bits and
+ * Equal values: the lowest index first.  Without a bias and with group_best 1
+ * or a single group (whose value nothing is compared with) experts are ordered
+ * by their logits; otherwise c is computed in 64 bits, so that rounding does
+ * not decide.  Weights are computed in 64 bits and
  * rounded once, but for softmax's sum over all experts where weights without
  * `renormalize` are divided by it: that is an fp32 sum unless there is a bias
  * (or group_best 2).

@@ -58,3 +58,28 @@ def test_experts_forward_and_reverse_derivatives_agree():
     assert rev.abs().max() > 0 and torch.all((fwd - rev).abs() <= 8 * U * rev.abs())
     ws = torch.stack([w, t])
     assert torch.equal(torch.vmap(lambda v: m(x, e, v))(ws), torch.stack([m(x, e, w), m(x, e, t)]))
+
+
+# ------------------------------------------------------------------- route --
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("topk", [61, 62, 63, 64])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_one_group_by_two_is_ordered_by_its_logits(sigmoid, topk, dtype):
+    """Scores that no number of bits tells apart (sigmoids of 1, softmax terms of 0), one group valued
+    by its two largest, so many experts that a kernel of its own takes them: the logits' order."""
+    E = 64
+    step = torch.arange(E).float()
+    logits = torch.stack([40 + 0.5 * step, 100 - step, -1200 + 4 * step, -900 - 8 * ((step * 37) % E),
+                          (step * 29) % E * 16 - 1000])
+    logits[3, 5] = 0.0                                   # the others vanish beside it
+    logits = logits.to(DT[dtype])
+    e, w = lb.lowbit_moe_route(logits.to(DEV), topk, score=lb.ROUTE_SIGMOID if sigmoid else lb.ROUTE_SOFTMAX,
+                               groups=1, topk_groups=1, group_best=2)
+    assert torch.equal(e.cpu().long(), logits.float().sort(dim=1, descending=True, stable=True).indices[:, :topk])
+    ref_e, ref_w = o.route(f64(logits), topk, sigmoid=sigmoid, groups=1, topk_groups=1, best=2)
+    assert np.array_equal(e.cpu().numpy(), ref_e)
+    # (64-bit weights, rounded once)
+    assert np.all(np.abs(f64(w) - ref_w) <= 1.01 * U * ref_w + 2.0 ** -149)
+    one = lb.lowbit_moe_route(logits.to(DEV), topk, score=lb.ROUTE_SIGMOID if sigmoid else lb.ROUTE_SOFTMAX)
+    assert torch.equal(e, one[0]) and torch.equal(w, one[1])
