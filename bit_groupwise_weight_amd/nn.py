@@ -750,8 +750,10 @@ class F8Experts(_F8Module):
         weights = weights.reshape(T, k).float()
         if _derived(weights):
             # the same sum from torch's operations, which know the derivatives of the routing weights
-            out = slots[position.clamp(min=0).long()].float() * weights.unsqueeze(-1)
-            return torch.where((position >= 0).unsqueeze(-1), out, 0.0).sum(1).to(self.dtype)
+            # (both factors of a slot without an expert are 0 before they meet, for the derivatives' sake)
+            used = position >= 0
+            out = torch.where(used.unsqueeze(-1), slots[position.clamp(min=0).long()].float(), 0.0)
+            return (out * torch.where(used, weights, 0.0).unsqueeze(-1)).sum(1).to(self.dtype)
         return torch.ops.lowbit.moe_combine(slots, position, weights, None)
 
     def extra_repr(self) -> str:

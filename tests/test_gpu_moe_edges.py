@@ -60,6 +60,26 @@ def test_experts_forward_and_reverse_derivatives_agree():
     assert torch.equal(torch.vmap(lambda v: m(x, e, v))(ws), torch.stack([m(x, e, w), m(x, e, t)]))
 
 
+def test_experts_gradient_of_padded_slots_is_zero():
+    """Beside a token that is not a number, whose rows come first, and where no slot has an expert."""
+    m, n, g = experts_of(22)
+    x, w, up = n(9, 64), n(9, 3), n(9, 64)
+    e = torch.stack([torch.randperm(6, generator=g, device=DEV)[:3] for _ in range(9)])
+    e[0] = torch.tensor([0, 1, 2], device=DEV)
+    e[4, 0] = e[4, 2] = e[7, 1] = -1
+
+    def grad(x, e, w):
+        v = w.clone().requires_grad_()
+        (m(x, e, v)[1:] * up[1:]).sum().backward()
+        return v.grad
+
+    want = grad(x, e, w)
+    x[0] = NAN
+    got = grad(x, e, w)
+    assert torch.equal(got[1:], want[1:]) and got[4, 0] == 0 and got[4, 2] == 0 and got[7, 1] == 0
+    assert (grad(x, torch.full_like(e, -1), torch.full_like(w, NAN)) == 0).all()
+
+
 # ------------------------------------------------------------------- route --
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])

@@ -143,3 +143,57 @@ def test_compiled_experts_keep_their_derivatives(calls):
         want = fn(w, t)
         got = torch.compile(fn, fullgraph=True, backend="aot_eager")(w, t)
         assert want.abs().max() > 1 and (got - want).abs().max() <= 1e-5 * want.abs().max()
+
+
+# ----------------------------------------------------------- padded slots --
+
+def test_experts_gradient_beside_rows_that_are_not_finite(calls):
+    """A token that is not finite, whose rows come first, leaves the gradients of other tokens' padded
+    slots alone: they are 0, and the other weights' are what they are without it."""
+    m, (x, e, w, up) = experts_of(), batch()
+    up = torch.randn(6, 32, generator=torch.Generator().manual_seed(3))
+    e[0] = torch.tensor([0, 1, 2])                      # row 0 of the experts' is token 0's
+    e[2, 1], e[4, 0], e[4, 2] = -1, 5, -1
+
+    def grad(x):
+        v = w.clone().requires_grad_()
+        out = m(x, e, v)
+        (out * torch.where(torch.arange(6)[:, None] > 0, up, 0.0))[1:].sum().backward()
+        return out.detach(), v.grad
+
+    out, want = grad(x)
+    for bad in (NAN, INF):
+        y = x.clone()
+        y[0] = bad
+        got_out, got = grad(y)
+        assert torch.equal(got_out[1:], out[1:])
+        assert torch.equal(got[1:], want[1:])
+        assert got[2, 1] == 0 and got[4, 0] == 0 and got[4, 2] == 0
+    assert want[1].abs().min() > 0
+
+
+def test_experts_gradient_where_no_slot_has_an_expert(calls):
+    """Nothing is written for any row then: sums and gradients are 0, whatever the weights hold."""
+    m, (x, e, w, _) = experts_of(), batch()
+    e[:] = -1
+    for fill in (1.0, NAN, INF):
+        v = torch.full_like(w, fill).requires_grad_()
+        out = m(x, e, v)
+        assert (out == 0).all() and torch.equal(out.detach(), m(x, e, v.detach()))
+        out.sum().backward()
+        assert (v.grad == 0).all()
+
+
+@pytest.mark.parametrize("weight", [NAN, INF, -INF])
+def test_experts_padded_slots_of_any_weight_add_nothing(calls, weight):
+    m, (x, e, w, t) = experts_of(), batch()
+    e[3, 2] = -1
+    w[3, 2] = weight
+    plain = m(x, e, w)
+    assert torch.isfinite(plain).all()
+    v = w.clone().requires_grad_()
+    out = m(x, e, v)
+    assert torch.allclose(out, plain, rtol=1e-5, atol=1e-5)
+    out.sum().backward()
+    assert torch.isfinite(v.grad).all() and v.grad[3, 2] == 0
+    assert torch.isfinite(torch.func.jvp(lambda u: m(x, e, u), (w,), (t,))[1]).all()
