@@ -425,14 +425,15 @@ __device__ __forceinline__ void put_t(TileT<ACT, BM, RANKS>& t, int r, int k, fl
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= by;
     }
+    constexpr float kMost = ACT == ACT_F16 ? 65504.0f : 0x1.fep127f;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      hi[i] = pack2<ACT>(v[2 * i], v[2 * i + 1]);
-      const float h0 = act_bits_to_float<ACT>(hi[i] & 0xffffu), h1 = act_bits_to_float<ACT>(hi[i] >> 16);
-      // (an infinity has no rest)
-      lo[i] = pack2<ACT>(fabsf(h0) <= 3.402823466e38f ? v[2 * i] - h0 : 0.0f,
-                         fabsf(h1) <= 3.402823466e38f ? v[2 * i + 1] - h1 : 0.0f);
+      // (hi is finite; an infinity and what is no number are lo's)
+      hi[i] = pack2<ACT>(__builtin_amdgcn_fmed3f(v[2 * i], -kMost, kMost),
+                         __builtin_amdgcn_fmed3f(v[2 * i + 1], -kMost, kMost));
+      lo[i] = pack2<ACT>(v[2 * i] - act_bits_to_float<ACT>(hi[i] & 0xffffu),
+                         v[2 * i + 1] - act_bits_to_float<ACT>(hi[i] >> 16));
     }
     *reinterpret_cast<u32v4_t*>(&t.v[0][r][k]) = u32v4_t{hi[0], hi[1], hi[2], hi[3]};
     *reinterpret_cast<u32v4_t*>(&t.v[1][r][k]) = u32v4_t{lo[0], lo[1], lo[2], lo[3]};
