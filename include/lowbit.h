@@ -568,7 +568,8 @@ lowbit_status lowbit_moe_combine(const void* y, const int32_t* position, const f
  *
  * Sums are fp32.  x . a^T stays fp32, and enters the second product as a sum
  * of two numbers of dtype (2^-16 of it in bf16, less in fp16; fp32: as it is);
- * y is rounded once, to nearest even. */
+ * y is rounded once, to nearest even.  Infinities and NaN in x, a, b and base
+ * reach y as the formula has them, and stay in their rows and columns. */
 lowbit_status lowbit_lora(const void* x, const void* a, const void* b, const float* scales,
                           const int32_t* rows, const int32_t* offsets, const void* base, void* y,
                           lowbit_dtype dtype, int64_t M, int64_t T, int64_t L, int64_t rank, int64_t N,

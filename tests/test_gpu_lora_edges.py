@@ -17,9 +17,96 @@ def _lib(lowbit_lib):
     return lowbit_lib
 
 
+# One launch (ranks to 32, one and two steps of columns) and two, ranks of one pass and of several.
+INF_SHAPES = [(1, 1, 8, 16, 40), (40, 20, 16, 272, 300), (60, 30, 32, 144, 1200), (70, 2, 16, 528, 264), (300, 2, 64, 96, 200),
+              (90, 2, 136, 80, 136), (33, 2, 256, 64, 150)]
+
+
 def reference(t):
     with np.errstate(all="ignore"):
         return o.lora(f64(t["x"]), f64(t["a"]), f64(t["b"]), f64(t["scales"]), t["ids"].numpy(), f64(t["base"]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M, L, rank, K, N", INF_SHAPES)
+def test_lora_infinite_elements_of_b(M, L, rank, K, N, dtype):
+    """One infinite element in every third column: +-inf there by the sign of its t, whatever t's size;
+    two of them: +-inf or not a number, as their signs are; the other columns as without any."""
+    t = inputs(M + rank, M, L, rank, K, N, dtype, ids=torch.arange(M) % L)
+    # x . a over a span of sizes: ranks of one row from 1 down to 2^-30 of its largest
+    fade = torch.linspace(0, -30 if dtype != "f16" else -8, rank).round()
+    t["a"] = (t["a"].float() * torch.exp2(fade)[None, :, None]).to(DT[dtype])
+    want = call(t)
+    g = torch.Generator().manual_seed(rank)
+    cols = torch.arange(0, N, 3)
+    at = torch.randint(0, rank, (len(cols),), generator=g)
+    sign = torch.randint(0, 2, (len(cols),), generator=g).float() * 2 - 1
+    t["b"] = t["b"].clone()
+    t["b"][:, cols, at] = (sign * INF).to(DT[dtype])
+    two = cols[1::4]
+    t["b"][:, two, (at[1::4] + 1) % rank] = INF
+    y = call(t)
+    x, a = f64(t["x"]), f64(t["a"])
+    ts = np.stack([a[l] @ x[m] for m, l in enumerate(t["ids"].tolist())])           # [M, rank]
+    # (no t is so near 0 that its sign is in doubt: sums of K products in fp32)
+    size = np.stack([np.abs(a[l]) @ np.abs(x[m]) for m, l in enumerate(t["ids"].tolist())])
+    sure = (np.abs(ts) > (2 * (K / 32 + 112) + 1) * 2.0 ** -24 * size).all(1)
+    assert sure.mean() > 0.9
+    ref = reference(t)[0]
+    got = f64(y)
+    assert np.isinf(ref[:, cols]).sum() > 0 or M == 1
+    assert np.array_equal(np.isnan(got)[sure], np.isnan(ref)[sure])
+    assert np.array_equal(np.isposinf(got)[sure], np.isposinf(ref)[sure])
+    assert np.array_equal(np.isneginf(got)[sure], np.isneginf(ref)[sure])
+    rest = [n for n in range(N) if n % 3]
+    assert torch.equal(y[:, rest], want[:, rest])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M, L, rank, K, N", INF_SHAPES[1:5])
+def test_lora_t_far_below_the_rows_largest_meets_an_infinity(M, L, rank, K, N, dtype):
+    """Ranks so small beside the row's largest that a number of the type keeps nothing of them, or
+    below the type's smallest number altogether: their sign still decides."""
+    t = inputs(M + 1, M, L, rank, K, N, dtype, ids=torch.arange(M) % L)
+    x, a = torch.ones(M, K), torch.zeros(L, rank, K)
+    x[:, 1:] = 0
+    x[1::2, 0] = -1
+    a[:, :, 0] = 4.0
+    tiny = {"f16": 2.0 ** -24, "bf16": 2.0 ** -120, "f32": 2.0 ** -120}[dtype]
+    a[:, 1::2, 0] = tiny
+    a[:, 3::4, 0] = -tiny
+    t["x"], t["a"] = x.to(DT[dtype]), a.to(DT[dtype])
+    t["scales"] = torch.full((L,), {"f16": 2.0 ** -60, "bf16": 2.0 ** -20, "f32": 1.0}[dtype])
+    t["b"] = t["b"].clone()
+    t["b"][:, 5, 1], t["b"][:, 6, 3], t["b"][:, 7, 0] = INF, INF, -INF
+    ref, got = reference(t)[0], f64(call(t))
+    for n in (5, 6, 7):
+        assert np.isinf(ref[:, n]).all() and np.array_equal(got[:, n], ref[:, n])
+    assert np.isfinite(got[:, 8:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M, L, rank, K, N", INF_SHAPES)
+def test_lora_not_finite_adapters_and_rows(M, L, rank, K, N, dtype):
+    """Infinities in x and a reach their rows as the definition has them, NaN in b its column, NaN in a
+    its adapter's rows; infinite t times an infinite b is infinite."""
+    t = inputs(M + 2 * rank, M, L, rank, K, N, dtype, ids=torch.arange(M) % L)
+    for k in ("x", "a", "b"):
+        t[k] = t[k].clone()
+    # (every factor positive: no sum holds two infinities of unlike signs)
+    t["x"], t["a"], t["b"] = t["x"].abs() + 0.125, t["a"].abs() + 0.125, t["b"].abs() + 0.125
+    plain = call(t)
+    t["x"][M // 2, 3] = INF
+    t["b"][:, N // 2, rank - 1] = INF
+    t["b"][:, N // 3, 0] = NAN
+    y = call(t)
+    assert (y[M // 2, [n for n in range(N) if n != N // 3]] == INF).all()
+    assert (y[:, N // 2] == INF).all() and torch.isnan(y[:, N // 3]).all()
+    rows = [m for m in range(M) if m != M // 2]
+    cols = [n for n in range(N) if n not in (N // 2, N // 3)]
+    assert torch.equal(y[rows][:, cols], plain[rows][:, cols])
+    t["a"][0, rank // 2, 1] = NAN
+    assert torch.isnan(call(t)[0]).all()
 
 
 @pytest.mark.parametrize("M", [1, 40])
