@@ -125,3 +125,32 @@ def test_lora_bf16_largest_t(M):
     value = 1.9921875 * (1 + 2.0 ** -8)
     assert torch.finfo(torch.bfloat16).max < value * 2.0 ** 127 < torch.finfo(torch.float32).max
     assert np.all(np.abs(f64(call(t)) - ref) <= tolerance(ref, At, Ab, Am, K, rank, torch.bfloat16))
+
+
+# (x and a, scale, b): powers of two; t = x A^T times the scale is some 2^(2 xa + 3.5) scale
+FAR = {"huge": (11, -4, -23), "largest": (15, -13, -24), "tiny": (-14, -3, 12), "smaller": (-14, -11, 15),
+       "scale up": (-14, 14, 8), "scale down": (14, -28, -4)}
+
+
+@pytest.mark.parametrize("M, L, rank, K, N", [(37, 1, 16, 128, 48), (45, 3, 24, 144, 70), (300, 2, 64, 112, 130)])
+@pytest.mark.parametrize("kind", FAR)
+def test_lora_f16_t_outside_fp16_and_y_within(kind, M, L, rank, K, N):
+    """x A^T (before and behind its scale) beyond fp16's largest number, or below its smallest, with y
+    an ordinary number: y is right where the base alone, or zeros, would not be."""
+    xa, scale, b = FAR[kind]
+    g = torch.Generator().manual_seed(M + len(kind))
+    t = inputs(5, M, L, rank, K, N, "f16", ids=torch.arange(M) % L)
+    unit = lambda *shape: (torch.rand(*shape, generator=g) + 0.5) * (torch.randint(0, 2, shape, generator=g) * 2 - 1)
+    # (up to 2^15 and down to 2^-14 in x and a, 2^-24 in b, where one bit is all there is)
+    t["x"], t["a"] = (unit(M, K) * 2.0 ** xa).half(), (unit(L, rank, K) * 2.0 ** xa).half()
+    t["b"] = (unit(L, N, rank) * 2.0 ** b).half()
+    t["scales"] = torch.full((L,), 2.0 ** scale)
+    t["base"] = torch.zeros(M, N).half()
+    y, At, Ab, Am = reference(t)
+    tol = tolerance(y, At, Ab, Am, K, rank, torch.float16)
+    size = np.abs(f64(t["x"]) @ f64(t["a"])[0].T)[np.arange(M) % L == 0] * (1.0 if kind.startswith("scale") else 2.0 ** scale)
+    outside = (size > 65504) if kind in ("huge", "largest", "scale down") else (size < 2.0 ** -14)
+    fits = np.abs(y) < 60000
+    assert outside.mean() > 0.9 and fits.mean() > 0.9 and np.mean(np.abs(y) > 8 * tol) > 0.5
+    err = np.abs(f64(call(t)) - y)
+    assert np.all(err[fits] <= tol[fits]), f"worst {np.max((err / tol)[fits])}"
