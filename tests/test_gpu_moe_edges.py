@@ -103,3 +103,29 @@ def test_route_one_group_by_two_is_ordered_by_its_logits(sigmoid, topk, dtype):
     assert np.all(np.abs(f64(w) - ref_w) <= 1.01 * U * ref_w + 2.0 ** -149)
     one = lb.lowbit_moe_route(logits.to(DEV), topk, score=lb.ROUTE_SIGMOID if sigmoid else lb.ROUTE_SOFTMAX)
     assert torch.equal(e, one[0]) and torch.equal(w, one[1])
+
+
+# -------------------------------------------------------------- group_rows --
+
+# Every schedule: a block an expert with one, four and sixteen waves (the last with one run of steps a
+# wave, and several), a block a chunk in one launch, and two launches with chunks of 1024 and 4096.
+ORDERS = [(3, 5, 4), (700, 3, 60), (1025, 7, 5), (2049, 8, 256), (5001, 4, 900), (5001, 4, 1500), (8192, 8, 61),
+          (8193, 1, 65536), (65535, 1, 901), (16385, 4, 3000), (12001, 8, 256), (70000, 2, 33), (70000, 2, 901),
+          (40000, 3, 900), (70001, 8, 257)]
+
+
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+@pytest.mark.parametrize("T, k, E", ORDERS)
+def test_group_rows_of_every_schedule_is_the_stable_order(T, k, E, kind):
+    """Against a stable sort on the CPU: ids spread out, all alike, and of the first and last only."""
+    g = torch.Generator().manual_seed(T + E)
+    for ids in (torch.randint(-1, E + 1, (T, k), generator=g), torch.full((T, k), E // 2),
+                torch.randint(0, 2, (T, k), generator=g) * (E - 1)):
+        rows, offsets, position = (v.cpu().long() for v in lb.lowbit_group_rows(ids.to(kind).to(DEV), E))
+        key = torch.where((ids >= 0) & (ids < E), ids, E).view(-1)
+        order = torch.argsort(key, stable=True)
+        place = torch.empty_like(order)
+        place[order] = torch.arange(T * k)
+        assert torch.equal(rows, order // k)
+        assert offsets[0] == 0 and torch.equal(offsets[1:], torch.bincount(key, minlength=E + 1)[:E].cumsum(0))
+        assert torch.equal(position.view(-1), torch.where(key < E, place, -1))
