@@ -748,8 +748,9 @@ class F8Experts(_F8Module):
                                                    None, self.dtype)
         # (rows of no expert are undefined; their slots have position -1 and add nothing)
         weights = weights.reshape(T, k).float()
-        if _derived(weights):
+        if k > 31 or _derived(weights):
             # the same sum from torch's operations, which know the derivatives of the routing weights
+            # (bit for bit up to 31 slots; from 32 on torch's sum adds in another order, and is kept)
             # (both factors of a slot without an expert are 0 before they meet, for the derivatives' sake)
             used = position >= 0
             out = torch.where(used.unsqueeze(-1), slots[position.clamp(min=0).long()].float(), 0.0)

@@ -129,3 +129,44 @@ def test_group_rows_of_every_schedule_is_the_stable_order(T, k, E, kind):
         assert torch.equal(rows, order // k)
         assert offsets[0] == 0 and torch.equal(offsets[1:], torch.bincount(key, minlength=E + 1)[:E].cumsum(0))
         assert torch.equal(position.view(-1), torch.where(key < E, place, -1))
+
+
+# ----------------------------------------------------------------- the sum --
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T, N", [(1, 16), (1, 2048), (3, 5008), (64, 272), (300, 1024), (2000, 64)])
+def test_combine_is_torch_s_sum_up_to_31_slots(T, N, dtype):
+    """Bit for bit: products in fp32, their sum over the slots by torch, rounded once, as F8Experts
+    computes it where a derivative may be asked for."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + N)
+    for k in range(1, 32):
+        y = torch.randn(T * k, N, generator=g, device=DEV).to(DT[dtype])
+        w = torch.rand(T, k, generator=g, device=DEV) - 0.25
+        position = torch.randperm(T * k, generator=g, device=DEV).view(T, k).int()
+        position = torch.where(torch.rand(T, k, generator=g, device=DEV) < 0.1, -1, position)
+        terms = y[position.clamp(min=0).long()].float() * w.unsqueeze(-1)
+        want = torch.where((position >= 0).unsqueeze(-1), terms, 0.0).sum(1).to(DT[dtype])
+        assert torch.equal(lb.lowbit_moe_combine(y, position, w), want), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("k", [1, 8, 16, 31, 32, 47, 64])
+def test_experts_sum_is_one_with_and_without_a_derivative(k, dtype):
+    """Bit for bit, and that of torch over the slots' rows."""
+    m, n, g = experts_of(23, E=64, H=272, I=48, dtype=DT[dtype])
+    x, w = n(50, 272).to(DT[dtype]), torch.rand(50, k, generator=g, device=DEV)
+    e = torch.stack([torch.randperm(64, generator=g, device=DEV)[:k] for _ in range(50)])
+    e = torch.where(torch.rand(50, k, generator=g, device=DEV) < 0.1, -1, e)
+    out = m(x, e, w)
+    assert torch.equal(m(x, e, w.clone().requires_grad_()), out)
+    assert torch.equal(torch.func.jvp(lambda v: m(x, e, v), (w,), (w,))[0], out)
+    # the slots' rows by the same calls (a linear by expert of fewer rows may add in another order)
+    op = torch.ops.lowbit
+    xq, xs = op.quantize_act_f8(x)
+    rows, offsets, position = op.group_rows(e, 64)
+    gate, up = op.linear_f8_grouped(xq, xs, rows, offsets, m.gate_up, m.gate_up_scale, None, m.dtype).split(48, dim=-1)
+    aq, a_s = op.quantize_act_f8(torch.nn.functional.silu(gate) * up)
+    slots = op.linear_f8_grouped(aq, a_s, None, offsets, m.down, m.down_scale, None, m.dtype)
+    terms = slots[position.clamp(min=0).long()].float() * w.unsqueeze(-1)
+    assert torch.equal(torch.where((position >= 0).unsqueeze(-1), terms, 0.0).sum(1).to(DT[dtype]), out)

@@ -197,3 +197,14 @@ def test_experts_padded_slots_of_any_weight_add_nothing(calls, weight):
     out.sum().backward()
     assert torch.isfinite(v.grad).all() and v.grad[3, 2] == 0
     assert torch.isfinite(torch.func.jvp(lambda u: m(x, e, u), (w,), (t,))[1]).all()
+
+
+def test_experts_of_very_many_slots_keep_torch_s_order_of_the_sum(calls):
+    """torch's sum over up to 31 slots is the library's, bit for bit; from 32 on it adds in another
+    order, and is kept."""
+    m = experts_of(E=40)
+    for k in (31, 32, 40):
+        x, e, w, _ = batch(E=40, k=k)
+        del calls[:]
+        m(x, e, w)
+        assert ("combine" in calls) == (k < 32)
