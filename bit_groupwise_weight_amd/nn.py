@@ -736,6 +736,8 @@ class F8Experts(_F8Module):
         T, k = xq.shape[0], experts.shape[-1]
         if experts.shape != weights.shape or experts.numel() != T * k:
             raise ValueError("experts and weights must both be [T, k]")
+        if k == 0:
+            return weights.reshape(T, 0, 1).float().expand(T, 0, self.hidden).sum(1).to(self.dtype)
         ids = experts.reshape(T, k)
         if ids.dtype not in (torch.int32, torch.int64):
             ids = ids.long()

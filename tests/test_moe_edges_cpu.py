@@ -208,3 +208,18 @@ def test_experts_of_very_many_slots_keep_torch_s_order_of_the_sum(calls):
         del calls[:]
         m(x, e, w)
         assert ("combine" in calls) == (k < 32)
+
+
+@pytest.mark.parametrize("shape", [(6,), (2, 3), (0,)])
+def test_experts_of_no_slots_are_zeros(calls, shape):
+    m = experts_of(dtype=torch.bfloat16)
+    x = torch.randn(*shape, 32).bfloat16()
+    e, w = torch.empty(*shape, 0, dtype=torch.int32), torch.empty(*shape, 0)
+    out = m(x, e, w)
+    assert out.shape == x.shape and out.dtype == torch.bfloat16 and (out == 0).all()
+    v = w.clone().requires_grad_()
+    m(x, e, v).float().sum().backward()
+    assert v.grad.shape == v.shape
+    meta = lnn.F8Experts(5, 32, 16, device=META)
+    out = meta(x.to(META), e.to(META), w.to(META))
+    assert out.shape == x.shape and out.device == META
