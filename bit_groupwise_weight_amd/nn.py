@@ -465,6 +465,23 @@ def _derived(t: torch.Tensor) -> bool:
     return torch.autograd.forward_ad.unpack_dual(t).tangent is not None
 
 
+def _no_tangent(what: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuse tensors that carry a forward-mode tangent: the library's calls have no derivative, and
+    torch would drop the tangent without a word.  (Of nested derivatives the innermost one's is seen;
+    in a compiled program batched tensors are refused while forward mode is at work.)"""
+    if torch.autograd.forward_ad._current_level < 0:
+        return
+    functorch = torch._C._functorch
+    for t in tensors:
+        if t is None:
+            continue
+        compiling = torch.compiler.is_compiling()
+        while not compiling and functorch.is_batchedtensor(t):
+            t = functorch.get_unwrapped(t)
+        if functorch.is_batchedtensor(t) or torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{what} has no forward-mode derivative")
+
+
 class LowbitLinear(torch.nn.Module):
     """``nn.Linear`` with a groupwise b-bit weight: w = s * q + z per group.
 
@@ -804,6 +821,7 @@ class MoeRouter(torch.nn.Module):
         """logits[..., E] -> (experts int32, weights float32), both [..., topk]."""
         if logits.shape[-1:] != (self.num_experts,):
             raise ValueError(f"logits must be [..., {self.num_experts}], got {list(logits.shape)}")
+        _no_tangent("MoeRouter", logits, self.bias)
         return torch.ops.lowbit.moe_route(logits, self.bias, self.topk, self._score(), self.groups,
                                           self.topk_groups, self.group_best, self.renormalize, self.scale)
 
@@ -884,6 +902,7 @@ class LoraLinear(torch.nn.Module):
         y = self.linear(x)
         if plan is None:
             return y
+        _no_tangent("LoraLinear", x, y, self.a, self.b, self.scales)
         return torch.ops.lowbit.lora(x, self.a, self.b, self.scales, plan[0], plan[1], y)
 
     def extra_repr(self) -> str:

@@ -223,3 +223,71 @@ def test_experts_of_no_slots_are_zeros(calls, shape):
     meta = lnn.F8Experts(5, 32, 16, device=META)
     out = meta(x.to(META), e.to(META), w.to(META))
     assert out.shape == x.shape and out.device == META
+
+
+# ------------------------------------------- modules without a derivative --
+
+def router_and_lora(monkeypatch):
+    def route(logits, topk, bias, *rest):
+        w, e = torch.softmax(logits.float(), -1).topk(topk, -1)
+        return e.int(), w
+
+    def lora(x, a, b, scales, rows, offsets, base, y=None):
+        y = base.clone() if y is None else y
+        for l in range(a.shape[0]):
+            at = rows[int(offsets[l]):int(offsets[l + 1])].long()
+            y[at] = (base[at].float() + (x[at].float() @ a[l].float().t()) @ b[l].float().t() * scales[l]).to(y.dtype)
+        return y
+
+    monkeypatch.setattr(lb, "lowbit_moe_route", route)
+    monkeypatch.setattr(lb, "lowbit_lora", lora)
+    g = torch.Generator().manual_seed(5)
+    m = lnn.LoraLinear(torch.nn.Linear(32, 24), 2, 8).requires_grad_(False)
+    for i in range(2):
+        m.set_adapter(i, torch.randn(8, 32, generator=g), torch.randn(24, 8, generator=g), 0.5)
+    return lnn.MoeRouter(12, 3, bias=True), m, torch.randn(5, 12, generator=g), torch.randn(5, 32, generator=g)
+
+
+def test_router_and_adapters_refuse_forward_mode(calls, monkeypatch):
+    """They have no derivative: reverse mode raises at the backward pass, forward mode at the call, where
+    the tangent would be dropped without a word."""
+    router, m, logits, x = router_and_lora(monkeypatch)
+    plan = lnn.adapter_plan(torch.tensor([0, 1, -1, 1, 0]), 2)
+    route = lambda l: router(l)[1]
+    adapt = lambda v: m(v, plan)
+    for f, v in ((route, logits), (adapt, x)):
+        for g in (lambda: torch.func.jvp(f, (v,), (v,)), lambda: torch.func.jacfwd(f)(v),
+                  lambda: torch.vmap(lambda u: torch.func.jvp(f, (u,), (u,)))(v[None]),
+                  lambda: torch.func.jvp(torch.vmap(f), (v[None],), (v[None],)),
+                  lambda: torch.func.jvp(lambda a: torch.func.jvp(f, (a,), (v,))[1], (v,), (v,)),
+                  lambda: torch.compile(lambda u: torch.func.jvp(f, (u,), (u,))[1], backend="eager")(v)):
+            with pytest.raises(RuntimeError, match="forward"):
+                g()
+        with torch.autograd.forward_ad.dual_level(), pytest.raises(RuntimeError, match="forward"):
+            f(torch.autograd.forward_ad.make_dual(v, v))
+        with pytest.raises(RuntimeError):
+            f(v.clone().requires_grad_()).sum().backward()
+        with pytest.raises(RuntimeError):
+            torch.func.grad(lambda u: f(u).sum())(v)
+    with pytest.raises(RuntimeError, match="forward"):
+        torch.func.jvp(lambda a: torch.func.functional_call(m, {"a": a}, (x, plan)), (m.a,), (m.a,))
+
+
+def test_router_and_adapters_beside_a_derivative_of_something_else(calls, monkeypatch):
+    """Tensors without a tangent pass, inside a forward-mode derivative and under vmap."""
+    router, m, logits, x = router_and_lora(monkeypatch)
+    plan = lnn.adapter_plan(torch.tensor([0, 1, -1, 1, 0]), 2)
+    w, y = router(logits)[1], m(x, plan)
+    t = torch.ones(3)
+    out, tangent = torch.func.jvp(lambda s: s * router(logits)[1], (t,), (t,))
+    assert torch.equal(out, w) and torch.equal(tangent, w)
+    out, tangent = torch.func.jvp(lambda s: s[0] * m(x, plan), (t,), (t,))
+    assert torch.equal(out, y) and torch.equal(tangent, y)
+    # no plan, no adapters: the linear's own derivative
+    assert torch.equal(torch.func.jvp(m, (x,), (x,))[1], x @ m.linear.weight.t())
+    fn = torch.compile(lambda l, v: (router(l)[1], m(v, plan)), fullgraph=True, backend="aot_eager")
+    got = fn(logits, x)
+    assert torch.equal(got[0], w) and torch.equal(got[1], y)
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")
+        assert torch.equal(torch.vmap(lambda l: router(l)[1])(logits[None])[0], w)
