@@ -877,7 +877,7 @@ class LoraLinear(torch.nn.Module):
 
         def keep(t):
             moved = fn(t)
-            return t.to(moved.device) if t is scales else moved
+            return t.to(moved.device) if t is scales and moved.dtype != t.dtype else moved
 
         return super()._apply(keep, recurse)
 

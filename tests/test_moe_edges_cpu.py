@@ -291,3 +291,36 @@ def test_router_and_adapters_beside_a_derivative_of_something_else(calls, monkey
     with warnings.catch_warnings():
         warnings.simplefilter("ignore")
         assert torch.equal(torch.vmap(lambda l: router(l)[1])(logits[None])[0], w)
+
+
+# ------------------------------------------------------- modules, moved ----
+
+@pytest.mark.parametrize("make", [
+    lambda: lnn.LoraLinear(torch.nn.Linear(32, 24, device=META, dtype=torch.bfloat16), 2, 8),
+    lambda: lnn.LoraLinear(lnn.F8Linear(32, 24, device=META), 2, 8),
+    lambda: lnn.MoeRouter(12, 3, bias=True, device=META),
+])
+def test_modules_built_on_meta_are_materialized(make):
+    m = make().to_empty(device="cpu")
+    assert all(t.device.type == "cpu" for t in (*m.buffers(), *m.parameters()))
+    kept = m.scales if isinstance(m, lnn.LoraLinear) else m.bias
+    assert kept.dtype == torch.float32
+    kept.fill_(0.1)
+    m = m.half()
+    kept = m.scales if isinstance(m, lnn.LoraLinear) else m.bias
+    assert kept.dtype == torch.float32 and (kept == torch.tensor(0.1)).all()
+
+
+def test_lora_linear_keeps_its_scales_through_casts_and_moves():
+    """Their values and type; what the move itself does to them (here: memory of their own) is kept."""
+    m = lnn.LoraLinear(torch.nn.Linear(32, 24), 3, 8)
+    m.scales.copy_(torch.tensor([0.1, 1e-30, 3.0]))
+    want = m.scales.clone()
+    for cast in (lambda m: m.bfloat16(), lambda m: m.to(torch.float16), lambda m: m.double(), lambda m: m.float(),
+                 lambda m: m.cpu()):
+        m = cast(m)
+        assert m.scales.dtype == torch.float32 and torch.equal(m.scales, want)
+    before = m.scales
+    m._apply(lambda t: t.clone())
+    assert torch.equal(m.scales, want) and m.scales.data_ptr() != before.data_ptr()
+    assert torch.equal(lnn.LoraLinear(torch.nn.Linear(32, 24), 3, 8).share_memory().scales, torch.ones(3))
