@@ -827,8 +827,8 @@ class MoeRouter(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return (f"num_experts={self.num_experts}, topk={self.topk}, score={self.score}, groups={self.groups}, "
-                f"topk_groups={self.topk_groups}, renormalize={self.renormalize}, scale={self.scale}, "
-                f"bias={self.bias is not None}")
+                f"topk_groups={self.topk_groups}, group_best={self.group_best}, renormalize={self.renormalize}, "
+                f"scale={self.scale}, bias={self.bias is not None}")
 
 
 def adapter_plan(ids: torch.Tensor, num_adapters: int) -> Tuple[torch.Tensor, torch.Tensor]:

@@ -324,3 +324,11 @@ def test_lora_linear_keeps_its_scales_through_casts_and_moves():
     m._apply(lambda t: t.clone())
     assert torch.equal(m.scales, want) and m.scales.data_ptr() != before.data_ptr()
     assert torch.equal(lnn.LoraLinear(torch.nn.Linear(32, 24), 3, 8).share_memory().scales, torch.ones(3))
+
+
+def test_router_names_all_its_settings():
+    text = repr(lnn.MoeRouter(24, 3, "sigmoid", bias=True, groups=4, topk_groups=2, group_best=2, renormalize=False,
+                              scale=2.5))
+    for part in ("num_experts=24", "topk=3", "score=sigmoid", "bias=True", "groups=4", "topk_groups=2", "group_best=2",
+                 "renormalize=False", "scale=2.5"):
+        assert part in text
