@@ -951,7 +951,8 @@ def lowbit_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: Optio
     rows int32 [T] names the rows in the order of their adapter (None: T = M, as they stand),
     offsets int32 [L + 1] where each adapter's begin: lowbit_group_rows(ids[:, None], L) makes both
     for a batch, once for all its projections.  `y` may be base itself, which is then updated in
-    place.  (Rows that `rows` does not name are left as they are in y.)"""
+    place.  Rows that `rows` does not name are left as they are in y (undefined in a y that the
+    call makes)."""
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         raise ValueError("x must be [M, K], a [L, rank, K] and b [L, N, rank]")
     dt = x.dtype

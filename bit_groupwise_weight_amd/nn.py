@@ -48,15 +48,18 @@ Ops (namespace ``lowbit``):
 * ``lowbit::moe_combine(Tensor y, Tensor position, Tensor weights, Tensor?
   residual) -> Tensor`` -- each token's weighted sum of its experts' rows;
 * ``lowbit::lora(Tensor x, Tensor a, Tensor b, Tensor? scales, Tensor? rows,
-  Tensor offsets, Tensor? base) -> Tensor`` -- ``base`` plus the low-rank adapter
-  of each row.
+  Tensor offsets, Tensor? base, bool all_rows=False) -> Tensor`` -- ``base`` plus
+  the low-rank adapter of each row.  Rows that ``rows`` does not name keep
+  ``base``, of which a copy is made first; ``all_rows`` says that it names every
+  row, as group_rows makes it, so that none is needed (rows left out all the same
+  are undefined then).
 
 All run in liblowbit.so through :mod:`bit_groupwise_weight_amd.lowbit`;
 nothing here computes on the CPU.
 """
 from __future__ import annotations
 
-from typing import Callable, Optional, Tuple
+from typing import Callable, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -435,19 +438,21 @@ def _check_lora(x, a, b, scales, rows, offsets, base) -> Tuple[int, int]:
 
 @torch.library.custom_op("lowbit::lora", mutates_args=())
 def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: Optional[torch.Tensor],
-         rows: Optional[torch.Tensor], offsets: torch.Tensor, base: Optional[torch.Tensor]) -> torch.Tensor:
+         rows: Optional[torch.Tensor], offsets: torch.Tensor, base: Optional[torch.Tensor],
+         all_rows: bool = False) -> torch.Tensor:
     N, K = _check_lora(x, a, b, scales, rows, offsets, base)
     x2 = x.reshape(-1, K).contiguous()
     base2 = None if base is None else base.reshape(-1, N).contiguous()
-    y = None
-    if rows is not None and rows.shape[0] < x2.shape[0]:      # rows that are not named keep base, too
+    a, b, y = a.contiguous(), b.contiguous(), None
+    if rows is not None and (not all_rows or rows.shape[0] < x2.shape[0]):
         y = x2.new_zeros((x2.shape[0], N)) if base2 is None else base2.clone()
-    y = _lb.lowbit_lora(x2, a.contiguous(), b.contiguous(), scales, rows, offsets, base2, y=y)
+        base2 = None if base2 is None else y                  # (in place)
+    y = _lb.lowbit_lora(x2, a, b, scales, rows, offsets, base2, y=y)
     return y.reshape(*x.shape[:-1], N)
 
 
 @lora.register_fake
-def _lora_fake(x, a, b, scales, rows, offsets, base):
+def _lora_fake(x, a, b, scales, rows, offsets, base, all_rows=False):
     N, _ = _check_lora(x, a, b, scales, rows, offsets, base)
     return x.new_empty((*x.shape[:-1], N))
 
@@ -831,14 +836,21 @@ class MoeRouter(torch.nn.Module):
                 f"scale={self.scale}, bias={self.bias is not None}")
 
 
-def adapter_plan(ids: torch.Tensor, num_adapters: int) -> Tuple[torch.Tensor, torch.Tensor]:
+class AdapterPlan(NamedTuple):
+    """A batch's rows in the order of their adapter, every row named once, and where each adapter's
+    begin: ``rows`` and ``offsets`` of ``lowbit::group_rows``."""
+    rows: torch.Tensor
+    offsets: torch.Tensor
+
+
+def adapter_plan(ids: torch.Tensor, num_adapters: int) -> AdapterPlan:
     """The plan of a batch for its LoraLinear layers, from each row's adapter (any integer type;
     outside 0..num_adapters-1: none): (rows, offsets), made on the GPU, good for every layer."""
     ids = ids.reshape(-1, 1)
     if ids.dtype not in (torch.int32, torch.int64):
         ids = ids.long()
     rows, offsets, _ = torch.ops.lowbit.group_rows(ids, num_adapters)
-    return rows, offsets
+    return AdapterPlan(rows, offsets)
 
 
 class LoraLinear(torch.nn.Module):
@@ -898,12 +910,14 @@ class LoraLinear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, plan: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> torch.Tensor:
         """x[..., K] -> [..., N]; ``plan`` = adapter_plan(ids, num_adapters) for x's rows, None for
-        no adapters."""
+        no adapters.  Rows that a (rows, offsets) of another make does not name keep the linear's
+        output; an AdapterPlan names all of them, which saves the copy that keeping it takes."""
         y = self.linear(x)
         if plan is None:
             return y
         _no_tangent("LoraLinear", x, y, self.a, self.b, self.scales)
-        return torch.ops.lowbit.lora(x, self.a, self.b, self.scales, plan[0], plan[1], y)
+        return torch.ops.lowbit.lora(x, self.a, self.b, self.scales, plan[0], plan[1], y,
+                                     isinstance(plan, AdapterPlan))
 
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "

@@ -154,3 +154,29 @@ def test_lora_f16_t_outside_fp16_and_y_within(kind, M, L, rank, K, N):
     assert outside.mean() > 0.9 and fits.mean() > 0.9 and np.mean(np.abs(y) > 8 * tol) > 0.5
     err = np.abs(f64(call(t)) - y)
     assert np.all(err[fits] <= tol[fits]), f"worst {np.max((err / tol)[fits])}"
+
+
+@pytest.mark.parametrize("M, N", [(20, 40), (300, 264)])
+@pytest.mark.parametrize("with_base", [False, True])
+def test_op_lora_keeps_base_in_rows_that_are_not_named(with_base, M, N):
+    """Rows that a plan of as many entries, of more or of fewer leaves out: base, or 0; a whole plan
+    the same with and without a copy of base."""
+    t = inputs(31, M, 2, 16, 48, N, "bf16", ids=torch.arange(M) % 2)
+    d = {k: v.to(DEV) for k, v in t.items() if torch.is_tensor(v)}
+    base = d["base"] if with_base else None
+    want = torch.ops.lowbit.lora(d["x"], d["a"], d["b"], d["scales"], *plan(t), base, True)
+    assert torch.equal(torch.ops.lowbit.lora(d["x"], d["a"], d["b"], d["scales"], *plan(t), base), want)
+    rest = base if with_base else torch.zeros_like(want)
+    kept = d["base"].clone()
+    for entries in (M, 2 * M, M - 3):
+        named = torch.arange(0, M // 2 * 2, 4)           # (of adapter 0)
+        rows = torch.full((entries,), -1)
+        rows[:len(named)] = named
+        rows[len(named):len(named) + 2] = torch.tensor([M, 2 ** 31 - 1])
+        junk = torch.full((M, N), NAN, dtype=torch.bfloat16, device=DEV)       # (memory that is likely taken next)
+        del junk
+        y = torch.ops.lowbit.lora(d["x"], d["a"], d["b"], d["scales"], rows.int().to(DEV),
+                                  torch.tensor([0, entries, entries], dtype=torch.int32, device=DEV), base)
+        others = [m for m in range(M) if m not in named.tolist()]
+        assert torch.equal(y[named.to(DEV)], want[named.to(DEV)]) and torch.equal(y[others], rest[others])
+    assert torch.equal(d["base"], kept)

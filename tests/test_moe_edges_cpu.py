@@ -332,3 +332,77 @@ def test_router_names_all_its_settings():
     for part in ("num_experts=24", "topk=3", "score=sigmoid", "bias=True", "groups=4", "topk_groups=2", "group_best=2",
                  "renormalize=False", "scale=2.5"):
         assert part in text
+
+
+# ---------------------------------------------------- rows that are named ----
+
+@pytest.fixture
+def lora_calls(monkeypatch):
+    """lowbit_lora in plain torch: only rows that `rows` names are written; y of the call's own is NaN."""
+    seen = []
+
+    def lora(x, a, b, scales, rows, offsets, base, y=None):
+        seen.append("fresh" if y is None else "given")
+        M, L = x.shape[0], a.shape[0]
+        y = torch.full((M, b.shape[1]), NAN, dtype=x.dtype) if y is None else y
+        was = torch.zeros_like(y) if base is None else base.clone()
+        at = torch.arange(M) if rows is None else rows.long()
+        for p, m in enumerate(at.tolist()):
+            if not 0 <= m < M:
+                continue
+            l = next((l for l in range(L) if offsets[l] <= p < offsets[l + 1]), None)
+            y[m] = was[m]
+            if l is not None:
+                y[m] += (x[m] @ a[l].t()) @ b[l].t() * (1.0 if scales is None else scales[l])
+        return y
+
+    monkeypatch.setattr(lb, "lowbit_lora", lora)
+    return seen
+
+
+@pytest.mark.parametrize("with_base", [False, True])
+@pytest.mark.parametrize("rows, offsets", [
+    ([3, -1, 0, 6, 2, 9], [0, 3, 5]),            # as many as there are rows, some of them none
+    ([-1] * 6, [0, 3, 6]),
+    ([3, 1, -1, -1, -1, -1, -1, -1], [0, 1, 2]),  # more: a plan of fixed length, filled up
+    ([3, 1], [0, 1, 2]), ([], [0, 0, 0]),        # fewer
+    ([5, 4, 3, 2, 1, 0], [0, 2, 4]),             # all of them
+])
+def test_op_lora_keeps_base_in_rows_that_are_not_named(lora_calls, with_base, rows, offsets):
+    g = torch.Generator().manual_seed(4)
+    x, a, b = torch.randn(6, 32, generator=g), torch.randn(2, 8, 32, generator=g), torch.randn(2, 24, 8, generator=g)
+    base = torch.randn(6, 24, generator=g) if with_base else None
+    kept = base.clone() if with_base else None
+    y = torch.ops.lowbit.lora(x, a, b, None, torch.tensor(rows, dtype=torch.int32), torch.tensor(offsets, dtype=torch.int32), base)
+    assert torch.isfinite(y).all()
+    was = torch.zeros(6, 24) if base is None else base
+    want = was.clone()
+    for p, m in enumerate(rows):
+        l = 0 if p < offsets[1] else 1 if p < offsets[2] else None
+        if 0 <= m < 6 and l is not None and p >= offsets[0]:
+            want[m] += (x[m] @ a[l].t()) @ b[l].t()
+    assert torch.equal(y, want)
+    assert base is None or torch.equal(base, kept)
+
+
+def test_lora_linear_takes_plans_of_other_makers(lora_calls, calls):
+    """adapter_plan's names every row, and no copy of the linear's output is made for it; any other
+    plan's rows that are not named keep the linear's output."""
+    m = lnn.LoraLinear(torch.nn.Linear(32, 24), 2, 8).requires_grad_(False)
+    for i in range(2):
+        m.set_adapter(i, torch.randn(8, 32), torch.randn(24, 8))
+    x = torch.randn(2, 3, 32)
+    plan = lnn.adapter_plan(torch.tensor([0, 1, 1, -1, 0, 1]), 2)
+    rows, offsets = plan
+    y = m(x, plan)
+    assert lora_calls == ["fresh"]
+    assert torch.equal(y, m(x, (rows, offsets))) and lora_calls == ["fresh", "given"]
+    own = m(x, (torch.tensor([1, -1, 8, 4, -1, -1], dtype=torch.int32), torch.tensor([0, 1, 4], dtype=torch.int32)))
+    base = m.linear(x)
+    assert torch.equal(own.view(6, 24)[[0, 2, 3, 5]], base.view(6, 24)[[0, 2, 3, 5]])
+    assert not torch.equal(own, base) and torch.isfinite(own).all()
+    # (as many entries as rows: only the maker's word tells a whole plan from another)
+    del lora_calls[:]
+    m(x, lnn.AdapterPlan(rows, offsets))
+    fn = torch.compile(m, fullgraph=True, backend="aot_eager")
+    assert torch.equal(fn(x, plan), y) and lora_calls == ["fresh", "fresh"]
