@@ -443,7 +443,8 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: Optional[tor
     N, K = _check_lora(x, a, b, scales, rows, offsets, base)
     x2 = x.reshape(-1, K).contiguous()
     base2 = None if base is None else base.reshape(-1, N).contiguous()
-    a, b, y = a.contiguous(), b.contiguous(), None
+    a, b, offsets, y = a.contiguous(), b.contiguous(), offsets.contiguous(), None
+    rows, scales = (None if t is None else t.contiguous() for t in (rows, scales))
     if rows is not None and (not all_rows or rows.shape[0] < x2.shape[0]):
         y = x2.new_zeros((x2.shape[0], N)) if base2 is None else base2.clone()
         base2 = None if base2 is None else y                  # (in place)

@@ -406,3 +406,23 @@ def test_lora_linear_takes_plans_of_other_makers(lora_calls, calls):
     m(x, lnn.AdapterPlan(rows, offsets))
     fn = torch.compile(m, fullgraph=True, backend="aot_eager")
     assert torch.equal(fn(x, plan), y) and lora_calls == ["fresh", "fresh"]
+
+
+def test_ops_take_strided_plans_scales_and_weights(lora_calls, calls, monkeypatch):
+    """Any strides, as of the other arguments: what reaches the library is contiguous."""
+    seen = []
+    for name in ("lowbit_lora", "lowbit_linear_f8_grouped", "lowbit_moe_combine"):
+        def call(*args, _run=getattr(lb, name), **kw):
+            seen.extend(t.is_contiguous() for t in (*args, *kw.values()) if torch.is_tensor(t))
+            return _run(*args, **kw)
+        monkeypatch.setattr(lb, name, call)
+    wide = lambda t: torch.stack([t, t], -1)[..., 0]
+    x, a, b = torch.randn(6, 32), torch.randn(2, 8, 32), torch.randn(2, 24, 8)
+    rows, offsets = torch.arange(6).int(), torch.tensor([0, 2, 5]).int()
+    args = (x, a, b, torch.rand(2), rows, offsets, torch.randn(6, 24))
+    assert torch.equal(torch.ops.lowbit.lora(*map(wide, args)), torch.ops.lowbit.lora(*args))
+    position, w = torch.tensor([[0, 1], [3, -1]]).int(), torch.rand(2, 2)
+    args = (x, position, w, torch.randn(2, 32))
+    assert torch.equal(torch.ops.lowbit.moe_combine(*map(wide, args)),
+                       torch.ops.lowbit.moe_combine(*args))
+    assert seen and all(seen)
