@@ -29,7 +29,8 @@ PATH_AUTO, PATH_QMV, PATH_QMM = 0, 1, 2
 Q8_NONE, Q8_I8, Q8_F8 = 0, 1, 2      # lowbit_q8_format
 ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1  # lowbit_route_score
 ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, ROUTE_MAX_GROUPS = 1024, 64, 64   # LOWBIT_ROUTE_MAX_*
-LORA_MAX_RANK = 256
+LORA_MAX_RANK, LORA_MAX_ADAPTERS, LORA_MAX_SIZE = 256, 1 << 16, 1 << 23      # (N and K)
+COMBINE_MAX_TOPK = 1 << 16
 F8_BLOCK = 128                       # K elements (and weight rows) sharing an e4m3 scale
 _DTYPE_ENUM = {torch.float32: LOWBIT_F32, torch.float16: LOWBIT_F16, torch.bfloat16: LOWBIT_BF16}
 _ENUM_DTYPE = {v: k for k, v in _DTYPE_ENUM.items()}

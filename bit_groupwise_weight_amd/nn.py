@@ -330,7 +330,7 @@ def _linear_f8_grouped_fake(xq, xscale, rows, offsets, wq, wscale, bias, dtype):
 
 # ------------------------------------------ ops, around the experts, adapters --
 
-def _check_route(logits, bias, topk, score, groups, topk_groups, group_best) -> int:
+def _check_route(logits, bias, topk, score, groups, topk_groups, group_best, scale) -> int:
     if logits.dim() < 1 or logits.dtype not in _SZ_DTYPES:
         raise ValueError(f"logits must be [..., E] in one of {_SZ_DTYPES}")
     E = logits.shape[-1]
@@ -346,6 +346,8 @@ def _check_route(logits, bias, topk, score, groups, topk_groups, group_best) -> 
         raise ValueError("topk_groups must be in 1..groups, group_best 1 or 2")
     if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32):
         raise ValueError("bias must be float32 [E]")
+    if not abs(scale) < float("inf"):
+        raise ValueError(f"scale={scale} is not finite")
     return E
 
 
@@ -353,7 +355,7 @@ def _check_route(logits, bias, topk, score, groups, topk_groups, group_best) -> 
 def moe_route(logits: torch.Tensor, bias: Optional[torch.Tensor], topk: int, score: int, groups: int,
               topk_groups: int, group_best: int, renormalize: bool,
               scale: float) -> Tuple[torch.Tensor, torch.Tensor]:
-    E = _check_route(logits, bias, topk, score, groups, topk_groups, group_best)
+    E = _check_route(logits, bias, topk, score, groups, topk_groups, group_best, scale)
     experts, weights = _lb.lowbit_moe_route(logits.reshape(-1, E).contiguous(), topk,
                                             None if bias is None else bias.contiguous(), score, groups,
                                             topk_groups, group_best, renormalize, scale)
@@ -363,7 +365,7 @@ def moe_route(logits: torch.Tensor, bias: Optional[torch.Tensor], topk: int, sco
 
 @moe_route.register_fake
 def _moe_route_fake(logits, bias, topk, score, groups, topk_groups, group_best, renormalize, scale):
-    _check_route(logits, bias, topk, score, groups, topk_groups, group_best)
+    _check_route(logits, bias, topk, score, groups, topk_groups, group_best, scale)
     shape = (*logits.shape[:-1], topk)
     return logits.new_empty(shape, dtype=torch.int32), logits.new_empty(shape, dtype=torch.float32)
 
@@ -394,6 +396,8 @@ def _check_combine(y, position, weights, residual) -> None:
         raise ValueError(f"y must be [R, N] in one of {_SZ_DTYPES}")
     if position.dim() != 2 or position.shape[1] < 1 or position.dtype != torch.int32:
         raise ValueError("position must be int32 [T, k]")
+    if position.shape[1] > _lb.COMBINE_MAX_TOPK:
+        raise ValueError(f"k={position.shape[1]} is more than {_lb.COMBINE_MAX_TOPK}")
     if weights.shape != position.shape or weights.dtype != torch.float32:
         raise ValueError("weights must be float32 [T, k]")
     if residual is not None and (residual.shape != (position.shape[0], y.shape[1]) or residual.dtype != y.dtype):
@@ -425,6 +429,9 @@ def _check_lora(x, a, b, scales, rows, offsets, base) -> Tuple[int, int]:
         raise ValueError(f"x has K={x.shape[-1]}; a {list(a.shape)} and b {list(b.shape)} do not fit it and each other")
     if L < 1 or N < 1 or K == 0 or K % 16 or rank == 0 or rank % 8 or rank > _lb.LORA_MAX_RANK:
         raise ValueError(f"L and N must be positive, K a positive multiple of 16, rank one of 8 up to {_lb.LORA_MAX_RANK}")
+    if L > _lb.LORA_MAX_ADAPTERS or max(N, K) > _lb.LORA_MAX_SIZE:
+        raise ValueError(f"L={L}, N={N} and K={K} must be at most {_lb.LORA_MAX_ADAPTERS}, {_lb.LORA_MAX_SIZE} and "
+                         f"{_lb.LORA_MAX_SIZE}")
     if offsets.shape != (L + 1,) or offsets.dtype != torch.int32:
         raise ValueError("offsets must be int32 [L + 1]")
     if scales is not None and (scales.shape != (L,) or scales.dtype != torch.float32):
@@ -807,7 +814,7 @@ class MoeRouter(torch.nn.Module):
         self.groups, self.topk_groups, self.group_best = groups, topk_groups, group_best
         self.renormalize = bool(renormalize)
         _check_route(torch.empty((1, num_experts), device="meta"), None, topk, self._score(), groups, topk_groups,
-                     group_best)
+                     group_best, self.scale)
         if bias:
             self.register_buffer("bias", torch.zeros((num_experts,), dtype=torch.float32, device=device))
         else:

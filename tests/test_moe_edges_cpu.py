@@ -426,3 +426,17 @@ def test_ops_take_strided_plans_scales_and_weights(lora_calls, calls, monkeypatc
     assert torch.equal(torch.ops.lowbit.moe_combine(*map(wide, args)),
                        torch.ops.lowbit.moe_combine(*args))
     assert seen and all(seen)
+
+
+@pytest.mark.parametrize("call", [
+    lambda m: torch.ops.lowbit.lora(m(4, 32), m(3, 8, 32), m(3, (1 << 23) + 1, 8), None, None, m(4, dtype=torch.int32), None),
+    lambda m: torch.ops.lowbit.lora(m(4, (1 << 23) + 16), m(3, 8, (1 << 23) + 16), m(3, 40, 8), None, None,
+                                    m(4, dtype=torch.int32), None),
+    lambda m: torch.ops.lowbit.lora(m(4, 32), m(65537, 8, 32), m(65537, 40, 8), None, None, m(65538, dtype=torch.int32), None),
+    lambda m: torch.ops.lowbit.moe_route(m(4, 8), None, 2, 0, 1, 1, 1, True, INF),
+    lambda m: torch.ops.lowbit.moe_combine(m(4, 8), m(2, 65537, dtype=torch.int32), m(2, 65537), None),
+])
+def test_shape_functions_refuse_sizes_that_the_calls_refuse(call):
+    """(Not numbers of rows, which a compiled program may not know.)"""
+    with pytest.raises(ValueError):
+        call(lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=META))
