@@ -463,10 +463,9 @@ typedef enum lowbit_route_score {
  * Equal values: the lowest index first.  Without a bias and with group_best 1
  * or a single group (whose value nothing is compared with) experts are ordered
  * by their logits; otherwise c is computed in 64 bits, so that rounding does
- * not decide.  Weights are computed in 64 bits and
- * rounded once, but for softmax's sum over all experts where weights without
- * `renormalize` are divided by it: that is an fp32 sum unless there is a bias
- * (or group_best 2).
+ * not decide.  Weights are computed in 64 bits and rounded once.  (Without
+ * `renormalize` softmax divides them by its sum over all experts, whose terms
+ * are good to 2^-32 of themselves or better.)
  *
  *   logits   device, T x E row-major, dtype, aligned to its element size.
  *   bias     device, E fp32, or NULL.

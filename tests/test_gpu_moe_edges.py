@@ -170,3 +170,24 @@ def test_experts_sum_is_one_with_and_without_a_derivative(k, dtype):
     slots = op.linear_f8_grouped(aq, a_s, None, offsets, m.down, m.down_scale, None, m.dtype)
     terms = slots[position.clamp(min=0).long()].float() * w.unsqueeze(-1)
     assert torch.equal(torch.where((position >= 0).unsqueeze(-1), terms, 0.0).sum(1).to(DT[dtype]), out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("spread", [0.01, 1.5, 20.0])
+@pytest.mark.parametrize("E, k", [(1, 1), (8, 2), (60, 4), (64, 8), (130, 7), (256, 8), (257, 8), (512, 10), (1023, 9), (1024, 64)])
+def test_route_softmax_weights_as_they_are(E, k, spread, dtype):
+    """Weights divided by the sum over all experts: each term of it is good to 2^-32 of itself, so a weight
+    is off by its own rounding to fp32 and 1 % of that for all else."""
+    for T in (1, 33, 2100):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(E + T)
+        logits = (spread * torch.randn(T, E, generator=g, device=DEV)).to(DT[dtype])
+        logits[T // 2] = logits[T // 2].abs().neg() * 40      # a row far from 0, with terms that vanish
+        if E > 4:
+            logits[0, ::3], logits[T - 1, 1::2] = NEG, torch.finfo(DT[dtype]).min
+        e, w = lb.lowbit_moe_route(logits, k, renormalize=False, scale=0.75)
+        want = 0.75 * torch.softmax(logits.double(), 1).gather(1, e.long().clamp(min=0))
+        want = torch.where(e >= 0, want, 0.0)
+        assert torch.all((w.double() - want).abs() <= 1.01 * U * want + 2.0 ** -149)
+    e, w = lb.lowbit_moe_route(torch.full((3, E), NEG, device=DEV, dtype=DT[dtype]), k, renormalize=False)
+    assert (e == -1).all() and (w == 0).all()
