@@ -629,7 +629,7 @@ __device__ __forceinline__ void copy_columns(const LoraParams& p, Outputs<ACT>& 
 // waves load together.  A step's B is asked for behind the products of the step
 // before and ahead of that one's stores, its base behind them.  Bound by memory:
 // base once in, y once out, past the caches (8192 rows, 14336 bf16 columns, rank
-// 64, 470 MB: 108 to 112 us, 4.2 to 4.4 TB/s, a copy of the base alone 89; 777
+// 64, 470 MB: 107 to 117 us, 4.0 to 4.4 TB/s, a copy of the base alone 89; 777
 // rows of 7 adapters, 5001 fp16 columns, rank 24: 10.5 us, most of it latencies
 // that follow each other: offsets, then t, B and rows, then base).  Measured and
 // left: the first base asked for with t (8192 rows 122), two row tiles a wave or
@@ -734,8 +734,8 @@ __global__ __launch_bounds__(64 * WM * WN) void lora_expand_kernel(LoraParams p,
 // block of a tile's columns makes the tile's t by itself.  Each wave has 128
 // columns at a time and loads their B alone, the first of it ahead of the first
 // product.  Bound by latencies and by A, which every block of a tile reads whole
-// (1 row of rank 16, 4096 -> 4096: 6.6 us, an empty launch 2.7; 64 rows of 32
-// adapters of rank 16, 4096 -> 14336 bf16, 20 MB: 10.2 us; two launches 14.6, without
+// (1 row of rank 16, 4096 -> 4096: 7.1 us, an empty launch 2.7; 64 rows of 32
+// adapters of rank 16, 4096 -> 14336 bf16, 20 MB: 10.7 us; two launches 14.6, without
 // the next step's B and base ahead of the products 0.7 more).  Measured and left: a
 // fourth stage, x's rows past the tile not loaded (neither is faster).
 template <int ACT, int NT, int WAVES, int STAGES>

@@ -796,7 +796,12 @@ LoraSchedule lora_schedule(int64_t T, int64_t L, int64_t rank, int64_t N, int64_
 
   // Two launches.  Tiles of 16 rows whose K the waves share, or, where adapters
   // have rows for them, of 64 or 128 in the first product (8192 rows, rank 64:
-  // 27 us in tiles of 128, 33 of 64) and of 32 in the second.
+  // 27 us in tiles of 128, 33 of 64) and of 32 in the second.  us, tiles of 16 and
+  // 16 / of 64 and 32, 4096 -> 4096 bf16, rank 64: 24 rows an adapter of 16 adapters
+  // 15.5 / 15.1, 32 rows 15.1 / 15.0, 64 rows 20.0 / 17.1, 128 rows 32 / 23; 1024 ->
+  // 14336, 32 rows 22.3 / 18.3.  Few adapters in all gain by the waves' sharing of K
+  // instead (32 rows of one 10.0 / 11.8, 64 of one 10.0 / 12.1, 64 of each of 4 11.2 /
+  // 12.7), which this rule gives away.
   s.plan.many = each >= 32;
   s.plan.shrink_rows = each >= 256 ? 128 : each >= 32 ? 64 : 16;
   // as many K ranges as there are CUs for: the second product adds their sums up

@@ -323,7 +323,9 @@ __device__ __forceinline__ void wave_sync() {
 }  // namespace
 
 // Everything in 64 bits: softmax scores that a bias or sums of two choose by, and
-// more experts a token than the keys' lanes hold.
+// more experts a token than the keys' lanes hold.  Bound by 64-bit exponentials, one
+// for each expert, and by choices of 64-bit values (8 of 256, softmax with a bias: 1
+// row 6.9 us, 1024 7.7, 8192 17.1; bf16, 8 of 4 of 8 groups by two: 7.8, 8.5, 18.1).
 template <int LANES, int V, int ACT>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_exact_kernel(RouteParams p) {
   constexpr int ROWS = kRouteThreads / LANES;
@@ -397,7 +399,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_exact_kernel(RoutePar
 // sigmoid, bias, 8 experts of 4 of 8 groups: 9.1 us, its 9 MB are 1.8; bf16 logits
 // alone 5.2), by a launch and one row's chain of choices where there are few (1 x
 // 256, 8 of 256 bf16 3.3 us, with groups 5.4, an empty launch 2.7).  The same with
-// 64-bit values throughout took 20 us.
+// 64-bit values throughout took 20 us.  fp32 logits alone, with three candidates
+// more than bf16's exact keys: 1 x 256 4.6 us, 8192 x 256 7.2.
 template <bool VALUED, int LANES, int V, int ACT>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(RouteParams p) {
   constexpr int ROWS = kRouteThreads / LANES;
@@ -589,7 +592,10 @@ hipError_t launch_route_as(const RouteParams& p, int act, hipStream_t stream) {
 // 16 lanes a row where its values and its candidates fit them and there are rows
 // enough, else 64 (us, 64 / 16 lanes, 256 experts: sigmoid, bias and groups by
 // two, 1 row 5.4 / 6.5, 2048 rows 7.6 / 8.0, 4096 9.6 / 7.6; bf16 logits alone, 1
-// row 3.3 / 4.0, 1024 3.8 / 4.4, 4096 5.4 / 4.5).
+// row 3.3 / 4.0, 1024 3.8 / 4.4, 4096 5.4 / 4.5).  Rows of at most four values a
+// lane have 16 lanes at any number of them: 64 experts, 8 chosen, bf16 logits alone,
+// 1 row 3.9 / 4.1, 64 4.3 / 4.1, 2048 4.9 / 4.2, 8192 9.1 / 4.5; with sigmoid, bias and 4
+// groups 5.7 / 5.7, 6.3 / 5.6, 7.1 / 6.3, 14.8 / 7.2.
 template <int KIND>
 hipError_t launch_route_of(const RouteParams& p, int candidates, int act, hipStream_t stream) {
   const int per_group = p.E / p.groups;

@@ -36,7 +36,10 @@ __device__ __forceinline__ uint32_t expert_of(int64_t id, uint32_t E) {
 // (One run a wave where S allows it; otherwise the masks are made again.)
 // Bound by a launch up to some 4096 slots (64 tokens of 8 in 64 experts: 3.1
 // us, an empty launch 2.7), by every block's reading of all ids from there: taken
-// up to 8192, and beyond for more experts than the chunks below count.
+// up to 8192, and beyond for more experts than the chunks below count.  One wave
+// up to 1024 slots, four to 8192 (us, 1 / 4 / 16 waves, 64 experts: 1024 slots 3.5
+// / 4.3 / 5.5, 2048 4.2 / 4.3 / 5.5, 4096 5.4 / 4.0 / 5.6, 8192 12.5 / 4.7 / 5.7,
+// 16384 23 / 6.1 / 5.3).
 template <class ID, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupRowsParams p) {
   __shared__ int s_below[WAVES], s_own[WAVES];
@@ -350,6 +353,12 @@ hipError_t launch_group_rows(const GroupRowsParams& p, int id_bytes, hipStream_t
 // 11.4 us where these take 8.2).  Bound by memory: each row once in, each sum once
 // out (8192 tokens x 8 rows of 2048 bf16, 302 MB: 45 us with rows just written, 57
 // without, 5.3 TB/s; 1500 x 4 x 2003 fp16, no row on 16 bytes: 8.2 us).
+// The fewest lanes that hold a row, 64 from there on and 256 for rows of several
+// blocks (us, 8 / 16 / 32 / 64 / 256 lanes, 8192 tokens of 8, bf16: N = 64 4.7 /
+// 4.8 / 5.9 / 7.5 / 9.9, 128 6.0 / 5.9 / 6.7 / 7.7 / 10.4, 256 9.8 / 9.7 / 9.6 /
+// 9.7 / 10.9, 512 17.0 / 16.7 / 16.5 / 13.8 / 14.5, 1024 31 / 30 / 29 / 24.4 / 24.9,
+// 2048 76 / 67 / 65 / 55.4 / 56.2; one token 0.2 to 0.5 more with 8 to 32 lanes:
+// N = 64 3.8 / 3.9 / 3.7 / 3.4 / 3.5, 4096 4.1 / 4.1 / 4.1 / 3.5 / 3.7).
 constexpr int kCombineThreads = 256;
 
 template <int ACT, int LX>

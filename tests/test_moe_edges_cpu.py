@@ -440,3 +440,12 @@ def test_shape_functions_refuse_sizes_that_the_calls_refuse(call):
     """(Not numbers of rows, which a compiled program may not know.)"""
     with pytest.raises(ValueError):
         call(lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=META))
+
+
+def test_group_rows_needs_no_workspace_up_to_its_bound(lowbit_lib):
+    """What the binding leaves unasked: up to that many slots the library asks for none."""
+    need = lowbit_lib.lowbit_group_rows_workspace_bytes
+    for E in (1, 64, 900, 65536):
+        for k in (1, 3, 8):
+            assert need(lb.GROUP_ROWS_ALONE // k, k, E) == 0
+    assert need(lb.GROUP_ROWS_ALONE + 1, 1, 64) > 0
