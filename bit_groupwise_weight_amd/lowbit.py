@@ -5,7 +5,8 @@ only turns torch tensors into device pointers and sizes, allocates outputs with
 torch when the caller does not pass them, and raises LowbitError on a non-OK
 status.  There is no fallback: if the library is missing or fails to load,
 every call raises.  Only pointers are handed over, so results carry no gradient,
-also where an input requires one (the torch ops raise in the backward pass).
+also where an input requires one (the torch ops raise in the backward pass), and no
+forward-mode tangent.
 """
 from __future__ import annotations
 
