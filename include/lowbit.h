@@ -464,8 +464,8 @@ typedef enum lowbit_route_score {
  * or a single group (whose value nothing is compared with) experts are ordered
  * by their logits; otherwise c is computed in 64 bits, so that rounding does
  * not decide.  Weights are computed in 64 bits and rounded once.  (Without
- * `renormalize` softmax divides them by its sum over all experts, whose terms
- * are good to 2^-32 of themselves or better.)
+ * `renormalize` softmax divides them by its sum over all experts, each term
+ * of which is good to 2^-32 of itself, or to 2^-1000 of the largest.)
  *
  *   logits   device, T x E row-major, dtype, aligned to its element size.
  *   bias     device, E fp32, or NULL.

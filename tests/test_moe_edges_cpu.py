@@ -449,3 +449,11 @@ def test_group_rows_needs_no_workspace_up_to_its_bound(lowbit_lib):
         for k in (1, 3, 8):
             assert need(lb.GROUP_ROWS_ALONE // k, k, E) == 0
     assert need(lb.GROUP_ROWS_ALONE + 1, 1, 64) > 0
+
+
+def test_experts_in_inference_mode(calls):
+    m, (x, e, w, _) = experts_of(), batch()
+    want = m(x, e, w)
+    with torch.inference_mode():
+        del calls[:]
+        assert torch.equal(m(x, e, w), want) and torch.equal(m(x, e, w.clone()), want) and "combine" in calls
