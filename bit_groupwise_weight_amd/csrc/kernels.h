@@ -279,6 +279,7 @@ hipError_t launch_moe_route(const RouteParams&, int act, hipStream_t);
 
 constexpr int kGroupChunkExperts = 900;   // 18 arrays of E + 2 in 64 KiB of LDS
 constexpr int64_t kGroupAlone = 65536;    // slots that one launch without workspace sorts
+constexpr int64_t kGroupOneByOne = int64_t(1) << 25;   // with more experts: slots x experts of a block an expert
 // Slots of a block of group_rows' two launches.
 constexpr int64_t group_chunk(int64_t S) { return S <= 128 * 1024 ? 1024 : 4096; }
 struct GroupRowsParams {
@@ -290,8 +291,37 @@ struct GroupRowsParams {
   int E;
   uint32_t topk_mul;      // s / topk == (s * topk_mul) >> topk_shift for 0 <= s < 2^30
   int topk_shift;
-  int* counts;            // workspace: ceil(S / group_chunk(S)) x (E + 1), or nullptr (one launch)
+  // workspace, as GroupWorkspace has it, or nullptr
+  int* counts;            // of each chunk; nullptr: one launch
+  int* totals;            // of all chunks; nullptr: added up from the counts
+  int32_t* order;         // S: slots by their id's low digit, and nullptr: one sort by whole ids
+  int32_t* keys;          // S: the sorted ids
 };
+// What a call with a workspace uses, in bytes from its begin: one sort by whole ids or
+// two by digits, and sums over the chunks taken ahead where there are many.
+constexpr int kGroupDigits = 512;
+struct GroupWorkspace {
+  bool used, scanned, digits;
+  size_t totals, order, keys, bytes;
+};
+constexpr GroupWorkspace group_workspace(int64_t S, int64_t E) {
+  GroupWorkspace w{};
+  w.digits = E > kGroupChunkExperts;
+  w.used = w.digits ? S * E > kGroupOneByOne : S > kGroupAlone;
+  if (!w.used) return w;
+  const int64_t chunks = (S + group_chunk(S) - 1) / group_chunk(S), values = w.digits ? kGroupDigits : E + 1;
+  w.scanned = w.digits || chunks > 512 || chunks * values > 32768;
+  const auto whole = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
+  w.totals = static_cast<size_t>(chunks) * values * sizeof(int);
+  w.bytes = w.totals;
+  if (w.scanned) {
+    w.totals = whole(w.totals);
+    w.order = w.totals + whole(values * sizeof(int));
+    w.keys = w.order + (w.digits ? whole(S * sizeof(int32_t)) : 0);
+    w.bytes = w.keys + (w.digits ? S * sizeof(int32_t) : 0);
+  }
+  return w;
+}
 hipError_t launch_group_rows(const GroupRowsParams&, int id_bytes, hipStream_t);
 
 struct CombineParams {

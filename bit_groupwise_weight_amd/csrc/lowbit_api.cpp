@@ -1219,9 +1219,7 @@ lowbit_status lowbit_moe_route(const void* logits, lowbit_dtype dtype, const flo
 
 size_t lowbit_group_rows_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
   if (T <= 0 || T > kMaxDim || topk < 1 || topk > kMaxDim || T * topk > kMaxDim || E < 1 || E > kF8MaxExperts) return 0;
-  const int64_t S = T * topk;
-  if (S <= lowbit::kGroupAlone || E > lowbit::kGroupChunkExperts) return 0;
-  return static_cast<size_t>((S + lowbit::group_chunk(S) - 1) / lowbit::group_chunk(S)) * (E + 1) * sizeof(int);
+  return lowbit::group_workspace(T * topk, E).bytes;
 }
 
 lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_t topk, int64_t E,
@@ -1246,9 +1244,18 @@ lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_
   int shift = 30;
   while ((int64_t{1} << (shift - 30)) < topk) ++shift;
   const uint32_t mul = static_cast<uint32_t>((uint64_t{1} << shift) / static_cast<uint64_t>(topk) + 1);
-  const size_t need = lowbit_group_rows_workspace_bytes(T, topk, E);
-  const lowbit::GroupRowsParams p{ids, rows, offsets, position, T * topk, static_cast<int>(E), mul, shift,
-                                  need > 0 && workspace_bytes >= need ? static_cast<int*>(workspace) : nullptr};
+  lowbit::GroupRowsParams p{ids, rows, offsets, position, T * topk, static_cast<int>(E), mul, shift,
+                            nullptr, nullptr, nullptr, nullptr};
+  const lowbit::GroupWorkspace w = lowbit::group_workspace(T * topk, E);
+  if (w.used && workspace_bytes >= w.bytes) {
+    char* at = static_cast<char*>(workspace);
+    p.counts = reinterpret_cast<int*>(at);
+    if (w.scanned) p.totals = reinterpret_cast<int*>(at + w.totals);
+    if (w.digits) {
+      p.order = reinterpret_cast<int32_t*>(at + w.order);
+      p.keys = reinterpret_cast<int32_t*>(at + w.keys);
+    }
+  }
   const hipError_t e = lowbit::launch_group_rows(p, id_bytes, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "group_rows launch");
   return LOWBIT_OK;

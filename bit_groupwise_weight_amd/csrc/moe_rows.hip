@@ -139,13 +139,37 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupRowsParams 
 // eager call takes 13 with two launches and a workspace); 131072 - / 18.5 /
 // 11.0; 524288 141 / - / 17 (two empty launches are 4.9).  Chunks of 1024 slots
 // up to 128 of them, of 4096 beyond (524288 slots 29 against 17): what a block
-// adds up of the others' counts grows with their number.
+// adds up of the others' counts grows with their number.  Where that is more than
+// 32768 of them, or past 512 chunks, a launch between the two turns the counts into
+// those of the chunks before (us, without / with it: 64 experts, 2^20 slots 17 / 19,
+// 2^21 32 / 31, 2^22 71 / 54; 256, 2^18 15.3 / 16.4, 2^19 18.0 / 17.4, 2^22 141 / 61;
+// 900, 2^17 22.8 / 13.8, 2^20 42 / 26, 2^22 381 / 76).
+//
+// More experts than the LDS has counts for take two such sorts, by the low 9 bits of
+// the id and then by the others, and their offsets from the sorted ids: seven
+// launches, past 2^25 slots x experts (us, a block an expert / so: 1024 experts, 32768
+// slots 22 / 26, 65536 35 / 28, 131072 92 / 30; 4096, 8192 slots 14 / 24, 16384 50 /
+// 25, 131072 302 / 30; 65536, 1024 slots 26 / 21, 16384 701 / 26).
 constexpr int kChunkWaves = 16;
 
-template <class ID>
+enum : int { WHOLE, LOW, HIGH };             // the part of the id that a sort goes by
+constexpr int kLowBits = 9;
+static_assert(1 << kLowBits == kGroupDigits, "the low digit's values");
+template <int PART> __device__ __forceinline__ uint32_t part_of(uint32_t x) {
+  return PART == WHOLE ? x : PART == LOW ? x & (kGroupDigits - 1) : x >> kLowBits;
+}
+template <int PART> __host__ __device__ __forceinline__ int parts(int E) {      // how many values it has
+  return PART == WHOLE ? E + 1 : PART == LOW ? kGroupDigits : (E >> kLowBits) + 1;
+}
+// The slot at place s of the sort before.
+template <int PART> __device__ __forceinline__ int64_t slot_at(const GroupRowsParams& p, int64_t s) {
+  return PART == HIGH ? p.order[s] : s;
+}
+// The part of the id at place s; past the last one, one more than there are.
+template <class ID, int PART>
 __device__ __forceinline__ uint32_t chunk_id(const GroupRowsParams& p, int64_t s) {
-  const uint32_t E = static_cast<uint32_t>(p.E);
-  return s < p.S ? expert_of(static_cast<const ID*>(p.ids)[s], E) : E + 1;
+  if (s >= p.S) return parts<PART>(p.E);
+  return part_of<PART>(expert_of(static_cast<const ID*>(p.ids)[slot_at<PART>(p, s)], static_cast<uint32_t>(p.E)));
 }
 
 // counts[x] += 1 for each lane's x.  (A wave of one id, as where all tokens go one
@@ -159,22 +183,56 @@ __device__ __forceinline__ void count_one(int* counts, uint32_t x) {
   }
 }
 
-template <class ID, int STEPS>
+template <class ID, int STEPS, int PART>
 __global__ __launch_bounds__(64 * kChunkWaves) void group_count_kernel(GroupRowsParams p) {
-  extern __shared__ int s_count[];           // E + 2: the experts, none, past the last slot
-  for (int e = threadIdx.x; e < p.E + 2; e += blockDim.x) s_count[e] = 0;
+  extern __shared__ int s_count[];           // the parts, past the last slot
+  const int values = parts<PART>(p.E);
+  for (int e = threadIdx.x; e <= values; e += blockDim.x) s_count[e] = 0;
   __syncthreads();
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * (1024 * STEPS);
   uint32_t x[STEPS];
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID>(p, begin + i * 64 * kChunkWaves + threadIdx.x);
+  for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID, PART>(p, begin + i * 64 * kChunkWaves + threadIdx.x);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     count_one(s_count, x[i]);
   }
   __syncthreads();
-  int* to = p.counts + static_cast<size_t>(blockIdx.x) * (p.E + 1);
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) to[e] = s_count[e];
+  int* to = p.counts + static_cast<size_t>(blockIdx.x) * values;
+  for (int e = threadIdx.x; e < values; e += blockDim.x) to[e] = s_count[e];
+}
+
+// Each chunk's counts become those of the chunks before it, and their sums over all
+// chunks go to p.totals: 64 values a block, whose waves share the chunks.
+__global__ __launch_bounds__(64 * kChunkWaves) void group_scan_kernel(GroupRowsParams p, int values, int chunks) {
+  __shared__ int s_sum[kChunkWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = static_cast<int>(blockIdx.x) * 64 + lane;
+  const int each = (chunks + kChunkWaves - 1) / kChunkWaves;
+  const int first = min(wave * each, chunks), last = min(first + each, chunks);
+  int* counts = p.counts + e;
+  int sum = 0;
+  if (e < values) {
+#pragma unroll 8
+    for (int c = first; c < last; ++c) sum += counts[static_cast<size_t>(c) * values];
+  }
+  s_sum[wave][lane] = sum;
+  __syncthreads();
+  if (e >= values) return;
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += s_sum[w][lane];
+  if (wave == kChunkWaves - 1) p.totals[e] = before + sum;
+  for (int c0 = first; c0 < last; c0 += 8) {
+    int v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c0 + i < last ? counts[static_cast<size_t>(c0 + i) * values] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c0 + i < last) counts[static_cast<size_t>(c0 + i) * values] = before;
+      before += v[i];
+    }
+  }
 }
 
 // Four ids from slot s on, as experts (E + 1 past the last slot).
@@ -193,11 +251,13 @@ __device__ __forceinline__ void load_four(const GroupRowsParams& p, int s, uint3
   }
 }
 
-// ALONE: in one launch, each block counting all slots itself.
-template <class ID, int STEPS, bool ALONE>
+// ALONE: in one launch, each block counting all slots itself; SUM: from all chunks'
+// counts; SCANNED: from the counts before its own.
+enum : int { ALONE, SUM, SCANNED };
+template <class ID, int STEPS, int FROM, int PART>
 __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRowsParams p, int chunks, int bits) {
   extern __shared__ int s_mem[];
-  const int ids = p.E + 2;
+  const int values = parts<PART>(p.E), ids = values + 1;
   int* s_all = s_mem;                        // [ids] an id's slots in all chunks
   int* s_base = s_mem + ids;                 // [ids] in the chunks before this one, then its first place here
   int* s_wave = s_mem + 2 * ids;             // [kChunkWaves][ids] its slots by wave, then those of the waves before
@@ -208,10 +268,10 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * (1024 * STEPS) + wave * (64 * STEPS);
   uint32_t x[STEPS];
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID>(p, begin + i * 64 + lane);
+  for (int i = 0; i < STEPS; ++i) x[i] = chunk_id<ID, PART>(p, begin + i * 64 + lane);
   for (int i = threadIdx.x; i < (2 + kChunkWaves) * ids; i += blockDim.x) s_mem[i] = 0;
   __syncthreads();
-  if constexpr (ALONE) {
+  if constexpr (FROM == ALONE) {
     const int here = static_cast<int>(blockIdx.x) * (1024 * STEPS), S = static_cast<int>(p.S);
 #pragma unroll 1
     for (int s0 = 0; s0 < S; s0 += 4 * 4096) {
@@ -228,13 +288,18 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
     }
     __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) s_all[e] += s_base[e];
+  } else if constexpr (FROM == SCANNED) {
+    for (int e = threadIdx.x; e < values; e += blockDim.x) {
+      s_all[e] = p.totals[e];
+      s_base[e] = p.counts[static_cast<size_t>(blockIdx.x) * values + e];
+    }
   } else {
-    for (int e = lane; e <= p.E; e += 64) {  // the waves take the chunks in turn
+    for (int e = lane; e < values; e += 64) {  // the waves take the chunks in turn
       int before = 0, all = 0;
       const int* from = p.counts + e;
 #pragma unroll 4
       for (int c = wave; c < chunks; c += kChunkWaves) {
-        const int v = from[static_cast<size_t>(c) * (p.E + 1)];
+        const int v = from[static_cast<size_t>(c) * values];
         all += v;
         before += c < static_cast<int>(blockIdx.x) ? v : 0;
       }
@@ -244,9 +309,9 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
   }
   __syncthreads();
   int carry = 0;
-  for (int e0 = 0; e0 <= p.E; e0 += 64 * kChunkWaves) {
+  for (int e0 = 0; e0 < values; e0 += 64 * kChunkWaves) {
     const int e = e0 + static_cast<int>(threadIdx.x);
-    const int all = e <= p.E ? s_all[e] : 0;
+    const int all = e < values ? s_all[e] : 0;
     int upto = all;                          // inclusive prefix sum over the lanes
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -262,10 +327,10 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
       less += w < wave ? s_part[w] : 0;
       carry += s_part[w];
     }
-    if (e <= p.E) {
+    if (e < values) {
       const int first = less + upto - all;
       s_base[e] += first;
-      if (blockIdx.x == 0) p.offsets[e] = first;
+      if (PART == WHOLE && blockIdx.x == 0) p.offsets[e] = first;
     }
   }
 
@@ -288,7 +353,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+  for (int e = threadIdx.x; e < values; e += blockDim.x) {
     int sum = 0;
 #pragma unroll
     for (int w = 0; w < kChunkWaves; ++w) {
@@ -300,39 +365,79 @@ __global__ __launch_bounds__(64 * kChunkWaves) void group_place_kernel(GroupRows
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    if (x[i] > E) continue;
     const int64_t s = begin + i * 64 + lane;
+    if (s >= p.S) continue;
     const int to = s_base[x[i]] + mine[x[i]] + rank[i];
-    p.rows[to] = static_cast<int>((static_cast<uint64_t>(s) * p.topk_mul) >> p.topk_shift);
-    if (p.position) p.position[s] = x[i] < E ? to : -1;
+    if constexpr (PART == LOW) {
+      p.order[to] = static_cast<int32_t>(s);
+    } else {
+      const int64_t slot = slot_at<PART>(p, s);
+      const uint32_t id = PART == WHOLE ? x[i] : expert_of(static_cast<const ID*>(p.ids)[slot], E);
+      p.rows[to] = static_cast<int>((static_cast<uint64_t>(slot) * p.topk_mul) >> p.topk_shift);
+      if (p.position) p.position[slot] = id < E ? to : -1;
+      if constexpr (PART == HIGH) p.keys[to] = static_cast<int32_t>(id);
+    }
   }
+}
+
+// Where each expert's begin among the sorted ids: the first that is not below it.
+__global__ __launch_bounds__(256) void group_bounds_kernel(GroupRowsParams p) {
+  const int e = static_cast<int>(blockIdx.x * 256 + threadIdx.x);
+  if (e > p.E) return;
+  int lo = 0, hi = static_cast<int>(p.S);
+  while (lo < hi) {
+    const int at = lo + (hi - lo) / 2;
+    if (p.keys[at] < e) lo = at + 1;
+    else hi = at;
+  }
+  p.offsets[e] = lo;
 }
 
 namespace {
 
-template <class ID, int STEPS>
-void launch_chunks_as(const GroupRowsParams& p, int bits, hipStream_t stream) {
+constexpr int bits_of(int values) {          // of the numbers 0 .. values
+  int bits = 1;
+  while ((1 << bits) < values + 1) ++bits;
+  return bits;
+}
+template <class ID, int STEPS, int PART>
+void launch_sort(const GroupRowsParams& p, bool scanned, hipStream_t stream) {
   const int chunks = static_cast<int>((p.S + 1024 * STEPS - 1) / (1024 * STEPS)), threads = 64 * kChunkWaves;
-  const size_t row = (p.E + 2) * sizeof(int);
-  group_count_kernel<ID, STEPS><<<chunks, threads, row, stream>>>(p);
-  group_place_kernel<ID, STEPS, false><<<chunks, threads, (kChunkWaves + 2) * row, stream>>>(p, chunks, bits);
+  const int values = parts<PART>(p.E), bits = bits_of(values);
+  const size_t row = (values + 1) * sizeof(int);
+  group_count_kernel<ID, STEPS, PART><<<chunks, threads, row, stream>>>(p);
+  if (scanned) {
+    group_scan_kernel<<<(values + 63) / 64, threads, 0, stream>>>(p, values, chunks);
+    group_place_kernel<ID, STEPS, SCANNED, PART><<<chunks, threads, (kChunkWaves + 2) * row, stream>>>(p, chunks, bits);
+  } else {
+    group_place_kernel<ID, STEPS, SUM, PART><<<chunks, threads, (kChunkWaves + 2) * row, stream>>>(p, chunks, bits);
+  }
+}
+template <class ID, int STEPS>
+void launch_chunks_as(const GroupRowsParams& p, hipStream_t stream) {
+  const bool scanned = p.totals != nullptr;
+  if (p.order == nullptr) {
+    launch_sort<ID, STEPS, WHOLE>(p, scanned, stream);
+  } else {
+    launch_sort<ID, STEPS, LOW>(p, scanned, stream);
+    launch_sort<ID, STEPS, HIGH>(p, scanned, stream);
+    group_bounds_kernel<<<p.E / 256 + 1, 256, 0, stream>>>(p);
+  }
 }
 template <class ID>
 void launch_group_as(const GroupRowsParams& p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.E + 1));
-  int bits = 1;
-  while ((1 << bits) < p.E + 2) ++bits;
-  if (p.S <= 1024) {
+  if (p.counts) {
+    if (group_chunk(p.S) == 1024) launch_chunks_as<ID, 1>(p, stream);
+    else launch_chunks_as<ID, 4>(p, stream);
+  } else if (p.S <= 1024) {
     group_rows_kernel<ID, 1><<<grid, 64, 0, stream>>>(p);
   } else if (p.S <= 8192) {
     group_rows_kernel<ID, 4><<<grid, 256, 0, stream>>>(p);
   } else if (p.S <= kGroupAlone && p.E <= kGroupChunkExperts) {
     const int chunks = static_cast<int>((p.S + 1023) / 1024);
     const size_t lds = (kChunkWaves + 2) * (p.E + 2) * sizeof(int);
-    group_place_kernel<ID, 1, true><<<chunks, 64 * kChunkWaves, lds, stream>>>(p, chunks, bits);
-  } else if (p.counts) {
-    if (group_chunk(p.S) == 1024) launch_chunks_as<ID, 1>(p, bits, stream);
-    else launch_chunks_as<ID, 4>(p, bits, stream);
+    group_place_kernel<ID, 1, ALONE, WHOLE><<<chunks, 64 * kChunkWaves, lds, stream>>>(p, chunks, bits_of(p.E + 1));
   } else {
     group_rows_kernel<ID, 16><<<grid, 1024, 0, stream>>>(p);
   }

@@ -32,7 +32,7 @@ ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1  # lowbit_route_score
 ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, ROUTE_MAX_GROUPS = 1024, 64, 64   # LOWBIT_ROUTE_MAX_*
 LORA_MAX_RANK, LORA_MAX_ADAPTERS, LORA_MAX_SIZE = 256, 1 << 16, 1 << 23      # (N and K)
 COMBINE_MAX_TOPK = 1 << 16
-GROUP_ROWS_ALONE = 65536             # slots that lowbit_group_rows orders without a workspace
+GROUP_ROWS_ALONE, GROUP_ROWS_EXPERTS = 65536, 900     # slots and experts that lowbit_group_rows needs no workspace for
 F8_BLOCK = 128                       # K elements (and weight rows) sharing an e4m3 scale
 _DTYPE_ENUM = {torch.float32: LOWBIT_F32, torch.float16: LOWBIT_F16, torch.bfloat16: LOWBIT_BF16}
 _ENUM_DTYPE = {v: k for k, v in _DTYPE_ENUM.items()}
@@ -897,7 +897,7 @@ def lowbit_group_rows(ids: torch.Tensor, E: int, rows: Optional[torch.Tensor] = 
     if workspace is not None and workspace.dtype is not torch.uint8:
         raise ValueError("workspace must be uint8")
     dev = _placed(ids, rows, offsets, position, workspace)
-    if workspace is None and T * k > GROUP_ROWS_ALONE:
+    if workspace is None and (T * k > GROUP_ROWS_ALONE or E > GROUP_ROWS_EXPERTS):
         need = _call_on(dev, "lowbit_group_rows_workspace_bytes", T, k, E)
         workspace = None if need == 0 else _made_on((need,), torch.uint8, ids, stream)
     st = _call_on(dev, "lowbit_group_rows", _ptr(ids), _ID_BYTES[ids.dtype], T, k, E, _ptr(rows), _ptr(offsets),

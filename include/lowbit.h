@@ -508,8 +508,9 @@ lowbit_status lowbit_group_rows(const void* ids, int id_bytes, int64_t T, int64_
                                 int32_t* rows, int32_t* offsets, int32_t* position, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that lowbit_group_rows can use (0: none).  With less, the
- * call reads the ids once for each expert. */
+/* Bytes of workspace that lowbit_group_rows can use (0: none; at most 12 a
+ * slot, or 256 KiB).  With less, the call reads the ids once for each expert (of
+ * more than 65536 slots, twice), which takes long where both are many. */
 size_t lowbit_group_rows_workspace_bytes(int64_t T, int64_t topk, int64_t E);
 
 /* Each token's weighted sum of its experts' rows:

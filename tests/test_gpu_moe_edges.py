@@ -108,20 +108,32 @@ def test_route_one_group_by_two_is_ordered_by_its_logits(sigmoid, topk, dtype):
 # -------------------------------------------------------------- group_rows --
 
 # Every schedule: a block an expert with one, four and sixteen waves (the last with one run of steps a
-# wave, and several), a block a chunk in one launch, and two launches with chunks of 1024 and 4096.
+# wave, and several), a block a chunk in one launch, two launches with chunks of 1024 and 4096, three,
+# and a sort by each of an id's digits.
 ORDERS = [(3, 5, 4), (700, 3, 60), (1025, 7, 5), (2049, 8, 256), (5001, 4, 900), (5001, 4, 1500), (8192, 8, 61),
           (8193, 1, 65536), (65535, 1, 901), (16385, 4, 3000), (12001, 8, 256), (70000, 2, 33), (70000, 2, 901),
-          (40000, 3, 900), (70001, 8, 257)]
+          (40000, 3, 900), (70001, 8, 257), (700000, 6, 61), (524289, 8, 3), (513, 1, 65536), (600, 1, 65535), (1024, 1, 65536),
+          (9000, 4, 1024), (40001, 1, 901), (11000, 7, 512 * 9), (16385, 8, 512 * 9 + 1), (60000, 3, 2047), (33000, 1, 5000)]
 
 
 @pytest.mark.parametrize("kind", [torch.int32, torch.int64])
 @pytest.mark.parametrize("T, k, E", ORDERS)
 def test_group_rows_of_every_schedule_is_the_stable_order(T, k, E, kind):
-    """Against a stable sort on the CPU: ids spread out, all alike, and of the first and last only."""
+    """Against a stable sort on the CPU: ids spread out, all alike, and of the first and last only; without
+    a workspace and with one, whose end is kept."""
     g = torch.Generator().manual_seed(T + E)
     for ids in (torch.randint(-1, E + 1, (T, k), generator=g), torch.full((T, k), E // 2),
                 torch.randint(0, 2, (T, k), generator=g) * (E - 1)):
-        rows, offsets, position = (v.cpu().long() for v in lb.lowbit_group_rows(ids.to(kind).to(DEV), E))
+        dev = ids.to(kind).to(DEV)
+        need = lb.load().lowbit_group_rows_workspace_bytes(T, k, E)
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
+        got = lb.lowbit_group_rows(dev, E, workspace=ws[:need] if need else None)
+        if need:
+            assert all(torch.equal(a, b) for a, b in zip(got, lb.lowbit_group_rows(dev, E)))
+            if T * k * E <= 1 << 30:
+                assert all(torch.equal(a, b) for a, b in zip(got, lb.lowbit_group_rows(dev, E, workspace=ws[:need - 1])))
+            assert (ws[need:] == 255).all()
+        rows, offsets, position = (v.cpu().long() for v in got)
         key = torch.where((ids >= 0) & (ids < E), ids, E).view(-1)
         order = torch.argsort(key, stable=True)
         place = torch.empty_like(order)
@@ -191,3 +203,28 @@ def test_route_softmax_weights_as_they_are(E, k, spread, dtype):
         assert torch.all((w.double() - want).abs() <= 1.01 * U * want + 2.0 ** -149)
     e, w = lb.lowbit_moe_route(torch.full((3, E), NEG, device=DEV, dtype=DT[dtype]), k, renormalize=False)
     assert (e == -1).all() and (w == 0).all()
+
+
+def test_group_rows_by_digits_in_a_graph_and_without_positions():
+    """Replays with new ids, eager calls between them, each with its own workspace; ids far outside."""
+    T, k, E = 9000, 4, 5000
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    ids = torch.randint(-3, E + 3, (T, k), generator=g, device=DEV)
+    ids[5] = torch.tensor([2 ** 40 + 1, -2 ** 63, 2 ** 63 - 1, 2 ** 31], device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lb.lowbit_group_rows(ids, E)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = lb.lowbit_group_rows(ids, E)
+    for i in range(4):
+        ids[:] = torch.where(torch.rand(T, k, generator=g, device=DEV) < 0.5, ids, torch.randint(-3, E + 3, (T, k), generator=g, device=DEV))
+        graph.replay()
+        want = lb.lowbit_group_rows(ids, E)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        key = torch.where((ids >= 0) & (ids < E), ids, E).view(-1)
+        assert torch.equal(got[0].long(), torch.argsort(key, stable=True) // k)

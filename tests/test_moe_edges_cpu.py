@@ -442,13 +442,24 @@ def test_shape_functions_refuse_sizes_that_the_calls_refuse(call):
         call(lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=META))
 
 
-def test_group_rows_needs_no_workspace_up_to_its_bound(lowbit_lib):
-    """What the binding leaves unasked: up to that many slots the library asks for none."""
+def test_group_rows_needs_no_workspace_up_to_its_bounds(lowbit_lib):
+    """What the binding leaves unasked: up to that many slots and experts the library asks for none."""
     need = lowbit_lib.lowbit_group_rows_workspace_bytes
-    for E in (1, 64, 900, 65536):
+    for E in (1, 64, lb.GROUP_ROWS_EXPERTS):
         for k in (1, 3, 8):
             assert need(lb.GROUP_ROWS_ALONE // k, k, E) == 0
-    assert need(lb.GROUP_ROWS_ALONE + 1, 1, 64) > 0
+        assert need(lb.GROUP_ROWS_ALONE + 1, 1, E) > 0
+    assert need(lb.GROUP_ROWS_ALONE, 1, 65536) > 0
+
+
+@pytest.mark.parametrize("E", [1, 64, 900, 901, 4096, 65536])
+def test_group_rows_workspace_grows_with_the_slots(lowbit_lib, E):
+    """At most a few bytes a slot, up to the largest call: counts of chunks, and two copies of the slots
+    where the experts are many."""
+    need = lowbit_lib.lowbit_group_rows_workspace_bytes
+    for p in range(0, 31):
+        assert need(1 << p, 1, E) <= (1 << p) * 12 + 4 * 128 * (E if E <= 900 else 512) + 8192
+    assert need(1 << 30, 1, E) > 0 and need((1 << 30) + 1, 1, E) == 0
 
 
 def test_experts_in_inference_mode(calls):
