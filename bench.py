@@ -51,11 +51,11 @@ ROTATE_BYTES = 1 << 30
 # sources of these kernels and of their dispatch whose sha256 prefix is
 # `src_hash`; for any others bench reports traffic as null.
 MEASURED_TRAFFIC = {
-    "src_hash": "17f4c055da7dad48",
+    "src_hash": "84c62f63c4dd2c36",
     "qmv_bits1to7_bytes": 67137536,
     "qmm_bytes": {"4096x14336": 72819712, "14336x4096": 95364096},
     # rocprofv3 MfmaUtil (%) of the main MFMA kernel per shape
-    "qmm_mfma_util": {"4096x14336": 19.59, "14336x4096": 20.08},
+    "qmm_mfma_util": {"4096x14336": 19.46, "14336x4096": 19.92},
     # HBM bytes per launch of the int8-activation linear per (K x N) shape
     "a8_bytes": {"4096x14336": 44677120, "14336x4096": 52544512},
 }
